@@ -436,6 +436,160 @@ typedef struct hg_row_stats {
 int hg_gather_stats(hg_handle *h, const void *const *shard_ptrs, void *const *out_ptrs, int M,
                     hg_row_stats *stats, hg_stream_t stream);
 
+/*
+ * Vocabulary operators: the two ends of a model on one vocab-parallel [V, K]
+ * matrix. The pages stop at the logits; these have no counterpart there. The
+ * matrix is tp shards of [shard_cols, K] (nn.Linear / nn.Embedding layout,
+ * rank r holding the rows of tokens r * shard_cols ...), as the weights of
+ * hg_gather_fused are; the token-side matrices ([N, K] hidden states,
+ * embeddings, their gradients) are single, replicated ones. All sums are fp32.
+ *
+ *   hg_vocab_embed       out[n] = scale * table[tokens[n]]
+ *   hg_vocab_embed_grad  grad_table[v] (+)= scale * sum of grad_out[n] over the
+ *                        n with tokens[n] = v
+ *   hg_vocab_loss        z[n][v] = logit_scale * sum_k hidden[n][k] * weight[v][k]
+ *                        lse[n] = log sum_v exp z[n][v]
+ *                        loss[n] = lse[n] - z[n][targets[n]]
+ *   hg_vocab_loss_grad   d[n][v] = grad_loss[n] * (exp(z[n][v] - lse[n]) -
+ *                        [v = targets[n]]);  grad_hidden = logit_scale * d weight;
+ *                        grad_weight (+)= logit_scale * d^T hidden
+ *
+ * v runs over the real vocabulary, [0, vocab). When vocab < tp * shard_cols the
+ * remaining rows of the last shards are padding: whatever they hold (infinities
+ * and NaN too) takes no part in the loss or its gradients, and their gradient
+ * rows are zero. The logits are never stored: the loss keeps a running
+ * maximum and sum, and the gradient recomputes them a piece of the vocabulary
+ * at a time, in the matrix's type.
+ *
+ * Conventions, beside those at the top of this file:
+ *  - Every call is asynchronous on `stream`, allocates nothing, does not wait
+ *    for the device and may be captured into a CUDA graph. The calls of one
+ *    handle share its workspace: issue them on one stream, or order them with
+ *    events.
+ *  - Results do not depend on timing: the same inputs give the same bits.
+ *  - Token and target arrays are device pointers to N signed integers of
+ *    id_bytes (4 or 8) bytes each, naturally aligned.
+ *  - ld_*: distance in elements between consecutive rows of a token-side
+ *    matrix, >= hidden.
+ *  - N = 0 is a call with no rows: gradients of the matrix are still written
+ *    (as zeros) unless they are accumulated into.
+ */
+typedef struct hg_vocab hg_vocab;
+
+/* Element types of the matrix and the token-side matrices. */
+enum { HG_BF16 = 0, HG_FP16 = 1, HG_FP32 = 2 };
+
+/* Operators a handle serves (hg_vocab_create's `ops`); embedding needs no
+ * workspace and is always served. */
+enum { HG_VOCAB_EMBED = 1, HG_VOCAB_EMBED_GRAD = 2, HG_VOCAB_LOSS = 4, HG_VOCAB_LOSS_GRAD = 8 };
+
+/*
+ * hg_vocab_create - allocate the workspace of the vocabulary operators
+ *
+ *   tp           shards, 1 <= tp <= HG_MAX_TP
+ *   shard_cols   W, matrix rows per shard, >= 1 (no evenness rule)
+ *   vocab        real vocabulary, 1 <= vocab <= tp * shard_cols; 0: tp * shard_cols
+ *   hidden       K, >= 1; a multiple of 8 for the loss and its gradient
+ *   max_rows     largest N of any later call, >= 1
+ *   dtype        HG_BF16, HG_FP16, or HG_FP32 (embedding and its gradient only)
+ *   ops          HG_VOCAB_* bits of the operators that will be called
+ *   piece_bytes  HG_VOCAB_LOSS_GRAD: bound on the logits' gradient kept at a
+ *                time (at least one piece of 256 columns per shard); 0: 512 MB
+ *   out          receives the handle
+ *
+ * Errors: HG_ERR_ARG (bad sizes or type, size overflow), HG_ERR_CUDA (no
+ * device, allocation failure). The handle belongs to the current device.
+ */
+int hg_vocab_create(int tp, int shard_cols, int vocab, int hidden, int max_rows, int dtype,
+                    int ops, size_t piece_bytes, hg_vocab **out);
+
+/* Free the handle; waits for the device first. NULL is a no-op. */
+int hg_vocab_destroy(hg_vocab *h);
+
+/* Bytes of device memory the handle holds (0 for NULL). */
+size_t hg_vocab_workspace_bytes(const hg_vocab *h);
+
+/* Wait for `stream`, then report the device status: HG_OK, HG_ERR_TIMEOUT (a
+ * kernel's bounded wait gave up; results of that call are undefined, and the
+ * status is cleared by this call) or HG_ERR_CUDA. */
+int hg_vocab_sync(hg_vocab *h, hg_stream_t stream);
+
+/*
+ * hg_vocab_embed - scaled embedding lookup
+ *
+ *   tokens      N ids; one outside [0, vocab) gives a row of zeros
+ *   table_ptrs  tp device pointers to [W, K], rows contiguous
+ *   scale       multiplied in fp32, rounded once; 1 copies the rows bit for bit
+ *   out         [N, K], row distance ld_out
+ *
+ * Pointers are aligned to their element; where the table, out and the row
+ * distances are 16-byte aligned the rows move as 16-byte vectors. Errors,
+ * before any device work: HG_ERR_ARG, HG_ERR_ROWS (N above max_rows),
+ * HG_ERR_CUDA.
+ */
+int hg_vocab_embed(hg_vocab *h, const void *tokens, int id_bytes, int N,
+                   const void *const *table_ptrs, float scale, void *out, size_t ld_out,
+                   hg_stream_t stream);
+
+/*
+ * hg_vocab_embed_grad - gradient of the lookup to the table
+ *
+ *   tokens          N ids as in the lookup; one outside [0, vocab) has no gradient
+ *   grad_out        [N, K], row distance ld_grad_out
+ *   grad_table_ptrs tp device pointers to [W, K], written
+ *   accumulate      0: every row is written, zeros where no token points; 1: the
+ *                   sum is added to what a row holds (rounded once), and rows
+ *                   without tokens are not touched
+ *
+ * The tokens are sorted and each row's gradients summed in fp32 in the order of
+ * their positions, in runs of fixed length. Errors as hg_vocab_embed.
+ */
+int hg_vocab_embed_grad(hg_vocab *h, const void *tokens, int id_bytes, int N,
+                        const void *grad_out, size_t ld_grad_out, void *const *grad_table_ptrs,
+                        float scale, int accumulate, hg_stream_t stream);
+
+/*
+ * hg_vocab_loss - LM head and softmax cross entropy without the logits
+ *
+ *   hidden       [N, K], 16-byte aligned, row distance ld_hidden (a multiple of 8)
+ *   weight_ptrs  tp device pointers to [W, K], 16-byte aligned
+ *   targets      N ids. A negative one masks its row: loss and lse are 0 and the
+ *                row's hidden state has no effect. One >= vocab gives a NaN loss.
+ *   loss, lse    N floats each
+ *
+ * Products are exact in fp32, accumulated in fp32 on the tensor cores. Errors,
+ * before any device work: HG_ERR_ARG (also: the handle was not created for it),
+ * HG_ERR_ROWS (N above max_rows), HG_ERR_CUDA.
+ */
+int hg_vocab_loss(hg_vocab *h, const void *hidden, size_t ld_hidden,
+                  const void *const *weight_ptrs, const void *targets, int id_bytes, int N,
+                  float logit_scale, float *loss, float *lse, hg_stream_t stream);
+
+/*
+ * hg_vocab_loss_grad - gradient of hg_vocab_loss
+ *
+ *   hidden, weight_ptrs, targets, logit_scale   as given to hg_vocab_loss
+ *   lse              N floats, hg_vocab_loss's
+ *   grad_loss        N floats, the upstream gradient of each row's loss
+ *   grad_hidden      NULL, or [N, K], row distance ld_grad_hidden (a multiple of 8),
+ *                    16-byte aligned; zeros in masked rows
+ *   grad_weight_ptrs NULL, or tp device pointers to [W, K], 16-byte aligned
+ *   accumulate       0: grad_weight is overwritten; 1: the gradient, rounded to the
+ *                    matrix's type, is added to what grad_weight holds, piece by
+ *                    piece of the vocabulary (each element once)
+ *
+ * At least one of the two gradients is wanted. A row whose target is negative or
+ * >= vocab has no gradient, and its hidden state no effect. d is rounded to the
+ * matrix's type before the two products (its error is that of one rounding
+ * per term); both products are summed in fp32 and rounded once. Errors as
+ * hg_vocab_loss.
+ */
+int hg_vocab_loss_grad(hg_vocab *h, const void *hidden, size_t ld_hidden,
+                       const void *const *weight_ptrs, const void *targets, int id_bytes,
+                       const float *lse, const float *grad_loss, int N, float logit_scale,
+                       void *grad_hidden, size_t ld_grad_hidden, void *const *grad_weight_ptrs,
+                       int accumulate, hg_stream_t stream);
+
 /* Human-readable text of a status code; never NULL. No counterpart on the
  * pages (HeadGather reports failures as Python exceptions). */
 const char *hg_strerror(int status);

@@ -1,0 +1,517 @@
+// Embedding lookup with scaling, and its gradient by sorted tokens.
+//
+// Lookup: out[n] = scale * table[tokens[n]], a copy of N rows of K elements
+// bound by memory: each row read and each output written once. One warp moves
+// kRowAccesses accesses per lane of one row, all loads in flight before the
+// first store.
+//
+// Gradient: grad_table[v] (+)= scale * sum of grad[n] over tokens[n] = v. The
+// positions are sorted by token (stable, so that a token's rows come in the
+// order of their positions), and the sorted sequence is cut into chunks of
+// kRunRows rows whatever the tokens are: text repeats a few tokens thousands
+// of times, and a chunk is the same work for one token as for 32. A warp sums
+// one chunk over the columns of its lanes in fp32 registers. A run of equal tokens that lies
+// within a chunk is finished there; one that crosses a chunk's end leaves its
+// partial sums in `runs` (slot 0: the run a chunk continues, slot 1: the run
+// it starts and does not finish), and join_kernel adds those in chunk order.
+// No atomics, so the order of every sum is fixed.
+
+#include <cooperative_groups.h>
+
+#include "hg_vocab.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace hg {
+namespace vocab {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRowAccesses = 4;  // accesses per lane of a unit of the lookup
+
+struct Table {
+  void* shard[HG_MAX_TP];
+};
+
+template <typename T>
+__device__ __forceinline__ T* table_row(const Table& t, long long id, int W, int K) {
+  const long long r = id / W;
+  return static_cast<T*>(t.shard[r]) + (size_t)(id - r * W) * K;
+}
+
+struct EmbedArgs {
+  Table table;
+  Ids tokens;
+  int N, K, W, vocab;
+  int units_per_row;
+  float scale;
+  void* out;
+  size_t ld;
+};
+
+template <typename T, int E>
+__global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__ EmbedArgs a) {
+  const int lane = threadIdx.x & 31;
+  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const long long n = unit / a.units_per_row;
+  if (n >= a.N) return;
+  const int first = (int)(unit - n * a.units_per_row) * (kRowAccesses * 32) + lane;
+  const int accesses = a.K / E;
+  using P = Pack<T, E>;
+  P x[kRowAccesses];
+  const long long id = load_id(a.tokens, (size_t)n);
+  const bool inside = id >= 0 && id < a.vocab;
+  const P* src = reinterpret_cast<const P*>(table_row<T>(a.table, inside ? id : 0, a.W, a.K));
+#pragma unroll
+  for (int j = 0; j < kRowAccesses; ++j) {
+    const int i = first + j * 32;
+    if (inside && i < accesses) {
+      x[j] = src[i];
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[j].v[e] = Elem<T>::down(0.f);
+    }
+  }
+  P* dst = reinterpret_cast<P*>(static_cast<T*>(a.out) + (size_t)n * a.ld);
+#pragma unroll
+  for (int j = 0; j < kRowAccesses; ++j) {
+    const int i = first + j * 32;
+    if (i >= accesses) continue;
+    if (a.scale != 1.f && inside) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[j].v[e] = Elem<T>::down(Elem<T>::up(x[j].v[e]) * a.scale);
+    }
+    dst[i] = x[j];
+  }
+}
+
+// ---- sort of the positions by token ------------------------------------------
+// Least-significant-digit radix sort by one cluster of kSortCtas CTAs. Each
+// warp of the cluster owns a contiguous part of the sequence; a pass counts the
+// digits of every part, turns the counts into the first place of each (digit,
+// part) pair, and moves the entries in order. The CTAs exchange their counts
+// through distributed shared memory and the entries through L2.
+
+constexpr int kSortCtas = 8;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxDigitBits = 10;
+
+struct SortArgs {
+  Ids tokens;
+  int N, vocab;
+  int digit_bits, passes;
+  uint32_t* key[2];
+  int* pos[2];
+};
+
+struct SortShared {
+  uint32_t hist[1 << kMaxDigitBits];  // this CTA's digit counts, read by the others
+  uint32_t base[1 << kMaxDigitBits];  // first place of this CTA's entries of a digit
+  uint32_t warp_sum[kSortWarps];
+};
+
+size_t sort_smem(int digit_bits) {
+  return sizeof(SortShared) + ((size_t)kSortWarps << digit_bits) * sizeof(uint32_t);
+}
+
+// Pass 0 reads the tokens (one outside the vocabulary gets the key `vocab`,
+// after every real one) and writes buffer 0; pass p moves buffer (p - 1) & 1
+// to buffer p & 1.
+__device__ void sort_pass(const SortArgs& a, int pass, SortShared* sh, uint32_t* place) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  const int cta = (int)cluster.block_rank();
+  const int D = 1 << a.digit_bits;
+  const int shift = pass * a.digit_bits;
+  const uint32_t* in_key = a.key[(pass + 1) & 1];
+  const int* in_pos = a.pos[(pass + 1) & 1];
+  uint32_t* out_key = a.key[pass & 1];
+  int* out_pos = a.pos[pass & 1];
+  const long long part = round_up(div_up(a.N, kSortCtas * kSortWarps), 32);
+  const long long lo = ((long long)cta * kSortWarps + warp) * part;
+  const long long hi = lo + part < a.N ? lo + part : a.N;
+  uint32_t* mine = place + warp * D;  // counts, then places, of this warp's entries
+
+  auto key_at = [&](long long i) -> uint32_t {
+    if (pass > 0) return __ldcg(in_key + i);
+    const long long id = load_id(a.tokens, (size_t)i);
+    return (uint32_t)(id >= 0 && id < a.vocab ? id : a.vocab);
+  };
+
+  for (int d = lane; d < D; d += 32) mine[d] = 0;
+  __syncwarp();
+  for (long long i0 = lo; i0 < hi; i0 += 32) {
+    const bool on = i0 + lane < hi;
+    const uint32_t digit = on ? (key_at(i0 + lane) >> shift) & (D - 1) : D;
+    const unsigned peers = __match_any_sync(0xffffffffu, digit);
+    if (on && lane == __ffs(peers) - 1) mine[digit] += __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    uint32_t sum = 0;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t c = place[w * D + threadIdx.x];
+      place[w * D + threadIdx.x] = sum;
+      sum += c;
+    }
+    sh->hist[threadIdx.x] = sum;
+  }
+  cluster.sync();
+  uint32_t all = 0, before = 0;
+  if (threadIdx.x < D) {
+    for (int c = 0; c < kSortCtas; ++c) {
+      const uint32_t x = cluster.map_shared_rank(sh->hist, c)[threadIdx.x];
+      if (c < cta) before += x;
+      all += x;
+    }
+  }
+  // Exclusive sum of `all` over the digits (threads D.. add nothing).
+  uint32_t incl = all;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) sh->warp_sum[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t w = sh->warp_sum[lane];
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += x;
+    }
+    sh->warp_sum[lane] = w;
+  }
+  __syncthreads();
+  if (threadIdx.x < D)
+    sh->base[threadIdx.x] = incl - all + before + (warp ? sh->warp_sum[warp - 1] : 0);
+  __syncthreads();
+  for (long long i0 = lo; i0 < hi; i0 += 32) {
+    const bool on = i0 + lane < hi;
+    const uint32_t key = on ? key_at(i0 + lane) : 0;
+    const uint32_t digit = on ? (key >> shift) & (D - 1) : D;
+    const unsigned peers = __match_any_sync(0xffffffffu, digit);
+    const int rank = __popc(peers & ((1u << lane) - 1));
+    if (on) {
+      const uint32_t to = sh->base[digit] + mine[digit] + rank;
+      out_key[to] = key;
+      out_pos[to] = pass > 0 ? __ldcg(in_pos + i0 + lane) : (int)(i0 + lane);
+    }
+    __syncwarp();
+    if (on && rank == 0) mine[digit] += __popc(peers);
+    __syncwarp();
+  }
+  cluster.sync();  // every entry moved, every count read
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ SortArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  SortShared* sh = reinterpret_cast<SortShared*>(smem);
+  uint32_t* place = reinterpret_cast<uint32_t*>(sh + 1);
+  for (int p = 0; p < a.passes; ++p) sort_pass(a, p, sh, place);
+}
+
+// ---- sums over the sorted sequence -------------------------------------------
+
+struct SumArgs {
+  Table table;
+  const uint32_t* key;
+  const int* pos;
+  int N, K, W, vocab;
+  int chunks;
+  int slices;  // units of columns of one chunk
+  const void* grad;
+  size_t ld;
+  float scale;
+  int accumulate;
+  float* runs;
+};
+
+// One lane's columns: U accesses of E elements, 32 accesses apart.
+template <typename T, int E, int U>
+struct Columns {
+  alignas(4 * E) float v[U * E];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < U * E; ++i) v[i] = 0.f;
+  }
+};
+
+template <typename T, int E, int U>
+__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int first, int accesses,
+                                          const Columns<T, E, U>& c) {
+  using P = Pack<T, E>;
+  P* dst = reinterpret_cast<P*>(table_row<T>(a.table, key, a.W, a.K));
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = first + u * 32;
+    if (i >= accesses) continue;
+    P x;
+    if (a.accumulate) {
+      x = dst[i];
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        x.v[e] = Elem<T>::down(fmaf(a.scale, c.v[u * E + e], Elem<T>::up(x.v[e])));
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x.v[e] = Elem<T>::down(a.scale * c.v[u * E + e]);
+    }
+    dst[i] = x;
+  }
+}
+
+template <typename T, int E, int U>
+__device__ __forceinline__ float* run_slot(const SumArgs& a, long long chunk, int slot) {
+  return a.runs + ((size_t)chunk * 2 + slot) * a.K;
+}
+
+template <typename T, int E, int U>
+__global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ SumArgs a) {
+  constexpr int kBatch = 8;  // rows whose loads are in flight at once
+  using P = Pack<T, E>;
+  const int lane = threadIdx.x & 31;
+  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const long long chunk = unit / a.slices;
+  if (chunk >= a.chunks) return;
+  const int accesses = a.K / E;
+  const int first = (int)(unit - chunk * a.slices) * (32 * U) + lane;
+  const long long at = chunk * kRunRows;
+  const int rows = (int)(a.N - at < kRunRows ? a.N - at : kRunRows);
+  // Lane l holds row l of the chunk; the keys on either side of it.
+  const uint32_t none = 0xffffffffu;
+  const uint32_t my_key = lane < rows ? a.key[at + lane] : none;
+  const int my_pos = lane < rows ? a.pos[at + lane] : 0;
+  const uint32_t prev = at > 0 ? a.key[at - 1] : none;
+  const uint32_t next = at + rows < a.N ? a.key[at + rows] : none;
+
+  Columns<T, E, U> sum;
+  sum.clear();
+  bool continued = prev == __shfl_sync(0xffffffffu, my_key, 0);
+  for (int i0 = 0; i0 < rows; i0 += kBatch) {
+    P x[kBatch][U];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const uint32_t key = __shfl_sync(0xffffffffu, my_key, (i0 + b) & 31);
+      const int pos = __shfl_sync(0xffffffffu, my_pos, (i0 + b) & 31);
+      const P* src = reinterpret_cast<const P*>(static_cast<const T*>(a.grad) + (size_t)pos * a.ld);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + b < rows && key < (uint32_t)a.vocab && first + u * 32 < accesses)
+          x[b][u] = src[first + u * 32];
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b;
+      const uint32_t key = __shfl_sync(0xffffffffu, my_key, i & 31);
+      const uint32_t after = __shfl_sync(0xffffffffu, my_key, (i + 1) & 31);
+      if (i >= rows || key >= (uint32_t)a.vocab) continue;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (first + u * 32 < accesses) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) sum.v[u * E + e] += Elem<T>::up(x[b][u].v[e]);
+        }
+      const uint32_t following = i + 1 < rows ? after : next;
+      if (following == key && i + 1 < rows) continue;
+      // The run ends here, or goes on in the next chunk.
+      const bool goes_on = following == key;
+      if (!continued && !goes_on) {
+        write_row<T, E, U>(a, key, first, accesses, sum);
+      } else {
+        float* slot = run_slot<T, E, U>(a, chunk, continued ? 0 : 1);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (first + u * 32 < accesses) {
+            reinterpret_cast<Pack<float, E>*>(slot)[first + u * 32] =
+                *reinterpret_cast<const Pack<float, E>*>(&sum.v[u * E]);
+          }
+      }
+      sum.clear();
+      continued = false;
+    }
+  }
+}
+
+// Joins the runs that cross a chunk's end: the warp of the chunk a run starts
+// in adds that chunk's slot 1 and slot 0 of the chunks after it, in order.
+template <typename T, int E, int U>
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ SumArgs a) {
+  constexpr int kBatch = 4;
+  const int lane = threadIdx.x & 31;
+  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const long long chunk = unit / a.slices;
+  if (chunk + 1 >= a.chunks) return;
+  const int accesses = a.K / E;
+  const int first = (int)(unit - chunk * a.slices) * (32 * U) + lane;
+  const long long at = chunk * kRunRows;
+  const uint32_t key = a.key[at + kRunRows - 1];
+  if (key >= (uint32_t)a.vocab || a.key[at + kRunRows] != key) return;    // does not go on
+  if (a.key[at] == key && at > 0 && a.key[at - 1] == key) return;  // starts earlier
+  // Last chunk of the run: the first whose own last row is not of the run, or
+  // whose last row ends it.
+  long long last = chunk + 1;
+  for (;; last += 32) {
+    const long long c = last + lane;
+    const bool ends = c + 1 >= a.chunks || a.key[(c + 1) * kRunRows] != key;
+    const unsigned m = __ballot_sync(0xffffffffu, ends);
+    if (m) {
+      last += __ffs(m) - 1;
+      break;
+    }
+  }
+  Columns<T, E, U> sum;
+  const Pack<float, E>* src =
+      reinterpret_cast<const Pack<float, E>*>(run_slot<T, E, U>(a, chunk, 1));
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (first + u * 32 < accesses)
+      *reinterpret_cast<Pack<float, E>*>(&sum.v[u * E]) = src[first + u * 32];
+  for (long long c0 = chunk + 1; c0 <= last; c0 += kBatch) {
+    Pack<float, E> x[kBatch][U];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c0 + b <= last && first + u * 32 < accesses)
+          x[b][u] = reinterpret_cast<const Pack<float, E>*>(
+              run_slot<T, E, U>(a, c0 + b, 0))[first + u * 32];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c0 + b <= last && first + u * 32 < accesses) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) sum.v[u * E + e] += x[b][u].v[e];
+        }
+  }
+  write_row<T, E, U>(a, key, first, accesses, sum);
+}
+
+bool vectors(int K, size_t ld, const void* p, const Table& t, int tp, size_t elem) {
+  auto fits = [](size_t v) { return v % 16 == 0; };
+  if (!fits((size_t)K * elem) || !fits(ld * elem) || !fits(reinterpret_cast<uintptr_t>(p)))
+    return false;
+  for (int r = 0; r < tp; ++r)
+    if (!fits(reinterpret_cast<uintptr_t>(t.shard[r]))) return false;
+  return true;
+}
+
+template <typename T, int E>
+cudaError_t embed_as(const EmbedArgs& args, cudaStream_t stream) {
+  EmbedArgs a = args;
+  a.units_per_row = (int)div_up(a.K / E, kRowAccesses * 32);
+  const long long blocks = div_up((long long)a.N * a.units_per_row, kWarps);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  embed_kernel<T, E><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int E, int U>
+cudaError_t sum_as(const SumArgs& args, cudaStream_t stream) {
+  SumArgs a = args;
+  a.slices = (int)div_up(a.K / E, 32 * U);
+  const long long blocks = div_up((long long)a.chunks * a.slices, kWarps);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  sum_kernel<T, E, U><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+  join_kernel<T, E, U><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t sort(const hg_vocab& h, const Ids& tokens, int N, int* sorted, cudaStream_t stream) {
+  SortArgs a;
+  a.tokens = tokens;
+  a.N = N;
+  a.vocab = h.vocab;
+  int bits = 1;
+  while ((1ll << bits) <= h.vocab) ++bits;  // keys 0 .. vocab
+  a.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
+  a.digit_bits = (bits + a.passes - 1) / a.passes;
+  for (int i = 0; i < 2; ++i) {
+    a.key[i] = h.key[i];
+    a.pos[i] = h.pos[i];
+  }
+  *sorted = (a.passes + 1) & 1;
+  const size_t smem = sort_smem(a.digit_bits);
+  cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sort_smem(kMaxDigitBits));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSortCtas);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kSortCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sort_kernel, a);
+}
+
+}  // namespace
+
+cudaError_t embed(const hg_vocab& h, const Ids& tokens, int N, const void* const* table,
+                  float scale, void* out, size_t ld_out, cudaStream_t stream) {
+  EmbedArgs a = {};
+  for (int r = 0; r < h.tp; ++r) a.table.shard[r] = const_cast<void*>(table[r]);
+  a.tokens = tokens;
+  a.N = N;
+  a.K = h.K;
+  a.W = h.W;
+  a.vocab = h.vocab;
+  a.scale = scale;
+  a.out = out;
+  a.ld = ld_out;
+  const bool vec = vectors(h.K, ld_out, out, a.table, h.tp, elem_bytes(h.dtype));
+  switch (h.dtype) {
+    case HG_BF16:
+      return vec ? embed_as<__nv_bfloat16, 8>(a, stream) : embed_as<__nv_bfloat16, 1>(a, stream);
+    case HG_FP16: return vec ? embed_as<__half, 8>(a, stream) : embed_as<__half, 1>(a, stream);
+    default: return vec ? embed_as<float, 4>(a, stream) : embed_as<float, 1>(a, stream);
+  }
+}
+
+cudaError_t embed_grad(const hg_vocab& h, const Ids& tokens, int N, const void* grad,
+                       size_t ld_grad, void* const* table, float scale, bool accumulate,
+                       cudaStream_t stream) {
+  SumArgs a = {};
+  const size_t e = elem_bytes(h.dtype);
+  for (int r = 0; r < h.tp; ++r) {
+    a.table.shard[r] = table[r];
+    if (!accumulate) {
+      const cudaError_t st = cudaMemsetAsync(table[r], 0, (size_t)h.W * h.K * e, stream);
+      if (st != cudaSuccess) return st;
+    }
+  }
+  if (N == 0) return cudaSuccess;
+  int sorted = 0;
+  const cudaError_t st = sort(h, tokens, N, &sorted, stream);
+  if (st != cudaSuccess) return st;
+  a.key = h.key[sorted];
+  a.pos = h.pos[sorted];
+  a.N = N;
+  a.K = h.K;
+  a.W = h.W;
+  a.vocab = h.vocab;
+  a.chunks = (int)div_up(N, kRunRows);
+  a.grad = grad;
+  a.ld = ld_grad;
+  a.scale = scale;
+  a.accumulate = accumulate;
+  a.runs = h.runs;
+  const bool vec = vectors(h.K, ld_grad, grad, a.table, h.tp, e);
+  switch (h.dtype) {
+    case HG_BF16:
+      return vec ? sum_as<__nv_bfloat16, 8, 1>(a, stream) : sum_as<__nv_bfloat16, 1, 4>(a, stream);
+    case HG_FP16: return vec ? sum_as<__half, 8, 1>(a, stream) : sum_as<__half, 1, 4>(a, stream);
+    default: return vec ? sum_as<float, 4, 1>(a, stream) : sum_as<float, 1, 4>(a, stream);
+  }
+}
+
+}  // namespace vocab
+}  // namespace hg

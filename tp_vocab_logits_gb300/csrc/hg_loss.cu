@@ -1,0 +1,1045 @@
+// LM head with softmax cross entropy, and its gradient, without the logits.
+//
+// With z[n][v] = s * x_n . w_v over the real vocabulary (s = logit_scale):
+//   loss_n = lse_n - z[n][t_n],  lse_n = log sum_v exp z[n][v]
+//   d[n][v] = g_n * s * (exp(z[n][v] - lse_n) - [v = t_n])
+//   grad_hidden = d W,  grad_weight = d^T X
+//
+// Four matrix products on the tensor cores, one kernel template (Kind):
+//   kLoss  z = X W^T, a tile of which is reduced to a maximum and a sum of
+//          exponentials per row where it leaves the tensor memory; merge_kernel
+//          joins the tiles' statistics. The logits are never written.
+//   kProb  z again, turned into d in the matrix's type, for a piece of the
+//          vocabulary (the columns [c0, c0 + wcols) of every shard)
+//   kDx    grad_hidden += d W over the piece, in fp32 (accum)
+//   kDw    grad_weight = d^T X for the rows of the piece
+// pack_kernel first copies the unmasked rows of hidden together, so that masked
+// rows cost nothing and what they hold (NaN too) reaches no product; all
+// later kernels read the number of packed rows from device memory.
+//
+// Everything in the exponent is kept in base 2: y = z * log2(e), ex2(y - lse2).
+
+#include <cfloat>
+
+#include "hg_tcgen05.cuh"
+#include "hg_vocab.cuh"
+
+namespace hg {
+namespace vocab {
+namespace {
+
+enum Kind { kLoss, kProb, kDx, kDw };
+
+constexpr int kTileM = 128;   // rows of a tile: TMEM lanes
+constexpr int kTileN = 256;   // columns of a tile: fp32 TMEM columns
+constexpr int kBlockK = 64;   // K per stage: one 128-byte swizzle atom of 16-bit elements
+constexpr int kMmaK = 16;     // K per tcgen05.mma of kind::f16
+constexpr int kStages = 4;
+constexpr uint32_t kABytes = kTileM * kBlockK * 2;
+constexpr uint32_t kBBytes = kTileN * kBlockK * 2;
+constexpr uint32_t kBox = 64 * 128;  // a [64 x 64] box of 16-bit elements
+constexpr uint32_t kTmemCols = 2 * kTileN;  // two accumulators
+constexpr int kThreads = 192;   // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
+constexpr uint32_t kStageOut = 32 * 128;  // a warp's staged [32 rows x 128 bytes]
+constexpr size_t kSmemBytes =
+    1024 + (size_t)kStages * (kABytes + kBBytes) + 4 * 2 * kStageOut + 256;
+static_assert(kSmemBytes <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
+
+constexpr int kGroupM = 8;      // row tiles that share the column tiles of a wave
+constexpr int kSmallRows = 128;  // up to here the loss reads hidden where it lies
+constexpr int kMaxSplits = 16;
+constexpr unsigned long long kTimeoutNs = 4000000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct GemmArgs {
+  CUtensorMap shard[HG_MAX_TP];  // the weights; kDw: grad_weight (stores)
+  CUtensorMap x;                 // hidden, packed or where it lies
+  CUtensorMap p;                 // loads from prob
+  CUtensorMap out;               // stores: prob (kProb), accum (kDx)
+  int* status;
+  const int* count;  // packed rows, on the device (nullptr: `rows`)
+  int rows;
+  int tp, W, vocab, K;
+  int c0, wc, wcols;  // the piece: first column, its width in prob, its columns
+  int bn;             // columns of a vocabulary tile (kLoss, kProb)
+  int a_rows;         // rows of a tile's A that are loaded (kLoss, kProb, kDx)
+  uint32_t idesc;
+  float c1;           // logit_scale * log2(e)
+  Ids targets;        // of the packed rows, or of all
+  const float* row_scale;
+  const float* row_lse;
+  float2* partial;
+  int tiles;          // vocabulary tiles: row length of partial
+  float* hit;
+  int splits;         // kDx: parts of the sum over the vocabulary
+  int accum_rows;     // rows of one part's slab
+  int add;            // kDx: add to accum; kDw: add to grad_weight
+  const float* unscale;
+};
+
+struct Shared {
+  uint64_t full[kStages];
+  uint64_t empty[kStages];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+};
+static_assert(sizeof(Shared) <= 256, "barriers must fit the 256 bytes kept for them");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Wait for a phase, bounded in time: on expiry the status word is set and the
+// kernel's roles stop issuing work.
+__device__ bool wait_phase(uint64_t* bar, uint32_t parity, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer_ns() - t0 > kTimeoutNs) {
+      atomicExch(status, 1);
+      return false;
+    }
+  }
+  return true;
+}
+
+// Operand whose M (or N) dimension is contiguous: 64 elements of it to a
+// 128-byte row, one row per k, boxes of [64 k][64 elements] one after another.
+// Leading byte offset: to the next 64 elements (a box); stride byte offset: to
+// the next 8 k.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(kBox >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      " .reg .pred p;\n"
+      " setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, int x, int y,
+                                             const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* tm, int x, int y, const void* src) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], "
+      "[%3];" ::"l"(reinterpret_cast<uint64_t>(tm)),
+      "r"(x), "r"(y), "r"(smem_u32(src))
+      : "memory");
+}
+
+// One tile of the output and the K blocks [kb0, kb1) that are summed into it.
+struct Tile {
+  int m;      // row tile (kDw: tile of the shard's rows)
+  int n;      // column tile; kLoss, kProb: tile within the shard
+  int r;      // shard (kDx: part of the sum)
+  int index;  // kLoss: vocabulary tile
+  int kb0, kb1;
+};
+
+template <int KIND>
+struct Work {
+  int mt, nt, total, kb, per_shard;
+  __device__ __forceinline__ Work(const GemmArgs& a, int rows) {
+    const int row_tiles = (rows + kTileM - 1) / kTileM;
+    const int k_tiles = (a.K + kTileN - 1) / kTileN;
+    if (KIND == kLoss || KIND == kProb) {
+      per_shard = (a.wcols + a.bn - 1) / a.bn;
+      mt = row_tiles;
+      nt = a.tp * per_shard;
+      kb = (a.K + kBlockK - 1) / kBlockK;
+      total = mt * nt;
+    } else if (KIND == kDx) {
+      per_shard = (a.wcols + kBlockK - 1) / kBlockK;  // K blocks of a shard
+      mt = row_tiles;
+      nt = k_tiles;
+      kb = a.tp * per_shard;
+      total = mt * nt * a.splits;
+    } else {
+      per_shard = (a.wcols + kTileM - 1) / kTileM;
+      mt = a.tp * per_shard;
+      nt = k_tiles;
+      kb = (rows + kBlockK - 1) / kBlockK;
+      total = mt * nt;
+    }
+  }
+  __device__ __forceinline__ Tile at(const GemmArgs& a, int i) const {
+    Tile t;
+    int part = 0;
+    if (KIND == kDx) {
+      part = i / (mt * nt);
+      i -= part * (mt * nt);
+    }
+    const int group = i / (kGroupM * nt);
+    const int rem = i - group * (kGroupM * nt);
+    const int left = mt - group * kGroupM;
+    const int rows = left < kGroupM ? left : kGroupM;
+    t.m = group * kGroupM + rem % rows;
+    t.n = rem / rows;
+    t.index = t.n;
+    t.kb0 = 0;
+    t.kb1 = kb;
+    t.r = part;
+    if (KIND == kLoss || KIND == kProb) {
+      t.r = t.n / per_shard;
+      t.n -= t.r * per_shard;
+    } else if (KIND == kDx) {
+      t.kb0 = (int)((long long)part * kb / a.splits);
+      t.kb1 = (int)((long long)(part + 1) * kb / a.splits);
+    } else {
+      t.r = t.m / per_shard;
+      t.m -= t.r * per_shard;
+    }
+    return t;
+  }
+};
+
+template <int KIND, typename T>
+__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  unsigned char* sA = base;
+  unsigned char* sB = sA + (size_t)kStages * kABytes;
+  unsigned char* sOut = sB + (size_t)kStages * kBBytes;
+  Shared* sh = reinterpret_cast<Shared*>(sOut + 4 * 2 * kStageOut);
+  const int warp = (int)threadIdx.x >> 5;
+  const int lane = (int)threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh->acc_full[b], 1);
+      mbar_init(&sh->acc_empty[b], 4);
+    }
+    mbar_init(&sh->drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sh->tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+
+  const int packed = a.count ? *a.count : a.rows;  // rows that count
+  // At least one row tile is made, so that a piece without rows comes out as zeros.
+  const Work<KIND> work(a, packed > 0 ? packed : 1);
+  const int G = (int)gridDim.x;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t keep = policy_evict_normal();
+      const uint32_t bytes = KIND == kDw ? kABytes + kBBytes
+                             : KIND == kDx
+                                 ? (uint32_t)a.a_rows * 128 + kBBytes
+                                 : (uint32_t)(a.a_rows + a.bn) * 128;
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; i < work.total && ok; i += G) {
+        const Tile t = work.at(a, i);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          if (!wait_phase(&sh->empty[stage], phase ^ 1u, a.status)) { ok = false; break; }
+          uint64_t* bar = &sh->full[stage];
+          unsigned char* A = sA + (size_t)stage * kABytes;
+          unsigned char* B = sB + (size_t)stage * kBBytes;
+          mbar_expect_tx(bar, bytes);
+          if (KIND == kLoss || KIND == kProb) {
+            tma_load_2d(A, &a.x, kb * kBlockK, t.m * kTileM, bar, keep);
+            tma_load_2d(B, &a.shard[t.r], kb * kBlockK, a.c0 + t.n * a.bn, bar, keep);
+          } else if (KIND == kDx) {
+            const int r = kb / work.per_shard;
+            const int b = kb - r * work.per_shard;
+            tma_load_2d(A, &a.p, r * a.wc + b * kBlockK, t.m * kTileM, bar, keep);
+            for (int j = 0; j < kTileN / 64; ++j)
+              tma_load_2d(B + j * kBox, &a.shard[r], t.n * kTileN + j * 64, a.c0 + b * kBlockK,
+                          bar, keep);
+          } else {
+            for (int j = 0; j < kTileM / 64; ++j)
+              tma_load_2d(A + j * kBox, &a.p, t.r * a.wc + t.m * kTileM + j * 64, kb * kBlockK,
+                          bar, keep);
+            for (int j = 0; j < kTileN / 64; ++j)
+              tma_load_2d(B + j * kBox, &a.x, t.n * kTileN + j * 64, kb * kBlockK, bar, keep);
+          }
+          ++issued;
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // Every copy issued must land before the CTA's shared memory goes: fill j
+      // completes the phase of parity (j / kStages) & 1 of stage j % kStages.
+      const int last = issued - 1;
+      for (int s = 0; s < kStages && s <= last; ++s) {
+        const int j = last - (last - s) % kStages;
+        wait_phase(&sh->full[s], (uint32_t)((j / kStages) & 1), a.status);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; i < work.total && ok; i += G) {
+        const Tile t = work.at(a, i);
+        if (!wait_phase(&sh->acc_empty[acc], acc_phase ^ 1u, a.status)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * kTileN);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          if (!wait_phase(&sh->full[stage], phase, a.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t A = smem_u32(sA + (size_t)stage * kABytes);
+          const uint32_t B = smem_u32(sB + (size_t)stage * kBBytes);
+          const uint64_t da = KIND == kDw ? smem_desc_mn(A) : smem_desc_sw128(A);
+          const uint64_t db = KIND == kDw || KIND == kDx ? smem_desc_mn(B) : smem_desc_sw128(B);
+          // A step of 16 k: 32 bytes along a K-contiguous row, or 16 rows of 128
+          // bytes of an operand with one row per k (the address field counts 16).
+          constexpr uint64_t step_a = KIND == kDw ? 128 : 2;
+          constexpr uint64_t step_b = KIND == kDw || KIND == kDx ? 128 : 2;
+#pragma unroll
+          for (int k = 0; k < kBlockK / kMmaK; ++k)
+            mma_f16(d, da + step_a * k, db + step_b * k, a.idesc,
+                    (kb != t.kb0 || k != 0) ? 1u : 0u);
+          mma_commit(&sh->empty[stage]);
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        mma_commit(&sh->acc_full[acc]);
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      }
+      // Every MMA issued must complete before the tensor memory is freed.
+      mma_commit(&sh->drain);
+      wait_phase(&sh->drain, 0, a.status);
+    }
+  } else {
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    unsigned char* const stage_out = sOut + (size_t)(warp - 2) * 2 * kStageOut;
+    int acc = 0, buf = 0;
+    uint32_t acc_phase = 0;
+    const float unscale = KIND == kDw ? *a.unscale : 1.f;
+    // Staged stores: the warp's 32 rows of 128 bytes, 16-byte column c of row r
+    // at c ^ (r & 7), the 128-byte swizzle of the tensor map.
+    auto store_begin = [&]() {
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      __syncwarp();
+      return stage_out + (size_t)buf * kStageOut + (size_t)lane * 128;
+    };
+    auto store_end = [&](const CUtensorMap* tm, int x, int y, bool add) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        const void* src = stage_out + (size_t)buf * kStageOut;
+        if (add)
+          tma_add_2d(tm, x, y, src);
+        else
+          tma_store_2d(tm, x, y, src);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+      buf ^= 1;
+    };
+    for (int i = blockIdx.x; i < work.total; i += G) {
+      const Tile t = work.at(a, i);
+      const bool ready = wait_phase(&sh->acc_full[acc], acc_phase, a.status);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      tc_fence_after();
+      const uint32_t tacc = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kTileN);
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->acc_empty[acc]);
+      };
+
+      if (KIND == kLoss || KIND == kProb) {
+        const int n = t.m * kTileM + row;
+        const bool on = n < packed;
+        // Columns of the tile in the real vocabulary, and the row's target in it.
+        const int col0 = a.c0 + t.n * a.bn;  // within the shard
+        int valid = a.vocab - t.r * a.W;
+        if (valid > a.W) valid = a.W;
+        valid -= col0;
+        long long id = -1;
+        if (on) id = load_id(a.targets, (size_t)n) - ((long long)t.r * a.W + col0);
+        const int at = id >= 0 && id < valid ? (int)id : -1;
+        if (KIND == kLoss) {
+          float top = -INFINITY, sum = 0.f;
+          for (int c = 0; c < a.bn; c += 32) {
+            uint32_t v[32];
+            tmem_ld_x32(tacc + (uint32_t)c, v);
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float y = c + j < valid ? __uint_as_float(v[j]) * a.c1 : -INFINITY;
+              v[j] = __float_as_uint(y);
+              mx = fmaxf(mx, y);
+            }
+            const float now = fmaxf(top, mx);
+            // Nothing above -inf yet: ex2(-inf - 0) = 0 adds nothing, and a NaN still shows.
+            const float ref = now == -INFINITY ? 0.f : now;
+            float part = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) part += ex2(__uint_as_float(v[j]) - ref);
+            sum = sum * ex2(top - ref) + part;
+            top = now;
+            if (at >= c && at < c + 32) {
+              float z = 0.f;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (at == c + j) z = __uint_as_float(v[j]);
+              a.hit[n] = z;
+            }
+          }
+          release();
+          if (on && n < a.rows) a.partial[(size_t)n * a.tiles + t.index] = make_float2(top, sum);
+        } else {
+          const float scale = on ? a.row_scale[n] : 0.f;
+          const float lse = on ? a.row_lse[n] : 0.f;
+          for (int c = 0; c < a.bn; c += 64) {
+            uint32_t v[2][32];
+            tmem_ld_x32(tacc + (uint32_t)c, v[0]);
+            tmem_ld_x32(tacc + (uint32_t)c + 32, v[1]);
+            if (c + 64 >= a.bn) release();
+            if (t.n * a.bn + c >= a.wc) continue;  // beyond the piece's place in prob
+            unsigned char* dst = store_begin();
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                float d[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int j = q * 8 + h * 2 + e;
+                  const float y = __uint_as_float(v[j >> 5][j & 31]);
+                  d[e] = ex2(fmaf(y, a.c1, -lse)) - (at == c + j ? 1.f : 0.f);
+                  d[e] = on && c + j < valid ? d[e] * scale : 0.f;
+                }
+                w[h] = Elem<T>::pack2(d[0], d[1]);
+              }
+              *reinterpret_cast<uint4*>(dst + ((q ^ (lane & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            store_end(&a.out, t.r * a.wc + t.n * a.bn + c, t.m * kTileM + quarter * 32, false);
+          }
+        }
+      } else if (KIND == kDx) {
+        for (int c = 0; c < kTileN; c += 32) {
+          uint32_t v[32];
+          tmem_ld_x32(tacc + (uint32_t)c, v);
+          if (c + 32 == kTileN) release();
+          if (t.n * kTileN + c >= a.K) continue;
+          unsigned char* dst = store_begin();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4*>(dst + ((q ^ (lane & 7)) << 4)) =
+                make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          store_end(&a.out, t.n * kTileN + c, t.r * a.accum_rows + t.m * kTileM + quarter * 32,
+                    a.add != 0);
+        }
+      } else {
+        for (int c = 0; c < kTileN; c += 64) {
+          uint32_t v[2][32];
+          tmem_ld_x32(tacc + (uint32_t)c, v[0]);
+          tmem_ld_x32(tacc + (uint32_t)c + 32, v[1]);
+          if (c + 64 == kTileN) release();
+          const int y = a.c0 + t.m * kTileM + quarter * 32;
+          if (t.n * kTileN + c >= a.K || y >= a.W) continue;
+          unsigned char* dst = store_begin();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const int j = q * 8 + h * 2;
+              w[h] = Elem<T>::pack2(__uint_as_float(v[j >> 5][j & 31]) * unscale,
+                                    __uint_as_float(v[j >> 5][(j & 31) + 1]) * unscale);
+            }
+            *reinterpret_cast<uint4*>(dst + ((q ^ (lane & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          store_end(&a.shard[t.r], t.n * kTileN + c, y, a.add != 0);
+        }
+      }
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+// ---- rows ----------------------------------------------------------------------
+
+constexpr int kPackThreads = 512;
+constexpr int kPackWarps = kPackThreads / 32;
+
+struct PackArgs {
+  const void* hidden;
+  size_t ld;
+  Ids targets;
+  int N, K, vocab;
+  int grad;  // for the gradient (targets outside the vocabulary are masked too)
+  float logit_scale;
+  const float* lse;
+  const float* grad_loss;
+  float* loss;     // zeros in masked rows
+  float* lse_out;
+  void* grad_hidden;
+  size_t ld_grad;
+  int headroom;  // the largest |row_scale| is brought below 2^headroom (0: kept as it is)
+  void* packed;
+  int* count;
+  float* unscale;
+  int* row_of;
+  int* target;
+  float* row_scale;
+  float* row_lse;
+};
+
+__device__ __forceinline__ bool unmasked(const PackArgs& a, long long id) {
+  return id >= 0 && (!a.grad || id < a.vocab);
+}
+
+// Copies the unmasked rows of hidden together, in order. CTA b has the rows
+// [b * N / G, (b + 1) * N / G); each CTA counts the unmasked rows before its own
+// from the targets (a few bytes per row from L2, against K elements copied), so
+// the CTAs need nothing from one another. The rows up to the next multiple of
+// 64 are filled with zeros: kDw sums 64 rows at a time.
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constant__ PackArgs a) {
+  __shared__ int warp_sum[3][kPackWarps];
+  __shared__ float warp_max[kPackWarps];
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  const long long G = gridDim.x;
+  const int lo = (int)(blockIdx.x * (long long)a.N / G);
+  const int hi = (int)((blockIdx.x + 1) * (long long)a.N / G);
+  int before = 0, all = 0;
+  float most = 0.f;
+  for (int n = threadIdx.x; n < a.N; n += kPackThreads) {
+    if (!unmasked(a, load_id(a.targets, n))) continue;
+    ++all;
+    if (n < lo) ++before;
+    if (a.headroom != 0) most = fmaxf(most, fabsf(a.grad_loss[n] * a.logit_scale));
+  }
+  for (int o = 16; o; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
+  if (lane == 0) {
+    warp_sum[0][warp] = before;
+    warp_sum[1][warp] = all;
+    warp_max[warp] = most;
+  }
+  __syncthreads();
+  before = all = 0;
+  most = 0.f;
+  for (int w = 0; w < kPackWarps; ++w) {
+    before += warp_sum[0][w];
+    all += warp_sum[1][w];
+    most = fmaxf(most, warp_max[w]);
+  }
+  // A power of two, so that scaling back is exact.
+  float up = 1.f;
+  if (a.headroom != 0 && most > 0.f && most <= FLT_MAX) {
+    int e;
+    frexpf(most, &e);  // most < 2^e
+    e = a.headroom - e;
+    up = ldexpf(1.f, e < -100 ? -100 : e > 100 ? 100 : e);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *a.count = all;
+    *a.unscale = 1.f / up;
+  }
+
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int vecs = a.K / 8;
+  uint4* const packed = static_cast<uint4*>(a.packed);
+  int at = before;
+  for (int n0 = lo; n0 < hi; n0 += kPackWarps) {
+    // Warp w has row n0 + w; its place follows the unmasked rows of the warps
+    // before it.
+    const int n = n0 + warp;
+    const long long id = n < hi ? load_id(a.targets, n) : -1;
+    const bool keep = n < hi && unmasked(a, id);
+    __syncthreads();  // the flags of the last round have been read
+    if (lane == 0) warp_sum[2][warp] = keep;
+    __syncthreads();
+    int to = at;
+    for (int w = 0; w < kPackWarps; ++w) {
+      const int f = warp_sum[2][w];
+      at += f;
+      if (w < warp) to += f;
+    }
+    if (n >= hi) continue;
+    if (keep) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.hidden) +
+                                                        (size_t)n * a.ld);
+      uint4* dst = packed + (size_t)to * vecs;
+      for (int v = lane; v < vecs; v += 128) {
+        uint4 x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (v + 32 * j < vecs) x[j] = src[v + 32 * j];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (v + 32 * j < vecs) dst[v + 32 * j] = x[j];
+      }
+      if (lane == 0) {
+        a.row_of[to] = n;
+        a.target[to] = id < a.vocab ? (int)id : -1;
+        if (a.grad) {
+          a.row_scale[to] = a.grad_loss[n] * a.logit_scale * up;
+          a.row_lse[to] = a.lse[n] * kLog2e;
+        }
+      }
+    } else if (a.grad) {
+      if (a.grad_hidden) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_hidden) +
+                                              (size_t)n * a.ld_grad);
+        for (int v = lane; v < vecs; v += 32) dst[v] = zero;
+      }
+    } else if (lane == 0) {
+      a.loss[n] = 0.f;
+      a.lse_out[n] = 0.f;
+    }
+  }
+  const int end = (int)round_up(all > 0 ? all : 1, 64);
+  for (int to = all + (int)blockIdx.x * kPackWarps + warp; to < end; to += (int)G * kPackWarps)
+    for (int v = lane; v < vecs; v += 32) packed[(size_t)to * vecs + v] = zero;
+}
+
+struct MergeArgs {
+  const float2* partial;
+  int tiles;
+  const float* hit;
+  const int* count;  // packed rows (nullptr: the rows are the caller's own)
+  const int* row_of;
+  Ids targets;
+  int rows, vocab;
+  float* loss;
+  float* lse;
+};
+
+// Joins the tiles' statistics of a row: one warp per row.
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ MergeArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int rows = a.count ? *a.count : a.rows;
+  const int step = gridDim.x * 8;
+  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += step) {
+    const float2* p = a.partial + (size_t)i * a.tiles;
+    float top = -INFINITY, sum = 0.f;
+    for (int t = lane; t < a.tiles; t += 32) {
+      const float2 x = p[t];
+      const float now = fmaxf(top, x.x);
+      const float ref = now == -INFINITY ? 0.f : now;
+      sum = sum * ex2(top - ref) + x.y * ex2(x.x - ref);
+      top = now;
+    }
+    for (int o = 16; o; o >>= 1) {
+      const float t = __shfl_xor_sync(0xffffffffu, top, o);
+      const float s = __shfl_xor_sync(0xffffffffu, sum, o);
+      const float now = fmaxf(top, t);
+      const float ref = now == -INFINITY ? 0.f : now;
+      sum = sum * ex2(top - ref) + s * ex2(t - ref);
+      top = now;
+    }
+    if (lane) continue;
+    const long long id = load_id(a.targets, i);
+    const int n = a.count ? a.row_of[i] : i;
+    const bool masked = !a.count && id < 0;
+    const float rest = log2f(sum);
+    // The difference to the largest logit first: it is exact where they are near.
+    const float loss = id >= 0 && id < a.vocab ? (top - a.hit[i] + rest) * kLn2 : NAN;
+    a.loss[n] = masked ? 0.f : loss;
+    a.lse[n] = masked ? 0.f : (top + rest) * kLn2;
+  }
+}
+
+struct FinishArgs {
+  const float* accum;
+  int splits, accum_rows, K;
+  const int* count;
+  const int* row_of;
+  const float* unscale;
+  void* grad;
+  size_t ld;
+};
+
+// grad_hidden: the parts' sums in order, rounded once, to the rows they belong to.
+template <typename T>
+__global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ FinishArgs a) {
+  const int vecs = a.K / 8;
+  const long long total = (long long)*a.count * vecs;
+  const float unscale = *a.unscale;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int row = (int)(i / vecs);
+    const int v = (int)(i - (long long)row * vecs);
+    float s[8] = {};
+    for (int p = 0; p < a.splits; ++p) {
+      const float4* src = reinterpret_cast<const float4*>(
+          a.accum + ((size_t)p * a.accum_rows + row) * a.K + (size_t)v * 8);
+      const float4 lo = src[0], hi = src[1];
+      s[0] += lo.x; s[1] += lo.y; s[2] += lo.z; s[3] += lo.w;
+      s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
+    }
+    uint4 x;
+    x.x = Elem<T>::pack2(s[0] * unscale, s[1] * unscale);
+    x.y = Elem<T>::pack2(s[2] * unscale, s[3] * unscale);
+    x.z = Elem<T>::pack2(s[4] * unscale, s[5] * unscale);
+    x.w = Elem<T>::pack2(s[6] * unscale, s[7] * unscale);
+    *reinterpret_cast<uint4*>(static_cast<T*>(a.grad) + (size_t)a.row_of[row] * a.ld +
+                              (size_t)v * 8) = x;
+  }
+}
+
+// ---- host ----------------------------------------------------------------------
+
+// Row-major [rows, cols] matrix, rows `ld` elements apart, box of [box_rows][128 bytes].
+bool encode(CUtensorMap* tm, const void* ptr, int dtype, uint64_t rows, uint64_t cols, uint64_t ld,
+            uint32_t box_rows) {
+  const EncodeTiled fn = tensor_map_encoder();
+  if (!fn) return false;
+  const uint32_t e = (uint32_t)elem_bytes(dtype);
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld * e};
+  cuuint32_t box[2] = {128 / e, box_rows};
+  cuuint32_t steps[2] = {1, 1};
+  const CUtensorMapDataType type = dtype == HG_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : dtype == HG_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  return fn(tm, type, 2, const_cast<void*>(ptr), dims, strides, box, steps,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Real vocabulary rows of shard r.
+int shard_rows(const hg_vocab& h, int r) {
+  const long long left = (long long)h.vocab - (long long)r * h.W;
+  return (int)(left < 0 ? 0 : left < h.W ? left : h.W);
+}
+
+// Shards that hold part of the real vocabulary.
+int real_shards(const hg_vocab& h) { return (int)div_up(h.vocab, h.W); }
+
+// The weights' maps stop at the real vocabulary: what lies beyond reads as
+// zeros. (A shard without any real row keeps one, whose logits kProb masks.)
+bool encode_weights(const hg_vocab& h, const void* const* w, uint32_t box_rows, CUtensorMap* tm) {
+  for (int r = 0; r < h.tp; ++r) {
+    const int rows = shard_rows(h, r);
+    if (!encode(&tm[r], w[r], h.dtype, rows > 0 ? rows : 1, h.K, h.K, box_rows)) return false;
+  }
+  return true;
+}
+
+// Instruction descriptor of tcgen05.mma kind::f16: D fp32 (bits 4-5 = 1), A and
+// B bf16 (1) or fp16 (0) (bits 7-9, 10-12), A and B transposed (bits 15, 16:
+// their M or N dimension is contiguous), N >> 3 in bits 17-22, M >> 4 in bits
+// 24-28.
+uint32_t instruction(int dtype, bool a_mn, bool b_mn, int n) {
+  const uint32_t type = dtype == HG_BF16 ? 1u : 0u;
+  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
+}
+
+template <int KIND, typename T>
+cudaError_t launch_as(const GemmArgs& a, int ctas, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(gemm_kernel<KIND, T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  gemm_kernel<KIND, T><<<(unsigned)ctas, kThreads, kSmemBytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int KIND>
+cudaError_t launch(const hg_vocab& h, const GemmArgs& a, cudaStream_t stream) {
+  return h.dtype == HG_BF16 ? launch_as<KIND, __nv_bfloat16>(a, h.sms, stream)
+                            : launch_as<KIND, __half>(a, h.sms, stream);
+}
+
+// Rows of A that a tile loads when all rows fit in one tile: the tile's other
+// rows keep what shared memory held, and only reach output rows nobody reads.
+int rows_loaded(int N) { return N >= kTileM ? kTileM : (int)round_up(N > 0 ? N : 1, 8); }
+
+// Width of the vocabulary tiles: kTileN, but for few rows, where reading the
+// weights bounds the call, the width that leaves the busiest SM the fewest bytes
+// (a tile also reads the rows, from L2: counted as half).
+int tile_width(const hg_vocab& h, int N, int cols, int step) {
+  if (N > kSmallRows) return kTileN;
+  const int rows = rows_loaded(N);
+  int best = kTileN;
+  long long least = -1;
+  for (int bn = kTileN; bn >= step; bn -= step) {
+    const long long tiles = (long long)h.tp * div_up(cols, bn);
+    const long long cost = div_up(tiles, h.sms) * (bn + rows / 2);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = bn;
+    }
+  }
+  return best;
+}
+
+// Parts of the sum over the vocabulary in kDx: the number that keeps the SMs
+// busiest, by at least 3 % over a smaller one.
+int dx_splits(const hg_vocab& h, int N) {
+  const long long tiles = div_up(N > 0 ? N : 1, kTileM) * div_up(h.K, kTileN);
+  const long long kb = real_shards(h) * div_up(h.piece_cols < h.W ? h.piece_cols : h.W, kBlockK);
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= kMaxSplits && s <= kb; ++s) {
+    const double cost = (double)div_up(tiles * s, h.sms) / s;
+    if (s == 1 || cost < 0.97 * least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+unsigned row_blocks(const hg_vocab& h, int N) {
+  const long long want = div_up(N, 8);
+  return (unsigned)(want < 1 ? 1 : want < 2 * h.sms ? want : 2 * h.sms);
+}
+
+PackArgs pack_args(const hg_vocab& h, const LossCall& c) {
+  PackArgs a = {};
+  a.hidden = c.hidden;
+  a.ld = c.ld;
+  a.targets = c.targets;
+  a.N = c.N;
+  a.K = h.K;
+  a.vocab = h.vocab;
+  a.logit_scale = c.logit_scale;
+  a.lse = c.lse;
+  a.grad_loss = c.grad_loss;
+  a.loss = c.loss;
+  a.lse_out = c.lse_out;
+  a.grad_hidden = c.grad_hidden;
+  a.ld_grad = c.ld_grad;
+  a.packed = h.packed;
+  a.count = h.count;
+  a.unscale = h.unscale;
+  a.row_of = h.row_of;
+  a.target = h.target;
+  a.row_scale = h.row_scale;
+  a.row_lse = h.row_lse;
+  return a;
+}
+
+GemmArgs gemm_args(const hg_vocab& h, const LossCall& c) {
+  GemmArgs a = {};
+  a.status = h.status;
+  a.rows = c.N;
+  a.tp = h.tp;
+  a.W = h.W;
+  a.vocab = h.vocab;
+  a.K = h.K;
+  a.c1 = c.logit_scale * kLog2e;
+  a.row_scale = h.row_scale;
+  a.row_lse = h.row_lse;
+  a.partial = h.partial;
+  a.hit = h.hit;
+  a.unscale = h.unscale;
+  a.splits = 1;
+  return a;
+}
+
+}  // namespace
+
+long long loss_partials(const hg_vocab& h) {
+  // Few rows have the narrowest tiles (tile_width steps by 32).
+  const long long few = (h.max_rows < kSmallRows ? h.max_rows : kSmallRows) * div_up(h.W, 32);
+  const long long many = h.max_rows * div_up(h.W, kTileN);
+  return h.tp * (few > many ? few : many);
+}
+
+long long loss_rows_pad(long long rows) { return round_up(rows, 256); }
+
+long long loss_accum_rows(const hg_vocab& h) {
+  long long most = 0;
+  for (long long n = 1; n <= h.max_rows + kTileM; n += kTileM) {
+    const int N = (int)(n < h.max_rows ? n : h.max_rows);
+    const long long rows = (long long)dx_splits(h, N) * round_up(N, kTileM);
+    if (rows > most) most = rows;
+  }
+  return most;
+}
+
+cudaError_t loss(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
+  GemmArgs a = gemm_args(h, c);
+  const bool pack = c.N > kSmallRows;
+  a.wcols = h.W;
+  a.bn = tile_width(h, c.N, h.W, 32);
+  a.a_rows = pack ? kTileM : rows_loaded(c.N);
+  a.tp = real_shards(h);
+  a.tiles = (int)(a.tp * div_up(h.W, a.bn));
+  a.idesc = instruction(h.dtype, false, false, a.bn);
+  if (!encode_weights(h, c.weight, a.bn, a.shard)) return cudaErrorInvalidValue;
+  cudaError_t e = cudaSuccess;
+  MergeArgs m = {};
+  if (pack) {
+    const PackArgs p = pack_args(h, c);
+    pack_kernel<<<row_blocks(h, c.N), kPackThreads, 0, stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    a.count = h.count;
+    a.targets = Ids{h.target, 4};
+    if (!encode(&a.x, h.packed, h.dtype, loss_rows_pad(c.N), h.K, h.K, kTileM))
+      return cudaErrorInvalidValue;
+    m.count = h.count;
+    m.row_of = h.row_of;
+  } else {
+    a.targets = c.targets;
+    if (!encode(&a.x, c.hidden, h.dtype, c.N, h.K, c.ld, a.a_rows)) return cudaErrorInvalidValue;
+  }
+  e = launch<kLoss>(h, a, stream);
+  if (e != cudaSuccess) return e;
+  m.partial = h.partial;
+  m.tiles = a.tiles;
+  m.hit = h.hit;
+  m.targets = a.targets;
+  m.rows = c.N;
+  m.vocab = h.vocab;
+  m.loss = c.loss;
+  m.lse = c.lse_out;
+  merge_kernel<<<(unsigned)div_up(c.N, 8), 256, 0, stream>>>(m);
+  return cudaGetLastError();
+}
+
+cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
+  const long long pad = loss_rows_pad(c.N > 0 ? c.N : 1);
+  const bool small = c.N <= kSmallRows;
+  const int a_rows = small ? rows_loaded(c.N) : kTileM;
+  PackArgs p = pack_args(h, c);
+  p.grad = 1;
+  p.headroom = h.dtype == HG_FP16 ? 14 : 0;  // |d| < 2^14 * 2, small terms kept off fp16's floor
+  pack_kernel<<<row_blocks(h, c.N), kPackThreads, 0, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+
+  // One argument block per product; only the piece changes between launches.
+  GemmArgs prob = gemm_args(h, c);
+  prob.count = h.count;
+  prob.targets = Ids{h.target, 4};
+  prob.wc = h.piece_cols;
+  prob.a_rows = a_rows;
+  GemmArgs dx = prob, dw = prob;
+  const uint64_t prob_cols = (uint64_t)h.tp * h.piece_cols;
+  const int first = h.piece_cols < h.W ? h.piece_cols : h.W;
+  prob.bn = tile_width(h, c.N, first, 64);
+  prob.idesc = instruction(h.dtype, false, false, prob.bn);
+  if (!encode_weights(h, c.weight, prob.bn, prob.shard) ||
+      !encode(&prob.x, h.packed, h.dtype, pad, h.K, h.K, a_rows) ||
+      !encode(&prob.out, h.prob, h.dtype, pad, prob_cols, prob_cols, 32))
+    return cudaErrorInvalidValue;
+  int splits = 1;
+  if (c.grad_hidden) {
+    dx.idesc = instruction(h.dtype, false, true, kTileN);
+    dx.tp = real_shards(h);  // 0 * NaN of a padding shard must not be summed
+    splits = dx_splits(h, c.N);
+    dx.accum_rows = (int)round_up(c.N > 0 ? c.N : 1, kTileM);
+    if (!encode_weights(h, c.weight, kBlockK, dx.shard) ||
+        !encode(&dx.p, h.prob, h.dtype, pad, prob_cols, prob_cols, a_rows) ||
+        !encode(&dx.out, h.accum, HG_FP32, (uint64_t)splits * dx.accum_rows, h.K, h.K, 32))
+      return cudaErrorInvalidValue;
+  }
+  if (c.grad_weight) {
+    dw.idesc = instruction(h.dtype, true, true, kTileN);
+    dw.add = c.accumulate;
+    for (int r = 0; r < h.tp; ++r)
+      if (!encode(&dw.shard[r], c.grad_weight[r], h.dtype, h.W, h.K, h.K, 32))
+        return cudaErrorInvalidValue;
+    if (!encode(&dw.p, h.prob, h.dtype, pad, prob_cols, prob_cols, kBlockK) ||
+        !encode(&dw.x, h.packed, h.dtype, pad, h.K, h.K, kBlockK))
+      return cudaErrorInvalidValue;
+  }
+  for (int c0 = 0; c0 < h.W; c0 += h.piece_cols) {
+    const int left = h.W - c0;
+    prob.c0 = dx.c0 = dw.c0 = c0;
+    prob.wcols = dx.wcols = dw.wcols = left < h.piece_cols ? left : h.piece_cols;
+    e = launch<kProb>(h, prob, stream);
+    if (e == cudaSuccess && c.grad_hidden) {
+      dx.add = c0 > 0;
+      // A short last piece may have fewer K blocks than parts: each part has one.
+      const int kb = dx.tp * (int)div_up(dx.wcols, kBlockK);
+      dx.splits = splits < kb ? splits : kb;
+      e = launch<kDx>(h, dx, stream);
+    }
+    if (e == cudaSuccess && c.grad_weight) e = launch<kDw>(h, dw, stream);
+    if (e != cudaSuccess) return e;
+  }
+  if (!c.grad_hidden || c.N == 0) return cudaSuccess;
+  FinishArgs f = {};
+  f.accum = h.accum;
+  f.splits = splits;
+  f.accum_rows = dx.accum_rows;
+  f.K = h.K;
+  f.count = h.count;
+  f.row_of = h.row_of;
+  f.unscale = h.unscale;
+  f.grad = c.grad_hidden;
+  f.ld = c.ld_grad;
+  const long long blocks = div_up((long long)c.N * (h.K / 8), 256);
+  const unsigned grid = (unsigned)(blocks < 8ll * h.sms ? blocks : 8ll * h.sms);
+  if (h.dtype == HG_BF16)
+    finish_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(f);
+  else
+    finish_kernel<__half><<<grid, 256, 0, stream>>>(f);
+  return cudaGetLastError();
+}
+
+}  // namespace vocab
+}  // namespace hg

@@ -71,13 +71,24 @@ def load() -> ctypes.CDLL:
     lib.hg_probe.argtypes = [i, i, i, vp, st]
     lib.hg_probe_scratch_bytes.argtypes = [i, i]
     lib.hg_probe_scratch_bytes.restype = ctypes.c_size_t
+    sz, f = ctypes.c_size_t, ctypes.c_float
+    lib.hg_vocab_create.argtypes = [i, i, i, i, i, i, i, sz, vpp]
+    lib.hg_vocab_destroy.argtypes = [vp]
+    lib.hg_vocab_workspace_bytes.argtypes = [vp]
+    lib.hg_vocab_workspace_bytes.restype = sz
+    lib.hg_vocab_sync.argtypes = [vp, st]
+    lib.hg_vocab_embed.argtypes = [vp, vp, i, i, vpp, f, vp, sz, st]
+    lib.hg_vocab_embed_grad.argtypes = [vp, vp, i, i, vp, sz, vpp, f, i, st]
+    lib.hg_vocab_loss.argtypes = [vp, vp, sz, vpp, vp, i, i, f, vp, vp, st]
+    lib.hg_vocab_loss_grad.argtypes = [vp, vp, sz, vpp, vp, i, vp, vp, i, f, vp, sz, vpp, i, st]
     lib.hg_strerror.argtypes = [i]
     lib.hg_strerror.restype = ctypes.c_char_p
     for name in ("hg_create", "hg_create_ex", "hg_destroy", "hg_gather", "hg_gather_host",
                  "hg_sync", "hg_rearm",
                  "hg_parity", "hg_mailbox", "hg_launch_shape", "hg_debug_skip_push",
                  "hg_stock_gather", "hg_gather_fused", "hg_gather_stats", "hg_timeline",
-                 "hg_probe"):
+                 "hg_probe", "hg_vocab_create", "hg_vocab_destroy", "hg_vocab_sync",
+                 "hg_vocab_embed", "hg_vocab_embed_grad", "hg_vocab_loss", "hg_vocab_loss_grad"):
         getattr(lib, name).restype = i
     _LIB = lib
     return lib
@@ -400,3 +411,160 @@ def hg_gather_static(shards: Sequence[torch.Tensor], outs: Sequence[torch.Tensor
         st_ptr = status_out.data_ptr()
     _check(fn(tp, W, _ptr_array(shards), _ptr_array(outs), M, st_ptr, _stream_ptr(stream)),
            "hg_gather_static")
+
+
+_VOCAB_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # HG_BF16, ...
+_VOCAB_OPS = {"embed": 1, "embed_grad": 2, "loss": 4, "loss_grad": 8}  # HG_VOCAB_*
+
+
+class VocabHandle:
+    """Owner of one hg_vocab (the workspace of the vocabulary operators); freed
+    by hg_vocab_destroy on close() or collection."""
+
+    def __init__(self, ptr: int, tp: int, shard_cols: int, vocab: int, hidden: int, max_rows: int,
+                 dtype: torch.dtype):
+        self.ptr = ptr
+        self.tp, self.shard_cols, self.vocab = tp, shard_cols, vocab
+        self.hidden, self.max_rows, self.dtype = hidden, max_rows, dtype
+
+    @property
+    def workspace_bytes(self) -> int:
+        return int(load().hg_vocab_workspace_bytes(self.ptr))
+
+    def close(self) -> None:
+        if self.ptr:
+            ptr, self.ptr = self.ptr, 0
+            _check(load().hg_vocab_destroy(ptr), "hg_vocab_destroy")
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def hg_vocab_create(tp: int, shard_cols: int, hidden: int, max_rows: int, *, vocab: int = 0,
+                    dtype: torch.dtype = torch.bfloat16,
+                    ops: Sequence[str] = ("embed", "embed_grad", "loss", "loss_grad"),
+                    piece_bytes: int = 0) -> VocabHandle:
+    """Workspace of the vocabulary operators on a [tp * shard_cols, hidden]
+    matrix in tp shards, for calls of up to max_rows rows. vocab: the real
+    vocabulary where the last shards are padded (0: all of it). ops: which of
+    "embed", "embed_grad", "loss", "loss_grad" will be called (each needs its
+    own workspace). piece_bytes: see include/hg.h."""
+    if dtype not in _VOCAB_TYPES:
+        raise ValueError(f"hg_vocab_create: dtype must be bfloat16, float16 or float32, got {dtype}")
+    bits = 0
+    for op in ops:
+        if op not in _VOCAB_OPS:
+            raise ValueError(f"hg_vocab_create: unknown operator {op!r}")
+        bits |= _VOCAB_OPS[op]
+    out = ctypes.c_void_p()
+    _check(load().hg_vocab_create(tp, shard_cols, vocab, hidden, max_rows, _VOCAB_TYPES[dtype],
+                                  bits, piece_bytes, ctypes.byref(out)), "hg_vocab_create")
+    return VocabHandle(out.value, tp, shard_cols, vocab or tp * shard_cols, hidden, max_rows, dtype)
+
+
+def hg_vocab_destroy(h: VocabHandle) -> None:
+    h.close()
+
+
+def hg_vocab_sync(h: VocabHandle, stream=None) -> None:
+    _check(load().hg_vocab_sync(h.ptr, _stream_ptr(stream)), "hg_vocab_sync")
+
+
+def _vocab_ids(t: torch.Tensor, what: str) -> int:
+    if not t.is_cuda or t.dtype not in (torch.int32, torch.int64) or t.dim() != 1 \
+            or not t.is_contiguous():
+        raise ValueError(f"{what}: need a contiguous 1-D int32 or int64 CUDA tensor")
+    return t.shape[0]
+
+
+def _vocab_rows(h: VocabHandle, t: torch.Tensor, n: int, what: str) -> int:
+    """Row distance of a token-side [n, hidden] matrix (rows contiguous)."""
+    if not t.is_cuda or t.dtype != h.dtype:
+        raise ValueError(f"{what}: need a CUDA tensor of {h.dtype}, got {t.dtype} on {t.device}")
+    if tuple(t.shape) != (n, h.hidden) or (h.hidden > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: need [{n}, {h.hidden}] with contiguous rows, got "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    if n <= 1:
+        return h.hidden
+    if t.stride(0) < h.hidden:
+        raise ValueError(f"{what}: rows overlap (row stride {t.stride(0)})")
+    return t.stride(0)
+
+
+def _vocab_shards(h: VocabHandle, ts: Sequence[torch.Tensor], what: str):
+    if len(ts) != h.tp:
+        raise ValueError(f"{what}: expected {h.tp} shards, got {len(ts)}")
+    for t in ts:
+        if not t.is_cuda or t.dtype != h.dtype:
+            raise ValueError(f"{what}: need CUDA tensors of {h.dtype}, got {t.dtype} on {t.device}")
+        if tuple(t.shape) != (h.shard_cols, h.hidden) or not t.is_contiguous():
+            raise ValueError(f"{what}: need contiguous [{h.shard_cols}, {h.hidden}], got "
+                             f"{tuple(t.shape)}")
+    return _ptr_array(ts)
+
+
+def _vocab_floats(t: torch.Tensor, n: int, what: str) -> int:
+    if not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != (n,) \
+            or not t.is_contiguous():
+        raise ValueError(f"{what}: need a contiguous float32 CUDA tensor [{n}]")
+    return t.data_ptr()
+
+
+def hg_vocab_embed(h: VocabHandle, tokens: torch.Tensor, table: Sequence[torch.Tensor],
+                   out: torch.Tensor, scale: float = 1.0, stream=None) -> None:
+    """out[n] = scale * table[tokens[n]]; a token outside [0, vocab) gives zeros."""
+    n = _vocab_ids(tokens, "tokens")
+    ld = _vocab_rows(h, out, n, "out")
+    _check(load().hg_vocab_embed(h.ptr, tokens.data_ptr(), tokens.element_size(), n,
+                                 _vocab_shards(h, table, "table"), scale, out.data_ptr(), ld,
+                                 _stream_ptr(stream)), "hg_vocab_embed")
+
+
+def hg_vocab_embed_grad(h: VocabHandle, tokens: torch.Tensor, grad_out: torch.Tensor,
+                        grad_table: Sequence[torch.Tensor], scale: float = 1.0,
+                        accumulate: bool = False, stream=None) -> None:
+    """grad_table[v] = scale * sum of grad_out[n] over tokens[n] = v (every row
+    written), or added to grad_table where accumulate."""
+    n = _vocab_ids(tokens, "tokens")
+    ld = _vocab_rows(h, grad_out, n, "grad_out")
+    _check(load().hg_vocab_embed_grad(h.ptr, tokens.data_ptr(), tokens.element_size(), n,
+                                      grad_out.data_ptr(), ld,
+                                      _vocab_shards(h, grad_table, "grad_table"), scale,
+                                      int(bool(accumulate)), _stream_ptr(stream)),
+           "hg_vocab_embed_grad")
+
+
+def hg_vocab_loss(h: VocabHandle, hidden: torch.Tensor, weight: Sequence[torch.Tensor],
+                  targets: torch.Tensor, loss: torch.Tensor, lse: torch.Tensor,
+                  logit_scale: float = 1.0, stream=None) -> None:
+    """Per-row softmax cross entropy of logit_scale * hidden @ weight.T and its
+    logsumexp, without storing logits. A negative target masks its row."""
+    n = _vocab_ids(targets, "targets")
+    ld = _vocab_rows(h, hidden, n, "hidden")
+    _check(load().hg_vocab_loss(h.ptr, hidden.data_ptr(), ld, _vocab_shards(h, weight, "weight"),
+                                targets.data_ptr(), targets.element_size(), n, logit_scale,
+                                _vocab_floats(loss, n, "loss"), _vocab_floats(lse, n, "lse"),
+                                _stream_ptr(stream)), "hg_vocab_loss")
+
+
+def hg_vocab_loss_grad(h: VocabHandle, hidden: torch.Tensor, weight: Sequence[torch.Tensor],
+                       targets: torch.Tensor, lse: torch.Tensor, grad_loss: torch.Tensor,
+                       grad_hidden: torch.Tensor | None,
+                       grad_weight: Sequence[torch.Tensor] | None, logit_scale: float = 1.0,
+                       accumulate: bool = False, stream=None) -> None:
+    """Gradient of hg_vocab_loss from its logsumexp and the upstream gradient of
+    each row's loss, to grad_hidden and grad_weight (either may be None);
+    accumulate adds to what grad_weight holds."""
+    n = _vocab_ids(targets, "targets")
+    ld = _vocab_rows(h, hidden, n, "hidden")
+    ld_grad = h.hidden if grad_hidden is None else _vocab_rows(h, grad_hidden, n, "grad_hidden")
+    _check(load().hg_vocab_loss_grad(
+        h.ptr, hidden.data_ptr(), ld, _vocab_shards(h, weight, "weight"), targets.data_ptr(),
+        targets.element_size(), _vocab_floats(lse, n, "lse"),
+        _vocab_floats(grad_loss, n, "grad_loss"), n, logit_scale,
+        None if grad_hidden is None else grad_hidden.data_ptr(), ld_grad,
+        None if grad_weight is None else _vocab_shards(h, grad_weight, "grad_weight"),
+        int(bool(accumulate)), _stream_ptr(stream)), "hg_vocab_loss_grad")
