@@ -30,21 +30,23 @@ namespace {
 
 enum Kind { kLoss, kProb, kDx, kDw };
 
-constexpr int kTileM = 128;   // rows of a tile: TMEM lanes
+constexpr int kTileM = 128;   // rows of a CTA's tile: TMEM lanes
 constexpr int kTileN = 256;   // columns of a tile: fp32 TMEM columns
 constexpr int kBlockK = 64;   // K per stage: one 128-byte swizzle atom of 16-bit elements
 constexpr int kMmaK = 16;     // K per tcgen05.mma of kind::f16
-constexpr int kStages = 4;
-constexpr uint32_t kABytes = kTileM * kBlockK * 2;
-constexpr uint32_t kBBytes = kTileN * kBlockK * 2;
+constexpr int kMaxStages = 12;
 constexpr uint32_t kBox = 64 * 128;  // a [64 x 64] box of 16-bit elements
 constexpr uint32_t kTmemCols = 2 * kTileN;  // two accumulators
-constexpr int kThreads = 192;   // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;  // warp 0 TMA, warp 1 MMA
 constexpr uint32_t kStageOut = 32 * 128;  // a warp's staged [32 rows x 128 bytes]
-constexpr size_t kSmemBytes =
-    1024 + (size_t)kStages * (kABytes + kBBytes) + 4 * 2 * kStageOut + 256;
-static_assert(kSmemBytes <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
+constexpr size_t kMaxSmem = 227 * 1024;
+constexpr size_t kFixedSmem = 1024 + 256;  // alignment of the stages, barriers
 
+// K blocks that kLoss sums in the tensor core before the epilogue adds them up in
+// registers: the tensor core drops the low bits of every step's sum (448 steps
+// at K = 7168 put the logsumexp 1e-6 off), fp32 additions round them.
+constexpr int kSegment = 32;
 constexpr int kGroupM = 8;      // row tiles that share the column tiles of a wave
 constexpr int kSmallRows = 128;  // up to here the loss reads hidden where it lies
 constexpr int kMaxSplits = 16;
@@ -63,14 +65,17 @@ struct GemmArgs {
   int tp, W, vocab, K;
   int c0, wc, wcols;  // the piece: first column, its width in prob, its columns
   int bn;             // columns of a vocabulary tile (kLoss, kProb)
-  int a_rows;         // rows of a tile's A that are loaded (kLoss, kProb, kDx)
+  int stages;         // K blocks in flight
+  uint32_t a_bytes;   // of one stage in shared memory
+  uint32_t b_bytes;
+  uint32_t load_bytes;  // of one stage that the copies of one CTA bring
   uint32_t idesc;
   float c1;           // logit_scale * log2(e)
   Ids targets;        // of the packed rows, or of all
   const float* row_scale;
   const float* row_lse;
   float2* partial;
-  int tiles;          // vocabulary tiles: row length of partial
+  int tiles;          // row length of partial: two halves of each vocabulary tile
   float* hit;
   int splits;         // kDx: parts of the sum over the vocabulary
   int accum_rows;     // rows of one part's slab
@@ -79,8 +84,8 @@ struct GemmArgs {
 };
 
 struct Shared {
-  uint64_t full[kStages];
-  uint64_t empty[kStages];
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint64_t drain;
@@ -122,15 +127,67 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
   return d;
 }
 
+template <int CTAS>
 __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                         uint32_t accumulate) {
+  if constexpr (CTAS == 1)
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrives on the barrier (in both CTAs of a pair) when the MMAs issued so far are done.
+template <int CTAS>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (CTAS == 1)
+    mma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// The same shared-memory object in the pair's first CTA.
+__device__ __forceinline__ uint32_t in_first_cta(const void* p) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+  return a;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A copy of a CTA pair: into this CTA's shared memory, counted on the first CTA's barrier.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* tm, int x, int y,
+                                              uint32_t bar, uint64_t policy) {
   asm volatile(
-      "{\n"
-      " .reg .pred p;\n"
-      " setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
-      "}\n" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "l"(policy)
       : "memory");
 }
 
@@ -173,11 +230,12 @@ struct Tile {
   int kb0, kb1;
 };
 
-template <int KIND>
+template <int KIND, int CTAS>
 struct Work {
+  static constexpr int kRows = kTileM * CTAS;  // rows of a tile of the pair
   int mt, nt, total, kb, per_shard;
   __device__ __forceinline__ Work(const GemmArgs& a, int rows) {
-    const int row_tiles = (rows + kTileM - 1) / kTileM;
+    const int row_tiles = (rows + kRows - 1) / kRows;
     const int k_tiles = (a.K + kTileN - 1) / kTileN;
     if (KIND == kLoss || KIND == kProb) {
       per_shard = (a.wcols + a.bn - 1) / a.bn;
@@ -192,12 +250,16 @@ struct Work {
       kb = a.tp * per_shard;
       total = mt * nt * a.splits;
     } else {
-      per_shard = (a.wcols + kTileM - 1) / kTileM;
+      per_shard = (a.wcols + kRows - 1) / kRows;
       mt = a.tp * per_shard;
       nt = k_tiles;
       kb = (rows + kBlockK - 1) / kBlockK;
       total = mt * nt;
     }
+  }
+  // Parts of a tile's sum over K that the epilogue adds up.
+  __device__ __forceinline__ int segments() const {
+    return KIND == kLoss ? (kb + kSegment - 1) / kSegment : 1;
   }
   __device__ __forceinline__ Tile at(const GemmArgs& a, int i) const {
     Tile t;
@@ -230,171 +292,211 @@ struct Work {
   }
 };
 
-template <int KIND, typename T>
+// One CTA (CTAS 1) or a pair (CTAS 2) takes tiles i, i + units, ... A pair's tile
+// is 256 x 256: each CTA holds 128 rows of A and 128 columns of B, one thread
+// of the first issues MMAs that read both, and each CTA's tensor memory holds
+// its 128 rows of the sum.
+template <int KIND, int CTAS, typename T>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  unsigned char* sA = base;
-  unsigned char* sB = sA + (size_t)kStages * kABytes;
-  unsigned char* sOut = sB + (size_t)kStages * kBBytes;
-  Shared* sh = reinterpret_cast<Shared*>(sOut + 4 * 2 * kStageOut);
+  const uint32_t stage_bytes = a.a_bytes + a.b_bytes;
+  unsigned char* sOut = base + (size_t)a.stages * stage_bytes;
+  Shared* sh = reinterpret_cast<Shared*>(sOut + (KIND == kLoss ? 0 : kEpilogueWarps * kStageOut));
   const int warp = (int)threadIdx.x >> 5;
   const int lane = (int)threadIdx.x & 31;
+  const int rank = CTAS == 2 ? (int)cta_rank() : 0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < a.stages; ++s) {
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh->acc_full[b], 1);
-      mbar_init(&sh->acc_empty[b], 4);
+      mbar_init(&sh->acc_empty[b], kEpilogueWarps * CTAS);
     }
     mbar_init(&sh->drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&sh->tmem_base)),
-                 "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (CTAS == 1) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&sh->tmem_base)),
+                   "r"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&sh->tmem_base)),
+                   "r"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
 
   const int packed = a.count ? *a.count : a.rows;  // rows that count
   // At least one row tile is made, so that a piece without rows comes out as zeros.
-  const Work<KIND> work(a, packed > 0 ? packed : 1);
-  const int G = (int)gridDim.x;
+  const Work<KIND, CTAS> work(a, packed > 0 ? packed : 1);
+  const int units = (int)gridDim.x / CTAS;
+  const int unit = (int)blockIdx.x / CTAS;
+  const int row0 = rank * kTileM;             // of this CTA in a tile
+  constexpr int kCols = kTileN / CTAS;        // columns of B in this CTA
 
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t keep = policy_evict_normal();
-      const uint32_t bytes = KIND == kDw ? kABytes + kBBytes
-                             : KIND == kDx
-                                 ? (uint32_t)a.a_rows * 128 + kBBytes
-                                 : (uint32_t)(a.a_rows + a.bn) * 128;
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int i = blockIdx.x; i < work.total && ok; i += G) {
+      for (int i = unit; i < work.total && ok; i += units) {
         const Tile t = work.at(a, i);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
           if (!wait_phase(&sh->empty[stage], phase ^ 1u, a.status)) { ok = false; break; }
           uint64_t* bar = &sh->full[stage];
-          unsigned char* A = sA + (size_t)stage * kABytes;
-          unsigned char* B = sB + (size_t)stage * kBBytes;
-          mbar_expect_tx(bar, bytes);
+          unsigned char* A = base + (size_t)stage * stage_bytes;
+          unsigned char* B = A + a.a_bytes;
+          if (rank == 0) mbar_expect_tx(bar, a.load_bytes * CTAS);
+          auto load = [&](unsigned char* dst, const CUtensorMap* tm, int x, int y) {
+            if constexpr (CTAS == 1)
+              tma_load_2d(dst, tm, x, y, bar, keep);
+            else
+              tma_load_pair(dst, tm, x, y, in_first_cta(bar), keep);
+          };
           if (KIND == kLoss || KIND == kProb) {
-            tma_load_2d(A, &a.x, kb * kBlockK, t.m * kTileM, bar, keep);
-            tma_load_2d(B, &a.shard[t.r], kb * kBlockK, a.c0 + t.n * a.bn, bar, keep);
+            load(A, &a.x, kb * kBlockK, t.m * work.kRows + row0);
+            load(B, &a.shard[t.r], kb * kBlockK, a.c0 + t.n * a.bn + rank * kCols);
           } else if (KIND == kDx) {
             const int r = kb / work.per_shard;
             const int b = kb - r * work.per_shard;
-            tma_load_2d(A, &a.p, r * a.wc + b * kBlockK, t.m * kTileM, bar, keep);
-            for (int j = 0; j < kTileN / 64; ++j)
-              tma_load_2d(B + j * kBox, &a.shard[r], t.n * kTileN + j * 64, a.c0 + b * kBlockK,
-                          bar, keep);
+            load(A, &a.p, r * a.wc + b * kBlockK, t.m * work.kRows + row0);
+#pragma unroll
+            for (int j = 0; j < kCols / 64; ++j)
+              load(B + j * kBox, &a.shard[r], t.n * kTileN + rank * kCols + j * 64,
+                   a.c0 + b * kBlockK);
           } else {
+#pragma unroll
             for (int j = 0; j < kTileM / 64; ++j)
-              tma_load_2d(A + j * kBox, &a.p, t.r * a.wc + t.m * kTileM + j * 64, kb * kBlockK,
-                          bar, keep);
-            for (int j = 0; j < kTileN / 64; ++j)
-              tma_load_2d(B + j * kBox, &a.x, t.n * kTileN + j * 64, kb * kBlockK, bar, keep);
+              load(A + j * kBox, &a.p, t.r * a.wc + t.m * work.kRows + row0 + j * 64,
+                   kb * kBlockK);
+#pragma unroll
+            for (int j = 0; j < kCols / 64; ++j)
+              load(B + j * kBox, &a.x, t.n * kTileN + rank * kCols + j * 64, kb * kBlockK);
           }
           ++issued;
-          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+          if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
       }
       // Every copy issued must land before the CTA's shared memory goes: fill j
-      // completes the phase of parity (j / kStages) & 1 of stage j % kStages.
-      const int last = issued - 1;
-      for (int s = 0; s < kStages && s <= last; ++s) {
-        const int j = last - (last - s) % kStages;
-        wait_phase(&sh->full[s], (uint32_t)((j / kStages) & 1), a.status);
+      // completes the phase of parity (j / stages) & 1 of stage j % stages (of a
+      // pair, on the first CTA's barriers; the second waits for it at the end).
+      const int last = rank == 0 ? issued - 1 : -1;
+      for (int s = 0; s < a.stages && s <= last; ++s) {
+        const int j = last - (last - s) % a.stages;
+        wait_phase(&sh->full[s], (uint32_t)((j / a.stages) & 1), a.status);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int i = blockIdx.x; i < work.total && ok; i += G) {
+      for (int i = unit; i < work.total && ok; i += units) {
         const Tile t = work.at(a, i);
-        if (!wait_phase(&sh->acc_empty[acc], acc_phase ^ 1u, a.status)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(acc * kTileN);
-        for (int kb = t.kb0; kb < t.kb1; ++kb) {
-          if (!wait_phase(&sh->full[stage], phase, a.status)) { ok = false; break; }
+        int kb = t.kb0;
+        while (kb < t.kb1) {
+          const int end = KIND == kLoss && kb + kSegment < t.kb1 ? kb + kSegment : t.kb1;
+          if (!wait_phase(&sh->acc_empty[acc], acc_phase ^ 1u, a.status)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t A = smem_u32(sA + (size_t)stage * kABytes);
-          const uint32_t B = smem_u32(sB + (size_t)stage * kBBytes);
-          const uint64_t da = KIND == kDw ? smem_desc_mn(A) : smem_desc_sw128(A);
-          const uint64_t db = KIND == kDw || KIND == kDx ? smem_desc_mn(B) : smem_desc_sw128(B);
-          // A step of 16 k: 32 bytes along a K-contiguous row, or 16 rows of 128
-          // bytes of an operand with one row per k (the address field counts 16).
-          constexpr uint64_t step_a = KIND == kDw ? 128 : 2;
-          constexpr uint64_t step_b = KIND == kDw || KIND == kDx ? 128 : 2;
+          const uint32_t d = tmem + (uint32_t)(acc * kTileN);
+          for (uint32_t accumulate = 0; kb < end; ++kb) {
+            if (!wait_phase(&sh->full[stage], phase, a.status)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t A = smem_u32(base) + (uint32_t)stage * stage_bytes;
+            const uint32_t B = A + a.a_bytes;
+            const uint64_t da = KIND == kDw ? smem_desc_mn(A) : smem_desc_sw128(A);
+            const uint64_t db = KIND == kDw || KIND == kDx ? smem_desc_mn(B) : smem_desc_sw128(B);
+            // A step of 16 k: 32 bytes along a K-contiguous row, or 16 rows of 128
+            // bytes of an operand with one row per k (the address field counts 16).
+            constexpr uint64_t step_a = KIND == kDw ? 128 : 2;
+            constexpr uint64_t step_b = KIND == kDw || KIND == kDx ? 128 : 2;
 #pragma unroll
-          for (int k = 0; k < kBlockK / kMmaK; ++k)
-            mma_f16(d, da + step_a * k, db + step_b * k, a.idesc,
-                    (kb != t.kb0 || k != 0) ? 1u : 0u);
-          mma_commit(&sh->empty[stage]);
-          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+            for (int k = 0; k < kBlockK / kMmaK; ++k) {
+              mma_f16<CTAS>(d, da + step_a * k, db + step_b * k, a.idesc, accumulate);
+              accumulate = 1;
+            }
+            commit<CTAS>(&sh->empty[stage]);
+            if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+          }
+          if (!ok) break;
+          commit<CTAS>(&sh->acc_full[acc]);
+          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
-        if (!ok) break;
-        mma_commit(&sh->acc_full[acc]);
-        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
       // Every MMA issued must complete before the tensor memory is freed.
-      mma_commit(&sh->drain);
+      commit<CTAS>(&sh->drain);
       wait_phase(&sh->drain, 0, a.status);
     }
   } else {
+    // Warps w and w + 4 share 32 rows and take half of the columns each.
     const int quarter = warp & 3;
-    const int row = quarter * 32 + lane;
-    unsigned char* const stage_out = sOut + (size_t)(warp - 2) * 2 * kStageOut;
-    int acc = 0, buf = 0;
+    const int half = (warp - 2) >> 2;
+    const int first = half * (kTileN / 2);
+    const int row = row0 + quarter * 32 + lane;  // in the tile
+    unsigned char* const stage_out = sOut + (size_t)(warp - 2) * kStageOut;
+    int acc = 0;
     uint32_t acc_phase = 0;
     const float unscale = KIND == kDw ? *a.unscale : 1.f;
     // Staged stores: the warp's 32 rows of 128 bytes, 16-byte column c of row r
     // at c ^ (r & 7), the 128-byte swizzle of the tensor map.
     auto store_begin = [&]() {
-      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       __syncwarp();
-      return stage_out + (size_t)buf * kStageOut + (size_t)lane * 128;
+      return stage_out + (size_t)lane * 128;
     };
     auto store_end = [&](const CUtensorMap* tm, int x, int y, bool add) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        const void* src = stage_out + (size_t)buf * kStageOut;
         if (add)
-          tma_add_2d(tm, x, y, src);
+          tma_add_2d(tm, x, y, stage_out);
         else
-          tma_store_2d(tm, x, y, src);
+          tma_store_2d(tm, x, y, stage_out);
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
-      buf ^= 1;
     };
-    for (int i = blockIdx.x; i < work.total; i += G) {
-      const Tile t = work.at(a, i);
+    auto acquire = [&]() {
       const bool ready = wait_phase(&sh->acc_full[acc], acc_phase, a.status);
-      if (!__all_sync(0xffffffffu, ready)) break;
+      if (!__all_sync(0xffffffffu, ready)) return false;
       tc_fence_after();
-      const uint32_t tacc = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kTileN);
-      auto release = [&]() {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->acc_empty[acc]);
-      };
-
+      return true;
+    };
+    auto acc_at = [&](int column) {
+      return tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kTileN + column);
+    };
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CTAS == 1)
+          mbar_arrive(&sh->acc_empty[acc]);
+        else
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                           in_first_cta(&sh->acc_empty[acc]))
+                       : "memory");
+      }
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    };
+    for (int i = unit; i < work.total; i += units) {
+      const Tile t = work.at(a, i);
       if (KIND == kLoss || KIND == kProb) {
-        const int n = t.m * kTileM + row;
+        const int n = t.m * work.kRows + row;
         const bool on = n < packed;
         // Columns of the tile in the real vocabulary, and the row's target in it.
         const int col0 = a.c0 + t.n * a.bn;  // within the shard
@@ -405,43 +507,63 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         if (on) id = load_id(a.targets, (size_t)n) - ((long long)t.r * a.W + col0);
         const int at = id >= 0 && id < valid ? (int)id : -1;
         if (KIND == kLoss) {
+          float v[4][32];
+          const int segments = work.segments();
+          bool ok = true;
+          for (int seg = 0; seg < segments; ++seg) {
+            ok = acquire();
+            if (!ok) break;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (first + q * 32 >= a.bn) continue;
+              uint32_t r[32];
+              tmem_ld_x32(acc_at(first + q * 32), r);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                v[q][j] = seg ? v[q][j] + __uint_as_float(r[j]) : __uint_as_float(r[j]);
+            }
+            release();
+          }
+          if (!ok) break;
           float top = -INFINITY, sum = 0.f;
-          for (int c = 0; c < a.bn; c += 32) {
-            uint32_t v[32];
-            tmem_ld_x32(tacc + (uint32_t)c, v);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int c = first + q * 32;
+            if (c >= a.bn) continue;
             float mx = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const float y = c + j < valid ? __uint_as_float(v[j]) * a.c1 : -INFINITY;
-              v[j] = __float_as_uint(y);
-              mx = fmaxf(mx, y);
+              v[q][j] = c + j < valid ? v[q][j] * a.c1 : -INFINITY;
+              mx = fmaxf(mx, v[q][j]);
             }
             const float now = fmaxf(top, mx);
             // Nothing above -inf yet: ex2(-inf - 0) = 0 adds nothing, and a NaN still shows.
             const float ref = now == -INFINITY ? 0.f : now;
             float part = 0.f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) part += ex2(__uint_as_float(v[j]) - ref);
+            for (int j = 0; j < 32; ++j) part += ex2(v[q][j] - ref);
             sum = sum * ex2(top - ref) + part;
             top = now;
             if (at >= c && at < c + 32) {
               float z = 0.f;
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (at == c + j) z = __uint_as_float(v[j]);
+                if (at == c + j) z = v[q][j];
               a.hit[n] = z;
             }
           }
-          release();
-          if (on && n < a.rows) a.partial[(size_t)n * a.tiles + t.index] = make_float2(top, sum);
+          if (on && n < a.rows)
+            a.partial[(size_t)n * a.tiles + t.index * 2 + half] = make_float2(top, sum);
         } else {
           const float scale = on ? a.row_scale[n] : 0.f;
           const float lse = on ? a.row_lse[n] : 0.f;
-          for (int c = 0; c < a.bn; c += 64) {
+          if (!acquire()) break;
+          if (first >= a.bn) release();
+          for (int c = first; c < a.bn && c < first + kTileN / 2; c += 64) {
             uint32_t v[2][32];
-            tmem_ld_x32(tacc + (uint32_t)c, v[0]);
-            tmem_ld_x32(tacc + (uint32_t)c + 32, v[1]);
-            if (c + 64 >= a.bn) release();
+            tmem_ld_x32(acc_at(c), v[0]);
+            tmem_ld_x32(acc_at(c + 32), v[1]);
+            if (c + 64 >= a.bn || c + 64 == first + kTileN / 2) release();
             if (t.n * a.bn + c >= a.wc) continue;  // beyond the piece's place in prob
             unsigned char* dst = store_begin();
 #pragma unroll
@@ -462,30 +584,32 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
               *reinterpret_cast<uint4*>(dst + ((q ^ (lane & 7)) << 4)) =
                   make_uint4(w[0], w[1], w[2], w[3]);
             }
-            store_end(&a.out, t.r * a.wc + t.n * a.bn + c, t.m * kTileM + quarter * 32, false);
+            store_end(&a.out, t.r * a.wc + t.n * a.bn + c, t.m * work.kRows + row0 + quarter * 32, false);
           }
         }
       } else if (KIND == kDx) {
-        for (int c = 0; c < kTileN; c += 32) {
+        if (!acquire()) break;
+        for (int c = first; c < first + kTileN / 2; c += 32) {
           uint32_t v[32];
-          tmem_ld_x32(tacc + (uint32_t)c, v);
-          if (c + 32 == kTileN) release();
+          tmem_ld_x32(acc_at(c), v);
+          if (c + 32 == first + kTileN / 2) release();
           if (t.n * kTileN + c >= a.K) continue;
           unsigned char* dst = store_begin();
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             *reinterpret_cast<uint4*>(dst + ((q ^ (lane & 7)) << 4)) =
                 make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-          store_end(&a.out, t.n * kTileN + c, t.r * a.accum_rows + t.m * kTileM + quarter * 32,
+          store_end(&a.out, t.n * kTileN + c, t.r * a.accum_rows + t.m * work.kRows + row0 + quarter * 32,
                     a.add != 0);
         }
       } else {
-        for (int c = 0; c < kTileN; c += 64) {
+        if (!acquire()) break;
+        for (int c = first; c < first + kTileN / 2; c += 64) {
           uint32_t v[2][32];
-          tmem_ld_x32(tacc + (uint32_t)c, v[0]);
-          tmem_ld_x32(tacc + (uint32_t)c + 32, v[1]);
-          if (c + 64 == kTileN) release();
-          const int y = a.c0 + t.m * kTileM + quarter * 32;
+          tmem_ld_x32(acc_at(c), v[0]);
+          tmem_ld_x32(acc_at(c + 32), v[1]);
+          if (c + 64 == first + kTileN / 2) release();
+          const int y = a.c0 + t.m * work.kRows + row0 + quarter * 32;
           if (t.n * kTileN + c >= a.K || y >= a.W) continue;
           unsigned char* dst = store_begin();
 #pragma unroll
@@ -503,19 +627,25 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           store_end(&a.shard[t.r], t.n * kTileN + c, y, a.add != 0);
         }
       }
-      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
+  // A pair leaves together: copies, MMAs and arrivals of one CTA reach into the other.
   tc_fence_before();
   __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync();
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(kTmemCols)
-                 : "memory");
+    if constexpr (CTAS == 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(kTmemCols)
+                   : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(kTmemCols)
+                   : "memory");
   }
 }
 
@@ -667,44 +797,56 @@ struct MergeArgs {
   const int* count;  // packed rows (nullptr: the rows are the caller's own)
   const int* row_of;
   Ids targets;
-  int rows, vocab;
+  int vocab;
   float* loss;
   float* lse;
 };
 
-// Joins the tiles' statistics of a row: one warp per row.
-__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ MergeArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int rows = a.count ? *a.count : a.rows;
-  const int step = gridDim.x * 8;
-  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += step) {
-    const float2* p = a.partial + (size_t)i * a.tiles;
-    float top = -INFINITY, sum = 0.f;
-    for (int t = lane; t < a.tiles; t += 32) {
-      const float2 x = p[t];
-      const float now = fmaxf(top, x.x);
-      const float ref = now == -INFINITY ? 0.f : now;
-      sum = sum * ex2(top - ref) + x.y * ex2(x.x - ref);
-      top = now;
+__device__ __forceinline__ void join_stats(float& top, float& sum, float t, float s) {
+  const float now = fmaxf(top, t);
+  const float ref = now == -INFINITY ? 0.f : now;
+  sum = sum * ex2(top - ref) + s * ex2(t - ref);
+  top = now;
+}
+
+// Joins the tiles' statistics of a row: one CTA per row, so that a single row's
+// hundreds of tiles are read at once.
+constexpr int kMergeThreads = 128;
+
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ MergeArgs a) {
+  __shared__ float2 joined[kMergeThreads / 32];
+  const int i = blockIdx.x;
+  if (a.count && i >= *a.count) return;
+  const float2* p = a.partial + (size_t)i * a.tiles;
+  float top = -INFINITY, sum = 0.f;
+  for (int t0 = threadIdx.x; t0 < a.tiles; t0 += 4 * kMergeThreads) {
+    float2 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = t0 + j * kMergeThreads;
+      x[j] = t < a.tiles ? p[t] : make_float2(-INFINITY, 0.f);
     }
-    for (int o = 16; o; o >>= 1) {
-      const float t = __shfl_xor_sync(0xffffffffu, top, o);
-      const float s = __shfl_xor_sync(0xffffffffu, sum, o);
-      const float now = fmaxf(top, t);
-      const float ref = now == -INFINITY ? 0.f : now;
-      sum = sum * ex2(top - ref) + s * ex2(t - ref);
-      top = now;
-    }
-    if (lane) continue;
-    const long long id = load_id(a.targets, i);
-    const int n = a.count ? a.row_of[i] : i;
-    const bool masked = !a.count && id < 0;
-    const float rest = log2f(sum);
-    // The difference to the largest logit first: it is exact where they are near.
-    const float loss = id >= 0 && id < a.vocab ? (top - a.hit[i] + rest) * kLn2 : NAN;
-    a.loss[n] = masked ? 0.f : loss;
-    a.lse[n] = masked ? 0.f : (top + rest) * kLn2;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) join_stats(top, sum, x[j].x, x[j].y);
   }
+  for (int o = 16; o; o >>= 1) {
+    const float t = __shfl_xor_sync(0xffffffffu, top, o);
+    const float s = __shfl_xor_sync(0xffffffffu, sum, o);
+    join_stats(top, sum, t, s);
+  }
+  if ((threadIdx.x & 31) == 0) joined[threadIdx.x >> 5] = make_float2(top, sum);
+  __syncthreads();
+  if (threadIdx.x) return;
+#pragma unroll
+  for (int w = 1; w < kMergeThreads / 32; ++w) join_stats(top, sum, joined[w].x, joined[w].y);
+  const long long id = load_id(a.targets, i);
+  const int n = a.count ? a.row_of[i] : i;
+  const bool masked = !a.count && id < 0;
+  const float rest = log2f(sum);
+  // The difference to the largest logit first: it is exact where they are near.
+  const float loss = id >= 0 && id < a.vocab ? (top - a.hit[i] + rest) * kLn2 : NAN;
+  a.loss[n] = masked ? 0.f : loss;
+  a.lse[n] = masked ? 0.f : (top + rest) * kLn2;
 }
 
 struct FinishArgs {
@@ -787,38 +929,77 @@ bool encode_weights(const hg_vocab& h, const void* const* w, uint32_t box_rows, 
 // B bf16 (1) or fp16 (0) (bits 7-9, 10-12), A and B transposed (bits 15, 16:
 // their M or N dimension is contiguous), N >> 3 in bits 17-22, M >> 4 in bits
 // 24-28.
-uint32_t instruction(int dtype, bool a_mn, bool b_mn, int n) {
+uint32_t instruction(int dtype, bool a_mn, bool b_mn, int m, int n) {
   const uint32_t type = dtype == HG_BF16 ? 1u : 0u;
   return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-template <int KIND, typename T>
-cudaError_t launch_as(const GemmArgs& a, int ctas, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(gemm_kernel<KIND, T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)kSmemBytes);
+// How one product is cut: a pair of CTAs or one, the rows of A and columns of B
+// that a CTA loads per stage.
+struct Shape {
+  int ctas = 2;
+  int a_rows = kTileM;
+  int b_cols = kTileN / 2;
+};
+
+template <int KIND, int CTAS, typename T>
+cudaError_t launch_as(const GemmArgs& a, int sms, cudaStream_t stream) {
+  auto* kernel = gemm_kernel<KIND, CTAS, T>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)kMaxSmem);
   if (e != cudaSuccess) return e;
-  gemm_kernel<KIND, T><<<(unsigned)ctas, kThreads, kSmemBytes, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sms / CTAS * CTAS));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kMaxSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CTAS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 template <int KIND>
-cudaError_t launch(const hg_vocab& h, const GemmArgs& a, cudaStream_t stream) {
-  return h.dtype == HG_BF16 ? launch_as<KIND, __nv_bfloat16>(a, h.sms, stream)
-                            : launch_as<KIND, __half>(a, h.sms, stream);
+cudaError_t launch(const hg_vocab& h, const Shape& shape, GemmArgs& a, cudaStream_t stream) {
+  a.a_bytes = (uint32_t)round_up(shape.a_rows * 128, 1024);
+  a.b_bytes = (uint32_t)shape.b_cols * 128;
+  a.load_bytes = (uint32_t)(shape.a_rows + shape.b_cols) * 128;
+  const size_t room = kMaxSmem - kFixedSmem - (KIND == kLoss ? 0 : kEpilogueWarps * kStageOut);
+  const size_t stages = room / (a.a_bytes + a.b_bytes);
+  a.stages = (int)(stages < kMaxStages ? stages : kMaxStages);
+  const bool bf16 = h.dtype == HG_BF16;
+  if (KIND == kDw || shape.ctas == 2)
+    return bf16 ? launch_as<KIND, 2, __nv_bfloat16>(a, h.sms, stream)
+                : launch_as<KIND, 2, __half>(a, h.sms, stream);
+  constexpr int kOne = KIND == kDw ? 2 : 1;  // kDw is never made by one CTA
+  return bf16 ? launch_as<KIND, kOne, __nv_bfloat16>(a, h.sms, stream)
+              : launch_as<KIND, kOne, __half>(a, h.sms, stream);
 }
 
-// Rows of A that a tile loads when all rows fit in one tile: the tile's other
-// rows keep what shared memory held, and only reach output rows nobody reads.
-int rows_loaded(int N) { return N >= kTileM ? kTileM : (int)round_up(N > 0 ? N : 1, 8); }
+// The shape of a product whose rows are the call's N: for few rows one CTA per
+// tile, which then holds all of them, and loads no more of A than there are
+// (the tile's other rows keep what shared memory held, and only reach output rows
+// nobody reads).
+Shape row_shape(int N, int columns) {
+  Shape s;
+  if (N > kSmallRows) return s;
+  s.ctas = 1;
+  s.a_rows = (int)round_up(N > 0 ? N : 1, 8);
+  s.b_cols = columns;
+  return s;
+}
 
 // Width of the vocabulary tiles: kTileN, but for few rows, where reading the
 // weights bounds the call, the width that leaves the busiest SM the fewest bytes
 // (a tile also reads the rows, from L2: counted as half).
 int tile_width(const hg_vocab& h, int N, int cols, int step) {
   if (N > kSmallRows) return kTileN;
-  const int rows = rows_loaded(N);
+  const int rows = (int)round_up(N > 0 ? N : 1, 8);
   int best = kTileN;
   long long least = -1;
   for (int bn = kTileN; bn >= step; bn -= step) {
@@ -835,18 +1016,25 @@ int tile_width(const hg_vocab& h, int N, int cols, int step) {
 // Parts of the sum over the vocabulary in kDx: the number that keeps the SMs
 // busiest, by at least 3 % over a smaller one.
 int dx_splits(const hg_vocab& h, int N) {
-  const long long tiles = div_up(N > 0 ? N : 1, kTileM) * div_up(h.K, kTileN);
+  const int ctas = row_shape(N, kTileN).ctas;
+  const long long tiles = div_up(N > 0 ? N : 1, kTileM * ctas) * div_up(h.K, kTileN);
+  const long long units = h.sms / ctas;
   const long long kb = real_shards(h) * div_up(h.piece_cols < h.W ? h.piece_cols : h.W, kBlockK);
   int best = 1;
   double least = 0;
   for (int s = 1; s <= kMaxSplits && s <= kb; ++s) {
-    const double cost = (double)div_up(tiles * s, h.sms) / s;
+    const double cost = (double)div_up(tiles * s, units) / s;
     if (s == 1 || cost < 0.97 * least) {
       least = cost;
       best = s;
     }
   }
   return best;
+}
+
+// Rows of one of kDx's slabs: whole tiles.
+int slab_rows(int N) {
+  return (int)round_up(N > 0 ? N : 1, kTileM * row_shape(N, kTileN).ctas);
 }
 
 unsigned row_blocks(const hg_vocab& h, int N) {
@@ -903,19 +1091,19 @@ long long loss_partials(const hg_vocab& h) {
   // Few rows have the narrowest tiles (tile_width steps by 32).
   const long long few = (h.max_rows < kSmallRows ? h.max_rows : kSmallRows) * div_up(h.W, 32);
   const long long many = h.max_rows * div_up(h.W, kTileN);
-  return h.tp * (few > many ? few : many);
+  return 2ll * h.tp * (few > many ? few : many);
 }
 
 long long loss_rows_pad(long long rows) { return round_up(rows, 256); }
 
 long long loss_accum_rows(const hg_vocab& h) {
   long long most = 0;
-  for (long long n = 1; n <= h.max_rows + kTileM; n += kTileM) {
+  for (long long n = kTileM;; n += kTileM) {
     const int N = (int)(n < h.max_rows ? n : h.max_rows);
-    const long long rows = (long long)dx_splits(h, N) * round_up(N, kTileM);
+    const long long rows = (long long)dx_splits(h, N) * slab_rows(N);
     if (rows > most) most = rows;
+    if (n >= h.max_rows) return most;
   }
-  return most;
 }
 
 cudaError_t loss(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
@@ -923,11 +1111,11 @@ cudaError_t loss(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
   const bool pack = c.N > kSmallRows;
   a.wcols = h.W;
   a.bn = tile_width(h, c.N, h.W, 32);
-  a.a_rows = pack ? kTileM : rows_loaded(c.N);
+  const Shape shape = row_shape(c.N, a.bn);
   a.tp = real_shards(h);
-  a.tiles = (int)(a.tp * div_up(h.W, a.bn));
-  a.idesc = instruction(h.dtype, false, false, a.bn);
-  if (!encode_weights(h, c.weight, a.bn, a.shard)) return cudaErrorInvalidValue;
+  a.tiles = (int)(2 * a.tp * div_up(h.W, a.bn));
+  a.idesc = instruction(h.dtype, false, false, kTileM * shape.ctas, a.bn);
+  if (!encode_weights(h, c.weight, shape.b_cols, a.shard)) return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   MergeArgs m = {};
   if (pack) {
@@ -943,26 +1131,24 @@ cudaError_t loss(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
     m.row_of = h.row_of;
   } else {
     a.targets = c.targets;
-    if (!encode(&a.x, c.hidden, h.dtype, c.N, h.K, c.ld, a.a_rows)) return cudaErrorInvalidValue;
+    if (!encode(&a.x, c.hidden, h.dtype, c.N, h.K, c.ld, shape.a_rows))
+      return cudaErrorInvalidValue;
   }
-  e = launch<kLoss>(h, a, stream);
+  e = launch<kLoss>(h, shape, a, stream);
   if (e != cudaSuccess) return e;
   m.partial = h.partial;
   m.tiles = a.tiles;
   m.hit = h.hit;
   m.targets = a.targets;
-  m.rows = c.N;
   m.vocab = h.vocab;
   m.loss = c.loss;
   m.lse = c.lse_out;
-  merge_kernel<<<(unsigned)div_up(c.N, 8), 256, 0, stream>>>(m);
+  merge_kernel<<<(unsigned)c.N, kMergeThreads, 0, stream>>>(m);
   return cudaGetLastError();
 }
 
 cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
   const long long pad = loss_rows_pad(c.N > 0 ? c.N : 1);
-  const bool small = c.N <= kSmallRows;
-  const int a_rows = small ? rows_loaded(c.N) : kTileM;
   PackArgs p = pack_args(h, c);
   p.grad = 1;
   p.headroom = h.dtype == HG_FP16 ? 14 : 0;  // |d| < 2^14 * 2, small terms kept off fp16's floor
@@ -975,29 +1161,31 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
   prob.count = h.count;
   prob.targets = Ids{h.target, 4};
   prob.wc = h.piece_cols;
-  prob.a_rows = a_rows;
   GemmArgs dx = prob, dw = prob;
   const uint64_t prob_cols = (uint64_t)h.tp * h.piece_cols;
   const int first = h.piece_cols < h.W ? h.piece_cols : h.W;
   prob.bn = tile_width(h, c.N, first, 64);
-  prob.idesc = instruction(h.dtype, false, false, prob.bn);
-  if (!encode_weights(h, c.weight, prob.bn, prob.shard) ||
-      !encode(&prob.x, h.packed, h.dtype, pad, h.K, h.K, a_rows) ||
+  const Shape prob_shape = row_shape(c.N, prob.bn);
+  const Shape dx_shape = row_shape(c.N, kTileN);
+  const Shape dw_shape;
+  prob.idesc = instruction(h.dtype, false, false, kTileM * prob_shape.ctas, prob.bn);
+  if (!encode_weights(h, c.weight, prob_shape.b_cols, prob.shard) ||
+      !encode(&prob.x, h.packed, h.dtype, pad, h.K, h.K, prob_shape.a_rows) ||
       !encode(&prob.out, h.prob, h.dtype, pad, prob_cols, prob_cols, 32))
     return cudaErrorInvalidValue;
   int splits = 1;
   if (c.grad_hidden) {
-    dx.idesc = instruction(h.dtype, false, true, kTileN);
+    dx.idesc = instruction(h.dtype, false, true, kTileM * dx_shape.ctas, kTileN);
     dx.tp = real_shards(h);  // 0 * NaN of a padding shard must not be summed
     splits = dx_splits(h, c.N);
-    dx.accum_rows = (int)round_up(c.N > 0 ? c.N : 1, kTileM);
+    dx.accum_rows = slab_rows(c.N);
     if (!encode_weights(h, c.weight, kBlockK, dx.shard) ||
-        !encode(&dx.p, h.prob, h.dtype, pad, prob_cols, prob_cols, a_rows) ||
+        !encode(&dx.p, h.prob, h.dtype, pad, prob_cols, prob_cols, dx_shape.a_rows) ||
         !encode(&dx.out, h.accum, HG_FP32, (uint64_t)splits * dx.accum_rows, h.K, h.K, 32))
       return cudaErrorInvalidValue;
   }
   if (c.grad_weight) {
-    dw.idesc = instruction(h.dtype, true, true, kTileN);
+    dw.idesc = instruction(h.dtype, true, true, kTileM * dw_shape.ctas, kTileN);
     dw.add = c.accumulate;
     for (int r = 0; r < h.tp; ++r)
       if (!encode(&dw.shard[r], c.grad_weight[r], h.dtype, h.W, h.K, h.K, 32))
@@ -1010,15 +1198,15 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
     const int left = h.W - c0;
     prob.c0 = dx.c0 = dw.c0 = c0;
     prob.wcols = dx.wcols = dw.wcols = left < h.piece_cols ? left : h.piece_cols;
-    e = launch<kProb>(h, prob, stream);
+    e = launch<kProb>(h, prob_shape, prob, stream);
     if (e == cudaSuccess && c.grad_hidden) {
       dx.add = c0 > 0;
       // A short last piece may have fewer K blocks than parts: each part has one.
       const int kb = dx.tp * (int)div_up(dx.wcols, kBlockK);
       dx.splits = splits < kb ? splits : kb;
-      e = launch<kDx>(h, dx, stream);
+      e = launch<kDx>(h, dx_shape, dx, stream);
     }
-    if (e == cudaSuccess && c.grad_weight) e = launch<kDw>(h, dw, stream);
+    if (e == cudaSuccess && c.grad_weight) e = launch<kDw>(h, dw_shape, dw, stream);
     if (e != cudaSuccess) return e;
   }
   if (!c.grad_hidden || c.N == 0) return cudaSuccess;
