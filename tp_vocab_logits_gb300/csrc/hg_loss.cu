@@ -99,12 +99,27 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// One bounded try: the thread sleeps until the phase completes or about 20 us pass.
+__device__ __forceinline__ bool try_phase(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      " .reg .pred p;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n"
+      " selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait for a phase, bounded in time: on expiry the status word is set and the
 // kernel's roles stop issuing work.
 __device__ bool wait_phase(uint64_t* bar, uint32_t parity, int* status) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (try_phase(bar, parity)) return true;
   const unsigned long long t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!try_phase(bar, parity)) {
     if (globaltimer_ns() - t0 > kTimeoutNs) {
       atomicExch(status, 1);
       return false;
@@ -669,6 +684,7 @@ struct PackArgs {
   size_t ld_grad;
   int headroom;  // the largest |row_scale| is brought below 2^headroom (0: kept as it is)
   void* packed;
+  int pitch;
   int* count;
   float* unscale;
   int* row_of;
@@ -681,7 +697,9 @@ __device__ __forceinline__ bool unmasked(const PackArgs& a, long long id) {
   return id >= 0 && (!a.grad || id < a.vocab);
 }
 
-// Copies the unmasked rows of hidden together, in order. CTA b has the rows
+// Copies the unmasked rows of hidden together, in order, each to the start of a
+// 128-byte line: TMA fetches a row of a box that straddles two lines twice (at
+// K = 1000, 512 rows, V = 49999 the loss took 82 us, against 57 us at K = 1024). CTA b has the rows
 // [b * N / G, (b + 1) * N / G); each CTA counts the unmasked rows before its own
 // from the targets (a few bytes per row from L2, against K elements copied), so
 // the CTAs need nothing from one another. The rows up to the next multiple of
@@ -756,7 +774,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constan
     if (keep) {
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.hidden) +
                                                         (size_t)n * a.ld);
-      uint4* dst = packed + (size_t)to * vecs;
+      uint4* dst = packed + (size_t)to * (a.pitch / 8);
       for (int v = lane; v < vecs; v += 128) {
         uint4 x[4];
 #pragma unroll
@@ -787,7 +805,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constan
   }
   const int end = (int)round_up(all > 0 ? all : 1, 64);
   for (int to = all + (int)blockIdx.x * kPackWarps + warp; to < end; to += (int)G * kPackWarps)
-    for (int v = lane; v < vecs; v += 32) packed[(size_t)to * vecs + v] = zero;
+    for (int v = lane; v < vecs; v += 32) packed[(size_t)to * (a.pitch / 8) + v] = zero;
 }
 
 struct MergeArgs {
@@ -851,7 +869,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
 
 struct FinishArgs {
   const float* accum;
-  int splits, accum_rows, K;
+  int splits, accum_rows, K, pitch;
   const int* count;
   const int* row_of;
   const float* unscale;
@@ -871,7 +889,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
     float s[8] = {};
     for (int p = 0; p < a.splits; ++p) {
       const float4* src = reinterpret_cast<const float4*>(
-          a.accum + ((size_t)p * a.accum_rows + row) * a.K + (size_t)v * 8);
+          a.accum + ((size_t)p * a.accum_rows + row) * a.pitch + (size_t)v * 8);
       const float4 lo = src[0], hi = src[1];
       s[0] += lo.x; s[1] += lo.y; s[2] += lo.z; s[3] += lo.w;
       s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
@@ -1058,6 +1076,7 @@ PackArgs pack_args(const hg_vocab& h, const LossCall& c) {
   a.grad_hidden = c.grad_hidden;
   a.ld_grad = c.ld_grad;
   a.packed = h.packed;
+  a.pitch = h.pitch;
   a.count = h.count;
   a.unscale = h.unscale;
   a.row_of = h.row_of;
@@ -1125,7 +1144,7 @@ cudaError_t loss(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     a.count = h.count;
     a.targets = Ids{h.target, 4};
-    if (!encode(&a.x, h.packed, h.dtype, loss_rows_pad(c.N), h.K, h.K, kTileM))
+    if (!encode(&a.x, h.packed, h.dtype, loss_rows_pad(c.N), h.K, h.pitch, kTileM))
       return cudaErrorInvalidValue;
     m.count = h.count;
     m.row_of = h.row_of;
@@ -1170,7 +1189,7 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
   const Shape dw_shape;
   prob.idesc = instruction(h.dtype, false, false, kTileM * prob_shape.ctas, prob.bn);
   if (!encode_weights(h, c.weight, prob_shape.b_cols, prob.shard) ||
-      !encode(&prob.x, h.packed, h.dtype, pad, h.K, h.K, prob_shape.a_rows) ||
+      !encode(&prob.x, h.packed, h.dtype, pad, h.K, h.pitch, prob_shape.a_rows) ||
       !encode(&prob.out, h.prob, h.dtype, pad, prob_cols, prob_cols, 32))
     return cudaErrorInvalidValue;
   int splits = 1;
@@ -1181,7 +1200,7 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
     dx.accum_rows = slab_rows(c.N);
     if (!encode_weights(h, c.weight, kBlockK, dx.shard) ||
         !encode(&dx.p, h.prob, h.dtype, pad, prob_cols, prob_cols, dx_shape.a_rows) ||
-        !encode(&dx.out, h.accum, HG_FP32, (uint64_t)splits * dx.accum_rows, h.K, h.K, 32))
+        !encode(&dx.out, h.accum, HG_FP32, (uint64_t)splits * dx.accum_rows, h.K, h.pitch, 32))
       return cudaErrorInvalidValue;
   }
   if (c.grad_weight) {
@@ -1191,7 +1210,7 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
       if (!encode(&dw.shard[r], c.grad_weight[r], h.dtype, h.W, h.K, h.K, 32))
         return cudaErrorInvalidValue;
     if (!encode(&dw.p, h.prob, h.dtype, pad, prob_cols, prob_cols, kBlockK) ||
-        !encode(&dw.x, h.packed, h.dtype, pad, h.K, h.K, kBlockK))
+        !encode(&dw.x, h.packed, h.dtype, pad, h.K, h.pitch, kBlockK))
       return cudaErrorInvalidValue;
   }
   for (int c0 = 0; c0 < h.W; c0 += h.piece_cols) {
@@ -1215,6 +1234,7 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
   f.splits = splits;
   f.accum_rows = dx.accum_rows;
   f.K = h.K;
+  f.pitch = h.pitch;
   f.count = h.count;
   f.row_of = h.row_of;
   f.unscale = h.unscale;

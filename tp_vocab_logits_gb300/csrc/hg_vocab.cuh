@@ -35,9 +35,10 @@ struct hg_vocab {
   float* row_lse = nullptr;    // [max_rows] packed row's logsumexp in base 2
   float* hit = nullptr;        // [max_rows] packed row's target logit in base 2
   float2* partial = nullptr;   // [max_rows][vocab tiles] maximum and sum of a tile
-  void* packed = nullptr;      // [rows_pad][K] unmasked rows of hidden
+  int pitch = 0;  // elements between rows of packed and accum: K up to whole 128-byte lines
+  void* packed = nullptr;      // [rows_pad][pitch] unmasked rows of hidden
   void* prob = nullptr;        // [rows_pad][tp * piece_cols] piece of the logits' gradient
-  float* accum = nullptr;      // [splits][rows_pad][K] grad_hidden before rounding
+  float* accum = nullptr;      // [splits][rows_pad][pitch] grad_hidden before rounding
   uint32_t* key[2] = {};       // [max_rows] sorted tokens, and the sort's other buffer
   int* pos[2] = {};            // [max_rows] their positions
   float* runs = nullptr;       // [chunks][2][K] sums of runs that cross a chunk's ends

@@ -45,7 +45,7 @@ size_t lay_out(hg_vocab* h, unsigned char* base) {
     const size_t pad = (size_t)hg::vocab::loss_rows_pad(h->max_rows);
     l.take(h->row_of, n);
     l.take(h->target, n);
-    l.take(h->packed, pad * h->K * e);
+    l.take(h->packed, pad * h->pitch * e);
     if (h->ops & HG_VOCAB_LOSS) {
       l.take(h->hit, n);
       l.take(h->partial, (size_t)hg::vocab::loss_partials(*h));
@@ -54,7 +54,7 @@ size_t lay_out(hg_vocab* h, unsigned char* base) {
       l.take(h->row_scale, n);
       l.take(h->row_lse, n);
       l.take(h->prob, pad * h->tp * (size_t)h->piece_cols * e);
-      l.take(h->accum, (size_t)hg::vocab::loss_accum_rows(*h) * h->K);
+      l.take(h->accum, (size_t)hg::vocab::loss_accum_rows(*h) * h->pitch);
     }
   }
   if (h->ops & HG_VOCAB_EMBED_GRAD) {
@@ -122,6 +122,7 @@ int hg_vocab_create(int tp, int shard_cols, int vocab, int hidden, int max_rows,
   h->W = shard_cols;
   h->vocab = vocab ? vocab : (int)total;
   h->K = hidden;
+  h->pitch = (int)hg::vocab::round_up(hidden, 64);
   h->max_rows = max_rows;
   h->dtype = dtype;
   h->ops = ops;
