@@ -52,6 +52,8 @@ struct EmbedArgs {
 
 template <typename T, int E>
 __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__ EmbedArgs a) {
+  wait_for_predecessor();
+  let_successor_start();
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const long long n = unit / a.units_per_row;
@@ -208,6 +210,8 @@ __device__ void sort_pass(const SortArgs& a, int pass, SortShared* sh, uint32_t*
 }
 
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ SortArgs a) {
+  wait_for_predecessor();
+  let_successor_start();
   extern __shared__ __align__(16) unsigned char smem[];
   SortShared* sh = reinterpret_cast<SortShared*>(smem);
   uint32_t* place = reinterpret_cast<uint32_t*>(sh + 1);
@@ -270,6 +274,8 @@ __device__ __forceinline__ float* run_slot(const SumArgs& a, long long chunk, in
 
 template <typename T, int E, int U>
 __global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ SumArgs a) {
+  wait_for_predecessor();
+  let_successor_start();
   constexpr int kBatch = 8;  // rows whose loads are in flight at once
   using P = Pack<T, E>;
   const int lane = threadIdx.x & 31;
@@ -339,6 +345,8 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ S
 // in adds that chunk's slot 1 and slot 0 of the chunks after it, in order.
 template <typename T, int E, int U>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ SumArgs a) {
+  wait_for_predecessor();
+  let_successor_start();
   constexpr int kBatch = 4;
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -405,8 +413,7 @@ cudaError_t embed_as(const EmbedArgs& args, cudaStream_t stream) {
   a.units_per_row = (int)div_up(a.K / E, kRowAccesses * 32);
   const long long blocks = div_up((long long)a.N * a.units_per_row, kWarps);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  embed_kernel<T, E><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(embed_kernel<T, E>, a, (unsigned)blocks, kThreads, 0, 1, stream);
 }
 
 template <typename T, int E, int U>
@@ -415,9 +422,10 @@ cudaError_t sum_as(const SumArgs& args, cudaStream_t stream) {
   a.slices = (int)div_up(a.K / E, 32 * U);
   const long long blocks = div_up((long long)a.chunks * a.slices, kWarps);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  sum_kernel<T, E, U><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-  join_kernel<T, E, U><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const cudaError_t e =
+      launch_dependent(sum_kernel<T, E, U>, a, (unsigned)blocks, kThreads, 0, 1, stream);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(join_kernel<T, E, U>, a, (unsigned)blocks, kThreads, 0, 1, stream);
 }
 
 cudaError_t sort(const hg_vocab& h, const Ids& tokens, int N, int* sorted, cudaStream_t stream) {
@@ -438,19 +446,7 @@ cudaError_t sort(const hg_vocab& h, const Ids& tokens, int N, int* sorted, cudaS
   cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)sort_smem(kMaxDigitBits));
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kSortCtas);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kSortCtas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sort_kernel, a);
+  return launch_dependent(sort_kernel, a, kSortCtas, kSortThreads, smem, kSortCtas, stream);
 }
 
 }  // namespace

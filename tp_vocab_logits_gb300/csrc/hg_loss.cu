@@ -356,6 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
 
+  wait_for_predecessor();
+  let_successor_start();
   const int packed = a.count ? *a.count : a.rows;  // rows that count
   // At least one row tile is made, so that a piece without rows comes out as zeros.
   const Work<KIND, CTAS> work(a, packed > 0 ? packed : 1);
@@ -709,6 +711,8 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constan
   __shared__ float warp_max[kPackWarps];
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
+  wait_for_predecessor();
+  let_successor_start();
   const long long G = gridDim.x;
   const int lo = (int)(blockIdx.x * (long long)a.N / G);
   const int hi = (int)((blockIdx.x + 1) * (long long)a.N / G);
@@ -833,6 +837,8 @@ constexpr int kMergeThreads = 128;
 
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ MergeArgs a) {
   __shared__ float2 joined[kMergeThreads / 32];
+  wait_for_predecessor();
+  let_successor_start();
   const int i = blockIdx.x;
   if (a.count && i >= *a.count) return;
   const float2* p = a.partial + (size_t)i * a.tiles;
@@ -880,6 +886,8 @@ struct FinishArgs {
 // grad_hidden: the parts' sums in order, rounded once, to the rows they belong to.
 template <typename T>
 __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ FinishArgs a) {
+  wait_for_predecessor();
+  let_successor_start();
   const int vecs = a.K / 8;
   const long long total = (long long)*a.count * vecs;
   const float unscale = *a.unscale;
@@ -967,19 +975,8 @@ cudaError_t launch_as(const GemmArgs& a, int sms, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kMaxSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(sms / CTAS * CTAS));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kMaxSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CTAS;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return launch_dependent(kernel, a, (unsigned)(sms / CTAS * CTAS), kThreads, kMaxSmem, CTAS,
+                          stream);
 }
 
 template <int KIND>
@@ -1139,8 +1136,7 @@ cudaError_t loss(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
   MergeArgs m = {};
   if (pack) {
     const PackArgs p = pack_args(h, c);
-    pack_kernel<<<row_blocks(h, c.N), kPackThreads, 0, stream>>>(p);
-    e = cudaGetLastError();
+    e = launch_dependent(pack_kernel, p, row_blocks(h, c.N), kPackThreads, 0, 1, stream);
     if (e != cudaSuccess) return e;
     a.count = h.count;
     a.targets = Ids{h.target, 4};
@@ -1162,8 +1158,7 @@ cudaError_t loss(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
   m.vocab = h.vocab;
   m.loss = c.loss;
   m.lse = c.lse_out;
-  merge_kernel<<<(unsigned)c.N, kMergeThreads, 0, stream>>>(m);
-  return cudaGetLastError();
+  return launch_dependent(merge_kernel, m, (unsigned)c.N, kMergeThreads, 0, 1, stream);
 }
 
 cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
@@ -1171,8 +1166,8 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
   PackArgs p = pack_args(h, c);
   p.grad = 1;
   p.headroom = h.dtype == HG_FP16 ? 14 : 0;  // |d| < 2^14 * 2, small terms kept off fp16's floor
-  pack_kernel<<<row_blocks(h, c.N), kPackThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e =
+      launch_dependent(pack_kernel, p, row_blocks(h, c.N), kPackThreads, 0, 1, stream);
   if (e != cudaSuccess) return e;
 
   // One argument block per product; only the piece changes between launches.
@@ -1242,11 +1237,9 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
   f.ld = c.ld_grad;
   const long long blocks = div_up((long long)c.N * (h.K / 8), 256);
   const unsigned grid = (unsigned)(blocks < 8ll * h.sms ? blocks : 8ll * h.sms);
-  if (h.dtype == HG_BF16)
-    finish_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(f);
-  else
-    finish_kernel<__half><<<grid, 256, 0, stream>>>(f);
-  return cudaGetLastError();
+  return h.dtype == HG_BF16
+             ? launch_dependent(finish_kernel<__nv_bfloat16>, f, grid, 256, 0, 1, stream)
+             : launch_dependent(finish_kernel<__half>, f, grid, 256, 0, 1, stream);
 }
 
 }  // namespace vocab

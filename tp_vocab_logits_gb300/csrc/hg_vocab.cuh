@@ -97,6 +97,39 @@ struct alignas(sizeof(T) * E) Pack {
   T v[E];
 };
 
+// Programmatic dependent launch: a kernel launched so may start while its
+// predecessor on the stream still runs, and waits for it (and all its writes)
+// here, before its first access to global memory.
+__device__ __forceinline__ void wait_for_predecessor() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Lets the next kernel on the stream start (and get as far as its own wait).
+__device__ __forceinline__ void let_successor_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Launch as a dependent of the kernel before it, in clusters of `cluster` CTAs.
+template <typename Args>
+cudaError_t launch_dependent(void (*kernel)(Args), const Args& args, unsigned grid, unsigned block,
+                             size_t smem, unsigned cluster, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 // Sorted tokens summed as one sequence in embed_grad.
 constexpr int kRunRows = 32;
 
