@@ -368,7 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
   if (warp == 0) {
     if (lane == 0) {
+      // The loss of few rows reads the weights once (evict-first: 1 row at V=163840,
+      // K=7168 342 us, against 359 us with the default policy); every other
+      // operand is read again by other tiles.
       const uint64_t keep = policy_evict_normal();
+      const uint64_t weights = KIND == kLoss && CTAS == 1 ? policy_evict_first() : keep;
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -380,31 +384,34 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           unsigned char* A = base + (size_t)stage * stage_bytes;
           unsigned char* B = A + a.a_bytes;
           if (rank == 0) mbar_expect_tx(bar, a.load_bytes * CTAS);
-          auto load = [&](unsigned char* dst, const CUtensorMap* tm, int x, int y) {
+          auto load = [&](unsigned char* dst, const CUtensorMap* tm, int x, int y,
+                          uint64_t policy) {
             if constexpr (CTAS == 1)
-              tma_load_2d(dst, tm, x, y, bar, keep);
+              tma_load_2d(dst, tm, x, y, bar, policy);
             else
-              tma_load_pair(dst, tm, x, y, in_first_cta(bar), keep);
+              tma_load_pair(dst, tm, x, y, in_first_cta(bar), policy);
           };
           if (KIND == kLoss || KIND == kProb) {
-            load(A, &a.x, kb * kBlockK, t.m * work.kRows + row0);
-            load(B, &a.shard[t.r], kb * kBlockK, a.c0 + t.n * a.bn + rank * kCols);
+            load(A, &a.x, kb * kBlockK, t.m * work.kRows + row0, keep);
+            load(B, &a.shard[t.r], kb * kBlockK, a.c0 + t.n * a.bn + rank * kCols,
+                 weights);
           } else if (KIND == kDx) {
             const int r = kb / work.per_shard;
             const int b = kb - r * work.per_shard;
-            load(A, &a.p, r * a.wc + b * kBlockK, t.m * work.kRows + row0);
+            load(A, &a.p, r * a.wc + b * kBlockK, t.m * work.kRows + row0, keep);
 #pragma unroll
             for (int j = 0; j < kCols / 64; ++j)
               load(B + j * kBox, &a.shard[r], t.n * kTileN + rank * kCols + j * 64,
-                   a.c0 + b * kBlockK);
+                   a.c0 + b * kBlockK, weights);
           } else {
 #pragma unroll
             for (int j = 0; j < kTileM / 64; ++j)
               load(A + j * kBox, &a.p, t.r * a.wc + t.m * work.kRows + row0 + j * 64,
-                   kb * kBlockK);
+                   kb * kBlockK, keep);
 #pragma unroll
             for (int j = 0; j < kCols / 64; ++j)
-              load(B + j * kBox, &a.x, t.n * kTileN + rank * kCols + j * 64, kb * kBlockK);
+              load(B + j * kBox, &a.x, t.n * kTileN + rank * kCols + j * 64, kb * kBlockK,
+                   keep);
           }
           ++issued;
           if (++stage == a.stages) { stage = 0; phase ^= 1u; }
@@ -707,7 +714,8 @@ __device__ __forceinline__ bool unmasked(const PackArgs& a, long long id) {
 // the CTAs need nothing from one another. The rows up to the next multiple of
 // 64 are filled with zeros: kDw sums 64 rows at a time.
 __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constant__ PackArgs a) {
-  __shared__ int warp_sum[3][kPackWarps];
+  __shared__ int warp_sum[2][kPackWarps];
+  __shared__ int kept[kPackWarps];
   __shared__ float warp_max[kPackWarps];
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
@@ -758,37 +766,44 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constan
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const int vecs = a.K / 8;
   uint4* const packed = static_cast<uint4*>(a.packed);
+  // Rows go in rounds of `rows`; the warps share them out evenly, several to a
+  // row where a CTA has few.
+  int per_row = 1;
+  while (per_row < kPackWarps && (hi - lo) * per_row * 2 <= kPackWarps) per_row *= 2;
+  const int rows = kPackWarps / per_row;
+  const int slot = warp / per_row;
+  const int part = (warp - slot * per_row) * 32 + lane;
+  const int step = per_row * 32;
   int at = before;
-  for (int n0 = lo; n0 < hi; n0 += kPackWarps) {
-    // Warp w has row n0 + w; its place follows the unmasked rows of the warps
-    // before it.
-    const int n = n0 + warp;
+  for (int n0 = lo; n0 < hi; n0 += rows) {
+    // Row n0 + slot; its place follows the unmasked rows of the slots before it.
+    const int n = n0 + slot;
     const long long id = n < hi ? load_id(a.targets, n) : -1;
     const bool keep = n < hi && unmasked(a, id);
     __syncthreads();  // the flags of the last round have been read
-    if (lane == 0) warp_sum[2][warp] = keep;
+    if (part == 0) kept[slot] = keep;
     __syncthreads();
     int to = at;
-    for (int w = 0; w < kPackWarps; ++w) {
-      const int f = warp_sum[2][w];
+    for (int w = 0; w < rows; ++w) {
+      const int f = kept[w];
       at += f;
-      if (w < warp) to += f;
+      if (w < slot) to += f;
     }
     if (n >= hi) continue;
     if (keep) {
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.hidden) +
                                                         (size_t)n * a.ld);
       uint4* dst = packed + (size_t)to * (a.pitch / 8);
-      for (int v = lane; v < vecs; v += 128) {
+      for (int v = part; v < vecs; v += 4 * step) {
         uint4 x[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (v + 32 * j < vecs) x[j] = src[v + 32 * j];
+          if (v + step * j < vecs) x[j] = src[v + step * j];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (v + 32 * j < vecs) dst[v + 32 * j] = x[j];
+          if (v + step * j < vecs) dst[v + step * j] = x[j];
       }
-      if (lane == 0) {
+      if (part == 0) {
         a.row_of[to] = n;
         a.target[to] = id < a.vocab ? (int)id : -1;
         if (a.grad) {
@@ -800,9 +815,9 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constan
       if (a.grad_hidden) {
         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.grad_hidden) +
                                               (size_t)n * a.ld_grad);
-        for (int v = lane; v < vecs; v += 32) dst[v] = zero;
+        for (int v = part; v < vecs; v += step) dst[v] = zero;
       }
-    } else if (lane == 0) {
+    } else if (part == 0) {
       a.loss[n] = 0.f;
       a.lse_out[n] = 0.f;
     }
@@ -988,12 +1003,11 @@ cudaError_t launch(const hg_vocab& h, const Shape& shape, GemmArgs& a, cudaStrea
   const size_t stages = room / (a.a_bytes + a.b_bytes);
   a.stages = (int)(stages < kMaxStages ? stages : kMaxStages);
   const bool bf16 = h.dtype == HG_BF16;
-  if (KIND == kDw || shape.ctas == 2)
+  if (shape.ctas == 2)
     return bf16 ? launch_as<KIND, 2, __nv_bfloat16>(a, h.sms, stream)
                 : launch_as<KIND, 2, __half>(a, h.sms, stream);
-  constexpr int kOne = KIND == kDw ? 2 : 1;  // kDw is never made by one CTA
-  return bf16 ? launch_as<KIND, kOne, __nv_bfloat16>(a, h.sms, stream)
-              : launch_as<KIND, kOne, __half>(a, h.sms, stream);
+  return bf16 ? launch_as<KIND, 1, __nv_bfloat16>(a, h.sms, stream)
+              : launch_as<KIND, 1, __half>(a, h.sms, stream);
 }
 
 // The shape of a product whose rows are the call's N: for few rows one CTA per
@@ -1053,8 +1067,7 @@ int slab_rows(int N) {
 }
 
 unsigned row_blocks(const hg_vocab& h, int N) {
-  const long long want = div_up(N, 8);
-  return (unsigned)(want < 1 ? 1 : want < 2 * h.sms ? want : 2 * h.sms);
+  return (unsigned)(N < 1 ? 1 : N < 2 * h.sms ? N : 2 * h.sms);
 }
 
 PackArgs pack_args(const hg_vocab& h, const LossCall& c) {
@@ -1098,6 +1111,7 @@ GemmArgs gemm_args(const hg_vocab& h, const LossCall& c) {
   a.hit = h.hit;
   a.unscale = h.unscale;
   a.splits = 1;
+
   return a;
 }
 
@@ -1181,7 +1195,11 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
   prob.bn = tile_width(h, c.N, first, 64);
   const Shape prob_shape = row_shape(c.N, prob.bn);
   const Shape dx_shape = row_shape(c.N, kTileN);
-  const Shape dw_shape;
+  // Of few rows a tile is a K block or two and a store, and the exchange between the
+  // CTAs of a pair costs more than sharing B saves: 16 rows at V=163840, K=7168
+  // took 382 us by single CTAs, against 480 us.
+  Shape dw_shape = row_shape(c.N, kTileN);
+  dw_shape.a_rows = kTileM;
   prob.idesc = instruction(h.dtype, false, false, kTileM * prob_shape.ctas, prob.bn);
   if (!encode_weights(h, c.weight, prob_shape.b_cols, prob.shard) ||
       !encode(&prob.x, h.packed, h.dtype, pad, h.K, h.pitch, prob_shape.a_rows) ||
