@@ -35,9 +35,9 @@ struct Table {
 };
 
 template <typename T>
-__device__ __forceinline__ T* table_row(const Table& t, long long id, int W, int K) {
-  const long long r = id / W;
-  return static_cast<T*>(t.shard[r]) + (size_t)(id - r * W) * K;
+__device__ __forceinline__ T* table_row(const Table& t, uint32_t id, int W, int K) {
+  const uint32_t r = id / (uint32_t)W;
+  return static_cast<T*>(t.shard[r]) + (size_t)(id - r * (uint32_t)W) * K;
 }
 
 struct EmbedArgs {
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__
   P x[kRowAccesses];
   const long long id = load_id(a.tokens, (size_t)n);
   const bool inside = id >= 0 && id < a.vocab;
-  const P* src = reinterpret_cast<const P*>(table_row<T>(a.table, inside ? id : 0, a.W, a.K));
+  const P* src = reinterpret_cast<const P*>(table_row<T>(a.table, inside ? (uint32_t)id : 0, a.W, a.K));
 #pragma unroll
   for (int j = 0; j < kRowAccesses; ++j) {
     const int i = first + j * 32;
@@ -209,6 +209,8 @@ __device__ void sort_pass(const SortArgs& a, int pass, SortShared* sh, uint32_t*
   cluster.sync();  // every entry moved, every count read
 }
 
+// The successor may start once every CTA here has seen its predecessor complete:
+// clear_kernel relies on that.
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ SortArgs a) {
   wait_for_predecessor();
   let_successor_start();
@@ -218,6 +220,41 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
   for (int p = 0; p < a.passes; ++p) sort_pass(a, p, sh, place);
 }
 
+// ---- zeros where no token points ----------------------------------------------
+
+struct ClearArgs {
+  Table table;
+  size_t bytes;  // of a shard
+  int blocks;    // CTAs of one shard
+};
+
+constexpr int kClearWords = 8;  // of a thread
+
+// Clears the table beside the sort, whose successor it is on the stream: it
+// starts when the sort has started, hence after everything before the sort, and
+// needs nothing of it. It waits for the sort before it ends, so that what waits
+// for this kernel finds both done.
+__global__ void __launch_bounds__(kThreads) clear_kernel(const __grid_constant__ ClearArgs a) {
+  let_successor_start();
+  const int r = (int)blockIdx.x / a.blocks;
+  const int block = (int)blockIdx.x - r * a.blocks;
+  unsigned char* const p = static_cast<unsigned char*>(a.table.shard[r]);
+  // 16-byte words from the first aligned address on; the ends in 16-bit words.
+  size_t head = (16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15;
+  if (head > a.bytes) head = a.bytes;
+  const size_t words = (a.bytes - head) / 16;
+  uint4* const body = reinterpret_cast<uint4*>(p + head);
+  const size_t first = (size_t)block * (kThreads * kClearWords) + threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < kClearWords; ++j)
+    if (first + j * kThreads < words) body[first + j * kThreads] = make_uint4(0, 0, 0, 0);
+  if (block == 0 && threadIdx.x < 16) {
+    const size_t at = threadIdx.x < 8 ? threadIdx.x * 2 : head + words * 16 + (threadIdx.x - 8) * 2;
+    if (at < (threadIdx.x < 8 ? head : a.bytes)) *reinterpret_cast<uint16_t*>(p + at) = 0;
+  }
+  wait_for_predecessor();
+}
+
 // ---- sums over the sorted sequence -------------------------------------------
 
 struct SumArgs {
@@ -225,12 +262,12 @@ struct SumArgs {
   const uint32_t* key;
   const int* pos;
   int N, K, W, vocab;
+  int run_rows;  // rows of a chunk
   int chunks;
   int slices;  // units of columns of one chunk
   const void* grad;
   size_t ld;
   float scale;
-  int accumulate;
   float* runs;
 };
 
@@ -244,9 +281,55 @@ struct Columns {
   }
 };
 
+// Load where `on`, without a branch: between the loads of a batch a branch cost more
+// than the loads (the tied table's 8192 rows: 230 us of sums, against 90 us
+// without the prefetch of the rows added to).
+template <typename P>
+__device__ __forceinline__ P load_if(const P* p, bool on) {
+  P x;
+  if constexpr (sizeof(P) == 16) {
+    uint4 w;
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n"
+        " mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
+        " @q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+        : "=&r"(w.x), "=&r"(w.y), "=&r"(w.z), "=&r"(w.w)
+        : "l"(p), "r"((int)on));
+    *reinterpret_cast<uint4*>(&x) = w;
+  } else if constexpr (sizeof(P) == 4) {
+    uint32_t w;
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n mov.b32 %0, 0;\n"
+        " @q ld.global.u32 %0, [%1];\n}"
+        : "=&r"(w)
+        : "l"(p), "r"((int)on));
+    *reinterpret_cast<uint32_t*>(&x) = w;
+  } else {
+    uint16_t w;
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n mov.b16 %0, 0;\n"
+        " @q ld.global.u16 %0, [%1];\n}"
+        : "=&h"(w)
+        : "l"(p), "r"((int)on));
+    *reinterpret_cast<uint16_t*>(&x) = w;
+  }
+  return x;
+}
+
 template <typename T, int E, int U>
+__device__ __forceinline__ void read_row(const SumArgs& a, uint32_t key, bool on, int first,
+                                         int accesses, Pack<T, E> (&old)[U]) {
+  const Pack<T, E>* src =
+      reinterpret_cast<const Pack<T, E>*>(table_row<T>(a.table, on ? key : 0, a.W, a.K));
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    old[u] = load_if(src + first + u * 32, on && first + u * 32 < accesses);
+}
+
+// `old`: what the row holds, where it is added to.
+template <bool ADD, typename T, int E, int U>
 __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int first, int accesses,
-                                          const Columns<T, E, U>& c) {
+                                          const Columns<T, E, U>& c, const Pack<T, E> (&old)[U]) {
   using P = Pack<T, E>;
   P* dst = reinterpret_cast<P*>(table_row<T>(a.table, key, a.W, a.K));
 #pragma unroll
@@ -254,8 +337,8 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int fi
     const int i = first + u * 32;
     if (i >= accesses) continue;
     P x;
-    if (a.accumulate) {
-      x = dst[i];
+    if (ADD) {
+      x = old[u];
 #pragma unroll
       for (int e = 0; e < E; ++e)
         x.v[e] = Elem<T>::down(fmaf(a.scale, c.v[u * E + e], Elem<T>::up(x.v[e])));
@@ -272,11 +355,11 @@ __device__ __forceinline__ float* run_slot(const SumArgs& a, long long chunk, in
   return a.runs + ((size_t)chunk * 2 + slot) * a.K;
 }
 
-template <typename T, int E, int U>
-__global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ SumArgs a) {
+template <typename T, int E, int U, bool ADD>
+__global__ void __launch_bounds__(kThreads, E > 1 ? 3 : 2) sum_kernel(const __grid_constant__ SumArgs a) {
   wait_for_predecessor();
   let_successor_start();
-  constexpr int kBatch = 8;  // rows whose loads are in flight at once
+  constexpr int kBatch = ADD ? 4 : 8;  // rows whose loads are in flight at once
   using P = Pack<T, E>;
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -284,8 +367,8 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ S
   if (chunk >= a.chunks) return;
   const int accesses = a.K / E;
   const int first = (int)(unit - chunk * a.slices) * (32 * U) + lane;
-  const long long at = chunk * kRunRows;
-  const int rows = (int)(a.N - at < kRunRows ? a.N - at : kRunRows);
+  const long long at = chunk * a.run_rows;
+  const int rows = (int)(a.N - at < a.run_rows ? a.N - at : a.run_rows);
   // Lane l holds row l of the chunk; the keys on either side of it.
   const uint32_t none = 0xffffffffu;
   const uint32_t my_key = lane < rows ? a.key[at + lane] : none;
@@ -296,8 +379,16 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ S
   Columns<T, E, U> sum;
   sum.clear();
   bool continued = prev == __shfl_sync(0xffffffffu, my_key, 0);
+  // Rows that end a run, and those of them that finish it here: not the last of a
+  // run that goes on, nor that of one that began earlier.
+  const uint32_t my_next = __shfl_down_sync(0xffffffffu, my_key, 1);
+  const bool last = lane == rows - 1;
+  const bool real = lane < rows && my_key < (uint32_t)a.vocab;
+  const unsigned ends = __ballot_sync(0xffffffffu, real && (last || my_next != my_key));
+  unsigned finishes = __ballot_sync(0xffffffffu, real && (last ? next : my_next) != my_key);
+  if (continued && finishes) finishes &= ~(ends & (0u - ends));
   for (int i0 = 0; i0 < rows; i0 += kBatch) {
-    P x[kBatch][U];
+    P x[kBatch][U], old[kBatch][U];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const uint32_t key = __shfl_sync(0xffffffffu, my_key, (i0 + b) & 31);
@@ -305,14 +396,14 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ S
       const P* src = reinterpret_cast<const P*>(static_cast<const T*>(a.grad) + (size_t)pos * a.ld);
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (i0 + b < rows && key < (uint32_t)a.vocab && first + u * 32 < accesses)
-          x[b][u] = src[first + u * 32];
+        x[b][u] = load_if(src + first + u * 32, i0 + b < rows && key < (uint32_t)a.vocab &&
+                                                    first + u * 32 < accesses);
+      if (ADD) read_row<T, E, U>(a, key, finishes >> (i0 + b) & 1, first, accesses, old[b]);
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int i = i0 + b;
       const uint32_t key = __shfl_sync(0xffffffffu, my_key, i & 31);
-      const uint32_t after = __shfl_sync(0xffffffffu, my_key, (i + 1) & 31);
       if (i >= rows || key >= (uint32_t)a.vocab) continue;
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -320,12 +411,9 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ S
 #pragma unroll
           for (int e = 0; e < E; ++e) sum.v[u * E + e] += Elem<T>::up(x[b][u].v[e]);
         }
-      const uint32_t following = i + 1 < rows ? after : next;
-      if (following == key && i + 1 < rows) continue;
-      // The run ends here, or goes on in the next chunk.
-      const bool goes_on = following == key;
-      if (!continued && !goes_on) {
-        write_row<T, E, U>(a, key, first, accesses, sum);
+      if (!(ends >> i & 1)) continue;
+      if (finishes >> i & 1) {
+        write_row<ADD, T, E, U>(a, key, first, accesses, sum, old[b]);
       } else {
         float* slot = run_slot<T, E, U>(a, chunk, continued ? 0 : 1);
 #pragma unroll
@@ -343,7 +431,7 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ S
 
 // Joins the runs that cross a chunk's end: the warp of the chunk a run starts
 // in adds that chunk's slot 1 and slot 0 of the chunks after it, in order.
-template <typename T, int E, int U>
+template <typename T, int E, int U, bool ADD>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ SumArgs a) {
   wait_for_predecessor();
   let_successor_start();
@@ -354,22 +442,24 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
   if (chunk + 1 >= a.chunks) return;
   const int accesses = a.K / E;
   const int first = (int)(unit - chunk * a.slices) * (32 * U) + lane;
-  const long long at = chunk * kRunRows;
-  const uint32_t key = a.key[at + kRunRows - 1];
-  if (key >= (uint32_t)a.vocab || a.key[at + kRunRows] != key) return;    // does not go on
+  const long long at = chunk * a.run_rows;
+  const uint32_t key = a.key[at + a.run_rows - 1];
+  if (key >= (uint32_t)a.vocab || a.key[at + a.run_rows] != key) return;    // does not go on
   if (a.key[at] == key && at > 0 && a.key[at - 1] == key) return;  // starts earlier
   // Last chunk of the run: the first whose own last row is not of the run, or
   // whose last row ends it.
   long long last = chunk + 1;
   for (;; last += 32) {
     const long long c = last + lane;
-    const bool ends = c + 1 >= a.chunks || a.key[(c + 1) * kRunRows] != key;
+    const bool ends = c + 1 >= a.chunks || a.key[(c + 1) * a.run_rows] != key;
     const unsigned m = __ballot_sync(0xffffffffu, ends);
     if (m) {
       last += __ffs(m) - 1;
       break;
     }
   }
+  Pack<T, E> old[U];
+  if (ADD) read_row<T, E, U>(a, key, true, first, accesses, old);
   Columns<T, E, U> sum;
   const Pack<float, E>* src =
       reinterpret_cast<const Pack<float, E>*>(run_slot<T, E, U>(a, chunk, 1));
@@ -395,7 +485,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
           for (int e = 0; e < E; ++e) sum.v[u * E + e] += x[b][u].v[e];
         }
   }
-  write_row<T, E, U>(a, key, first, accesses, sum);
+  write_row<ADD, T, E, U>(a, key, first, accesses, sum, old);
 }
 
 bool vectors(int K, size_t ld, const void* p, const Table& t, int tp, size_t elem) {
@@ -416,20 +506,26 @@ cudaError_t embed_as(const EmbedArgs& args, cudaStream_t stream) {
   return launch_dependent(embed_kernel<T, E>, a, (unsigned)blocks, kThreads, 0, 1, stream);
 }
 
-template <typename T, int E, int U>
+template <typename T, int E, int U, bool ADD>
 cudaError_t sum_as(const SumArgs& args, cudaStream_t stream) {
   SumArgs a = args;
   a.slices = (int)div_up(a.K / E, 32 * U);
   const long long blocks = div_up((long long)a.chunks * a.slices, kWarps);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const cudaError_t e =
-      launch_dependent(sum_kernel<T, E, U>, a, (unsigned)blocks, kThreads, 0, 1, stream);
+      launch_dependent(sum_kernel<T, E, U, ADD>, a, (unsigned)blocks, kThreads, 0, 1, stream);
   if (e != cudaSuccess) return e;
-  return launch_dependent(join_kernel<T, E, U>, a, (unsigned)blocks, kThreads, 0, 1, stream);
+  return launch_dependent(join_kernel<T, E, U, ADD>, a, (unsigned)blocks, kThreads, 0, 1, stream);
 }
 
+template <typename T, int E, int U>
+cudaError_t sum_for(const SumArgs& a, bool accumulate, cudaStream_t stream) {
+  return accumulate ? sum_as<T, E, U, true>(a, stream) : sum_as<T, E, U, false>(a, stream);
+}
+
+// Sorts the positions by token into buffer *sorted.
 cudaError_t sort(const hg_vocab& h, const Ids& tokens, int N, int* sorted, cudaStream_t stream) {
-  SortArgs a;
+  SortArgs a = {};
   a.tokens = tokens;
   a.N = N;
   a.vocab = h.vocab;
@@ -442,11 +538,30 @@ cudaError_t sort(const hg_vocab& h, const Ids& tokens, int N, int* sorted, cudaS
     a.pos[i] = h.pos[i];
   }
   *sorted = (a.passes + 1) & 1;
-  const size_t smem = sort_smem(a.digit_bits);
-  cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sort_smem(kMaxDigitBits));
+  const cudaError_t e = cudaFuncSetAttribute(sort_kernel,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)sort_smem(kMaxDigitBits));
   if (e != cudaSuccess) return e;
-  return launch_dependent(sort_kernel, a, kSortCtas, kSortThreads, smem, kSortCtas, stream);
+  return launch_dependent(sort_kernel, a, kSortCtas, kSortThreads, sort_smem(a.digit_bits),
+                          kSortCtas, stream);
+}
+
+cudaError_t clear(const hg_vocab& h, const Table& table, cudaStream_t stream) {
+  ClearArgs a = {};
+  a.table = table;
+  a.bytes = (size_t)h.W * h.K * elem_bytes(h.dtype);
+  const long long blocks = div_up((long long)a.bytes, kThreads * kClearWords * 16);
+  if (blocks * h.tp > 0x7fffffffLL) return cudaErrorInvalidValue;
+  a.blocks = (int)blocks;
+  return launch_dependent(clear_kernel, a, (unsigned)(blocks * h.tp), kThreads, 0, 1, stream);
+}
+
+// Rows of a chunk: kRunRows, but fewer where that leaves too few warps to hide
+// the loads' latency (at 3001 rows of 1001 fp32 the sums took 15 us).
+int run_rows(const hg_vocab& h, int N) {
+  const long long slices = div_up(h.K, 128);
+  const long long enough = 16ll * h.sms;
+  return div_up(N, kRunRows) * slices >= enough ? kRunRows : kFewRunRows;
 }
 
 }  // namespace
@@ -472,40 +587,49 @@ cudaError_t embed(const hg_vocab& h, const Ids& tokens, int N, const void* const
   }
 }
 
+long long embed_grad_chunks(const hg_vocab& h) {
+  // Short chunks are the most just before long ones take over.
+  const long long all = div_up(h.max_rows, run_rows(h, h.max_rows));
+  long long n = 16ll * h.sms / div_up(h.K, 128) * kRunRows + kRunRows;
+  if (n > h.max_rows) n = h.max_rows;
+  const long long most = div_up(n, kFewRunRows);
+  return all > most ? all : most;
+}
+
 cudaError_t embed_grad(const hg_vocab& h, const Ids& tokens, int N, const void* grad,
                        size_t ld_grad, void* const* table, float scale, bool accumulate,
                        cudaStream_t stream) {
   SumArgs a = {};
   const size_t e = elem_bytes(h.dtype);
-  for (int r = 0; r < h.tp; ++r) {
-    a.table.shard[r] = table[r];
-    if (!accumulate) {
-      const cudaError_t st = cudaMemsetAsync(table[r], 0, (size_t)h.W * h.K * e, stream);
-      if (st != cudaSuccess) return st;
-    }
-  }
-  if (N == 0) return cudaSuccess;
+  for (int r = 0; r < h.tp; ++r) a.table.shard[r] = table[r];
   int sorted = 0;
-  const cudaError_t st = sort(h, tokens, N, &sorted, stream);
-  if (st != cudaSuccess) return st;
+  // The sort runs for no tokens too: the clear starts after it.
+  cudaError_t st = sort(h, tokens, N, &sorted, stream);
+  if (st == cudaSuccess && !accumulate) st = clear(h, a.table, stream);
+  if (st != cudaSuccess || N == 0) return st;
   a.key = h.key[sorted];
   a.pos = h.pos[sorted];
   a.N = N;
   a.K = h.K;
   a.W = h.W;
   a.vocab = h.vocab;
-  a.chunks = (int)div_up(N, kRunRows);
+  a.run_rows = run_rows(h, N);
+  a.chunks = (int)div_up(N, a.run_rows);
   a.grad = grad;
   a.ld = ld_grad;
   a.scale = scale;
-  a.accumulate = accumulate;
   a.runs = h.runs;
   const bool vec = vectors(h.K, ld_grad, grad, a.table, h.tp, e);
   switch (h.dtype) {
     case HG_BF16:
-      return vec ? sum_as<__nv_bfloat16, 8, 1>(a, stream) : sum_as<__nv_bfloat16, 1, 4>(a, stream);
-    case HG_FP16: return vec ? sum_as<__half, 8, 1>(a, stream) : sum_as<__half, 1, 4>(a, stream);
-    default: return vec ? sum_as<float, 4, 1>(a, stream) : sum_as<float, 1, 4>(a, stream);
+      return vec ? sum_for<__nv_bfloat16, 8, 1>(a, accumulate, stream)
+                 : sum_for<__nv_bfloat16, 1, 4>(a, accumulate, stream);
+    case HG_FP16:
+      return vec ? sum_for<__half, 8, 1>(a, accumulate, stream)
+                 : sum_for<__half, 1, 4>(a, accumulate, stream);
+    default:
+      return vec ? sum_for<float, 4, 1>(a, accumulate, stream)
+                 : sum_for<float, 1, 4>(a, accumulate, stream);
   }
 }
 

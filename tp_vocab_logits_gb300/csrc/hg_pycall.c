@@ -12,12 +12,17 @@
  * already checked the tensors, and the C entry point validates them again.
  * The entry point's address is passed in by the binding (from the loaded
  * libhg), so this module does not link against libhg itself.
+ *
+ * shard_pointers checks a list of shard tensors and collects their data
+ * pointers, which in Python costs more than the call they are for (eight
+ * shards on the GPU machine's cores: 4.6 us, against 1 us for an embedding call itself).
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <stdint.h>
 #include <stdlib.h>
+#include <string.h>
 
 typedef int (*gather_fn)(void *h, const void *const *shards, void *const *outs, int M,
                          void *stream);
@@ -35,6 +40,7 @@ typedef struct {
 } CallObject;
 
 static PyObject *g_ptr_name; /* interned "ptr" */
+static PyObject *g_is_cuda, *g_dtype, *g_shape, *g_is_contiguous, *g_data_ptr; /* the same */
 
 static int read_ptrs(PyObject *seq, void ***out, Py_ssize_t *n) {
   PyObject *fast = PySequence_Fast(seq, "pointer list must be a sequence of ints");
@@ -140,6 +146,75 @@ static PyObject *call_call(PyObject *obj, PyObject *args, PyObject *kwds) {
   Py_RETURN_NONE;
 }
 
+/* 1: tensor t is a contiguous [rows, cols] CUDA tensor of the type, with *ptr its
+ * data; 0: it is not; -1: an exception is set. */
+static int shard_pointer(PyObject *t, PyObject *dtype, long long rows, long long cols,
+                         void **ptr) {
+  PyObject *x = PyObject_GetAttr(t, g_is_cuda);
+  if (!x) return -1;
+  int ok = x == Py_True;
+  Py_DECREF(x);
+  if (!ok) return 0;
+  x = PyObject_GetAttr(t, g_dtype);
+  if (!x) return -1;
+  ok = x == dtype;
+  Py_DECREF(x);
+  if (!ok) return 0;
+  x = PyObject_GetAttr(t, g_shape);
+  if (!x) return -1;
+  ok = PyTuple_Check(x) && PyTuple_GET_SIZE(x) == 2 &&
+       PyLong_AsLongLong(PyTuple_GET_ITEM(x, 0)) == rows &&
+       PyLong_AsLongLong(PyTuple_GET_ITEM(x, 1)) == cols;
+  Py_DECREF(x);
+  if (PyErr_Occurred()) return -1;
+  if (!ok) return 0;
+  x = PyObject_CallMethodNoArgs(t, g_is_contiguous);
+  if (!x) return -1;
+  ok = x == Py_True;
+  Py_DECREF(x);
+  if (!ok) return 0;
+  x = PyObject_CallMethodNoArgs(t, g_data_ptr);
+  if (!x) return -1;
+  *ptr = PyLong_AsVoidPtr(x);
+  Py_DECREF(x);
+  return PyErr_Occurred() ? -1 : 1;
+}
+
+/* shard_pointers(tensors, shards, dtype, rows, cols): the tensors' data pointers
+ * as an array in a bytes object, or None where there are not `shards` of them
+ * or one is not a contiguous [rows, cols] CUDA tensor of the type. */
+static PyObject *shard_pointers(PyObject *module, PyObject *args) {
+  PyObject *seq, *dtype;
+  Py_ssize_t n;
+  long long rows, cols;
+  (void)module;
+  if (!PyArg_ParseTuple(args, "OnOLL", &seq, &n, &dtype, &rows, &cols)) return NULL;
+  PyObject *fast = PySequence_Fast(seq, "shards must be a sequence of tensors");
+  if (!fast) return NULL;
+  if (n < 0 || PySequence_Fast_GET_SIZE(fast) != n) {
+    Py_DECREF(fast);
+    Py_RETURN_NONE;
+  }
+  PyObject *out = PyBytes_FromStringAndSize(NULL, n * (Py_ssize_t)sizeof(void *));
+  int st = out ? 1 : -1;
+  for (Py_ssize_t i = 0; i < n && st == 1; ++i) {
+    void *p = NULL;
+    st = shard_pointer(PySequence_Fast_GET_ITEM(fast, i), dtype, rows, cols, &p);
+    if (st == 1) memcpy(PyBytes_AS_STRING(out) + i * (Py_ssize_t)sizeof p, &p, sizeof p);
+  }
+  Py_DECREF(fast);
+  if (st == 1) return out;
+  Py_XDECREF(out);
+  if (st < 0) return NULL;
+  Py_RETURN_NONE;
+}
+
+static PyMethodDef hgcall_methods[] = {
+    {"shard_pointers", shard_pointers, METH_VARARGS,
+     "shard_pointers(tensors, shards, dtype, rows, cols) -> bytes or None"},
+    {NULL, NULL, 0, NULL},
+};
+
 static PyTypeObject CallType = {
     PyVarObject_HEAD_INIT(NULL, 0)
     .tp_name = "_hgcall.Call",
@@ -153,13 +228,19 @@ static PyTypeObject CallType = {
 
 static struct PyModuleDef hgcall_module = {
     PyModuleDef_HEAD_INIT, "_hgcall", "Direct hg_gather calls for the Python binding.", -1,
-    NULL /* methods */, NULL /* slots */, NULL /* traverse */, NULL /* clear */, NULL /* free */,
+    hgcall_methods, NULL /* slots */, NULL /* traverse */, NULL /* clear */, NULL /* free */,
 };
 
 PyMODINIT_FUNC PyInit__hgcall(void) {
   if (PyType_Ready(&CallType) < 0) return NULL;
   g_ptr_name = PyUnicode_InternFromString("ptr");
-  if (!g_ptr_name) return NULL;
+  g_is_cuda = PyUnicode_InternFromString("is_cuda");
+  g_dtype = PyUnicode_InternFromString("dtype");
+  g_shape = PyUnicode_InternFromString("shape");
+  g_is_contiguous = PyUnicode_InternFromString("is_contiguous");
+  g_data_ptr = PyUnicode_InternFromString("data_ptr");
+  if (!g_ptr_name || !g_is_cuda || !g_dtype || !g_shape || !g_is_contiguous || !g_data_ptr)
+    return NULL;
   PyObject *m = PyModule_Create(&hgcall_module);
   if (!m) return NULL;
   Py_INCREF(&CallType);

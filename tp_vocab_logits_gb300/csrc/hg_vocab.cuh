@@ -130,14 +130,18 @@ cudaError_t launch_dependent(void (*kernel)(Args), const Args& args, unsigned gr
   return cudaLaunchKernelEx(&cfg, kernel, args);
 }
 
-// Sorted tokens summed as one sequence in embed_grad.
+// Sorted rows that embed_grad sums as one sequence, and where there are few of them.
 constexpr int kRunRows = 32;
+constexpr int kFewRunRows = 8;
 
 cudaError_t embed(const hg_vocab& h, const Ids& tokens, int N, const void* const* table,
                   float scale, void* out, size_t ld_out, cudaStream_t stream);
 cudaError_t embed_grad(const hg_vocab& h, const Ids& tokens, int N, const void* grad,
                        size_t ld_grad, void* const* table, float scale, bool accumulate,
                        cudaStream_t stream);
+
+// Sequences of the largest call (workspace).
+long long embed_grad_chunks(const hg_vocab& h);
 
 // What one call of the loss or its gradient works on.
 struct LossCall {

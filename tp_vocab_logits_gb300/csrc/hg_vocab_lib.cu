@@ -62,7 +62,7 @@ size_t lay_out(hg_vocab* h, unsigned char* base) {
       l.take(h->key[i], n);
       l.take(h->pos[i], n);
     }
-    l.take(h->runs, (size_t)hg::vocab::div_up(h->max_rows, hg::vocab::kRunRows) * 2 * h->K);
+    l.take(h->runs, (size_t)hg::vocab::embed_grad_chunks(*h) * 2 * h->K);
   }
   return l.used;
 }

@@ -77,10 +77,10 @@ def load() -> ctypes.CDLL:
     lib.hg_vocab_workspace_bytes.argtypes = [vp]
     lib.hg_vocab_workspace_bytes.restype = sz
     lib.hg_vocab_sync.argtypes = [vp, st]
-    lib.hg_vocab_embed.argtypes = [vp, vp, i, i, vpp, f, vp, sz, st]
-    lib.hg_vocab_embed_grad.argtypes = [vp, vp, i, i, vp, sz, vpp, f, i, st]
-    lib.hg_vocab_loss.argtypes = [vp, vp, sz, vpp, vp, i, i, f, vp, vp, st]
-    lib.hg_vocab_loss_grad.argtypes = [vp, vp, sz, vpp, vp, i, vp, vp, i, f, vp, sz, vpp, i, st]
+    lib.hg_vocab_embed.argtypes = [vp, vp, i, i, vp, f, vp, sz, st]
+    lib.hg_vocab_embed_grad.argtypes = [vp, vp, i, i, vp, sz, vp, f, i, st]
+    lib.hg_vocab_loss.argtypes = [vp, vp, sz, vp, vp, i, i, f, vp, vp, st]
+    lib.hg_vocab_loss_grad.argtypes = [vp, vp, sz, vp, vp, i, vp, vp, i, f, vp, sz, vp, i, st]
     lib.hg_strerror.argtypes = [i]
     lib.hg_strerror.restype = ctypes.c_char_p
     for name in ("hg_create", "hg_create_ex", "hg_destroy", "hg_gather", "hg_gather_host",
@@ -473,6 +473,13 @@ def hg_vocab_sync(h: VocabHandle, stream=None) -> None:
     _check(load().hg_vocab_sync(h.ptr, _stream_ptr(stream)), "hg_vocab_sync")
 
 
+def _vocab_stream(stream, t: torch.Tensor) -> int:
+    """The raw stream of a call on t's device (the current one by default)."""
+    if stream is None:  # torch.cuda.current_stream() builds two objects to say the same
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream_ptr(stream)
+
+
 def _vocab_ids(t: torch.Tensor, what: str) -> int:
     if not t.is_cuda or t.dtype not in (torch.int32, torch.int64) or t.dim() != 1 \
             or not t.is_contiguous():
@@ -484,31 +491,33 @@ def _vocab_rows(h: VocabHandle, t: torch.Tensor, n: int, what: str) -> int:
     """Row distance of a token-side [n, hidden] matrix (rows contiguous)."""
     if not t.is_cuda or t.dtype != h.dtype:
         raise ValueError(f"{what}: need a CUDA tensor of {h.dtype}, got {t.dtype} on {t.device}")
-    if tuple(t.shape) != (n, h.hidden) or (h.hidden > 1 and t.stride(1) != 1):
+    if t.shape != (n, h.hidden) or (h.hidden > 1 and t.stride(1) != 1):
         raise ValueError(f"{what}: need [{n}, {h.hidden}] with contiguous rows, got "
                          f"{tuple(t.shape)} with strides {t.stride()}")
     if n <= 1:
         return h.hidden
-    if t.stride(0) < h.hidden:
-        raise ValueError(f"{what}: rows overlap (row stride {t.stride(0)})")
-    return t.stride(0)
+    ld = t.stride(0)
+    if ld < h.hidden:
+        raise ValueError(f"{what}: rows overlap (row stride {ld})")
+    return ld
 
 
-def _vocab_shards(h: VocabHandle, ts: Sequence[torch.Tensor], what: str):
+def _vocab_shards(h: VocabHandle, ts: Sequence[torch.Tensor], what: str) -> bytes:
+    """Checked shards as an array of device pointers."""
+    ptrs = _pycall().shard_pointers(ts, h.tp, h.dtype, h.shard_cols, h.hidden)
+    if ptrs is not None:
+        return ptrs
     if len(ts) != h.tp:
         raise ValueError(f"{what}: expected {h.tp} shards, got {len(ts)}")
     for t in ts:
         if not t.is_cuda or t.dtype != h.dtype:
             raise ValueError(f"{what}: need CUDA tensors of {h.dtype}, got {t.dtype} on {t.device}")
-        if tuple(t.shape) != (h.shard_cols, h.hidden) or not t.is_contiguous():
-            raise ValueError(f"{what}: need contiguous [{h.shard_cols}, {h.hidden}], got "
-                             f"{tuple(t.shape)}")
-    return _ptr_array(ts)
+    raise ValueError(f"{what}: need contiguous [{h.shard_cols}, {h.hidden}] shards, got "
+                     f"{[tuple(t.shape) for t in ts]}")
 
 
 def _vocab_floats(t: torch.Tensor, n: int, what: str) -> int:
-    if not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != (n,) \
-            or not t.is_contiguous():
+    if not t.is_cuda or t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what}: need a contiguous float32 CUDA tensor [{n}]")
     return t.data_ptr()
 
@@ -520,7 +529,7 @@ def hg_vocab_embed(h: VocabHandle, tokens: torch.Tensor, table: Sequence[torch.T
     ld = _vocab_rows(h, out, n, "out")
     _check(load().hg_vocab_embed(h.ptr, tokens.data_ptr(), tokens.element_size(), n,
                                  _vocab_shards(h, table, "table"), scale, out.data_ptr(), ld,
-                                 _stream_ptr(stream)), "hg_vocab_embed")
+                                 _vocab_stream(stream, out)), "hg_vocab_embed")
 
 
 def hg_vocab_embed_grad(h: VocabHandle, tokens: torch.Tensor, grad_out: torch.Tensor,
@@ -533,7 +542,7 @@ def hg_vocab_embed_grad(h: VocabHandle, tokens: torch.Tensor, grad_out: torch.Te
     _check(load().hg_vocab_embed_grad(h.ptr, tokens.data_ptr(), tokens.element_size(), n,
                                       grad_out.data_ptr(), ld,
                                       _vocab_shards(h, grad_table, "grad_table"), scale,
-                                      int(bool(accumulate)), _stream_ptr(stream)),
+                                      int(bool(accumulate)), _vocab_stream(stream, grad_out)),
            "hg_vocab_embed_grad")
 
 
@@ -547,7 +556,7 @@ def hg_vocab_loss(h: VocabHandle, hidden: torch.Tensor, weight: Sequence[torch.T
     _check(load().hg_vocab_loss(h.ptr, hidden.data_ptr(), ld, _vocab_shards(h, weight, "weight"),
                                 targets.data_ptr(), targets.element_size(), n, logit_scale,
                                 _vocab_floats(loss, n, "loss"), _vocab_floats(lse, n, "lse"),
-                                _stream_ptr(stream)), "hg_vocab_loss")
+                                _vocab_stream(stream, hidden)), "hg_vocab_loss")
 
 
 def hg_vocab_loss_grad(h: VocabHandle, hidden: torch.Tensor, weight: Sequence[torch.Tensor],
@@ -567,4 +576,4 @@ def hg_vocab_loss_grad(h: VocabHandle, hidden: torch.Tensor, weight: Sequence[to
         _vocab_floats(grad_loss, n, "grad_loss"), n, logit_scale,
         None if grad_hidden is None else grad_hidden.data_ptr(), ld_grad,
         None if grad_weight is None else _vocab_shards(h, grad_weight, "grad_weight"),
-        int(bool(accumulate)), _stream_ptr(stream)), "hg_vocab_loss_grad")
+        int(bool(accumulate)), _vocab_stream(stream, hidden)), "hg_vocab_loss_grad")
