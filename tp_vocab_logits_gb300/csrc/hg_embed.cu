@@ -29,6 +29,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowAccesses = 4;  // accesses per lane of a unit of the lookup
+constexpr int kLookupThreads = 128;
 
 struct Table {
   void* shard[HG_MAX_TP];
@@ -51,11 +52,11 @@ struct EmbedArgs {
 };
 
 template <typename T, int E>
-__global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__ EmbedArgs a) {
+__global__ void __launch_bounds__(kLookupThreads) embed_kernel(const __grid_constant__ EmbedArgs a) {
   wait_for_predecessor();
   let_successor_start();
   const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const long long unit = (long long)blockIdx.x * (kLookupThreads / 32) + (threadIdx.x >> 5);
   const long long n = unit / a.units_per_row;
   if (n >= a.N) return;
   const int first = (int)(unit - n * a.units_per_row) * (kRowAccesses * 32) + lane;
@@ -96,9 +97,11 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__
 // through distributed shared memory and the entries through L2.
 
 constexpr int kSortCtas = 8;
-constexpr int kSortThreads = 1024;
+constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kMaxDigitBits = 10;
+constexpr int kMaxDigitBits = 9;  // a thread per digit
+static_assert((1 << kMaxDigitBits) <= kSortThreads && kSortWarps <= 32, "sort_pass's layout");
+constexpr int kKeys = 4;  // keys of a lane whose loads are in flight at once
 
 struct SortArgs {
   Ids tokens;
@@ -145,32 +148,46 @@ __device__ void sort_pass(const SortArgs& a, int pass, SortShared* sh, uint32_t*
 
   for (int d = lane; d < D; d += 32) mine[d] = 0;
   __syncwarp();
-  for (long long i0 = lo; i0 < hi; i0 += 32) {
-    const bool on = i0 + lane < hi;
-    const uint32_t digit = on ? (key_at(i0 + lane) >> shift) & (D - 1) : D;
-    const unsigned peers = __match_any_sync(0xffffffffu, digit);
-    if (on && lane == __ffs(peers) - 1) mine[digit] += __popc(peers);
-    __syncwarp();
+  for (long long i0 = lo; i0 < hi; i0 += 32 * kKeys) {
+    uint32_t digit[kKeys];
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) {
+      const long long i = i0 + j * 32 + lane;
+      digit[j] = i < hi ? (key_at(i) >> shift) & (D - 1) : D;
+    }
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) {
+      if (i0 + j * 32 >= hi) break;
+      const unsigned peers = __match_any_sync(0xffffffffu, digit[j]);
+      if (digit[j] < D && lane == __ffs(peers) - 1) mine[digit[j]] += __popc(peers);
+      __syncwarp();
+    }
   }
   __syncthreads();
   if (threadIdx.x < D) {
-    uint32_t sum = 0;
+    uint32_t c[kSortWarps], sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) c[w] = place[w * D + threadIdx.x];
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
-      const uint32_t c = place[w * D + threadIdx.x];
       place[w * D + threadIdx.x] = sum;
-      sum += c;
+      sum += c[w];
     }
     sh->hist[threadIdx.x] = sum;
   }
   cluster.sync();
   uint32_t all = 0, before = 0;
   if (threadIdx.x < D) {
+#pragma unroll
     for (int c = 0; c < kSortCtas; ++c) {
       const uint32_t x = cluster.map_shared_rank(sh->hist, c)[threadIdx.x];
       if (c < cta) before += x;
       all += x;
     }
   }
+  const bool final = pass + 1 == a.passes;
+  // The counts have been read: after the last pass nothing else is shared.
+  if (final) cluster.barrier_arrive();
   // Exclusive sum of `all` over the digits (threads D.. add nothing).
   uint32_t incl = all;
   for (int o = 1; o < 32; o <<= 1) {
@@ -180,33 +197,47 @@ __device__ void sort_pass(const SortArgs& a, int pass, SortShared* sh, uint32_t*
   if (lane == 31) sh->warp_sum[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    uint32_t w = sh->warp_sum[lane];
+    uint32_t w = lane < kSortWarps ? sh->warp_sum[lane] : 0;
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w += x;
     }
-    sh->warp_sum[lane] = w;
+    if (lane < kSortWarps) sh->warp_sum[lane] = w;
   }
   __syncthreads();
   if (threadIdx.x < D)
     sh->base[threadIdx.x] = incl - all + before + (warp ? sh->warp_sum[warp - 1] : 0);
   __syncthreads();
-  for (long long i0 = lo; i0 < hi; i0 += 32) {
-    const bool on = i0 + lane < hi;
-    const uint32_t key = on ? key_at(i0 + lane) : 0;
-    const uint32_t digit = on ? (key >> shift) & (D - 1) : D;
-    const unsigned peers = __match_any_sync(0xffffffffu, digit);
-    const int rank = __popc(peers & ((1u << lane) - 1));
-    if (on) {
-      const uint32_t to = sh->base[digit] + mine[digit] + rank;
-      out_key[to] = key;
-      out_pos[to] = pass > 0 ? __ldcg(in_pos + i0 + lane) : (int)(i0 + lane);
+  for (long long i0 = lo; i0 < hi; i0 += 32 * kKeys) {
+    uint32_t key[kKeys];
+    int from[kKeys];
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) {
+      const long long i = i0 + j * 32 + lane;
+      key[j] = i < hi ? key_at(i) : 0;
+      from[j] = i < hi ? (pass > 0 ? __ldcg(in_pos + i) : (int)i) : 0;
     }
-    __syncwarp();
-    if (on && rank == 0) mine[digit] += __popc(peers);
-    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) {
+      if (i0 + j * 32 >= hi) break;
+      const bool on = i0 + j * 32 + lane < hi;
+      const uint32_t digit = on ? (key[j] >> shift) & (D - 1) : D;
+      const unsigned peers = __match_any_sync(0xffffffffu, digit);
+      const int rank = __popc(peers & ((1u << lane) - 1));
+      if (on) {
+        const uint32_t to = sh->base[digit] + mine[digit] + rank;
+        out_key[to] = key[j];
+        out_pos[to] = from[j];
+      }
+      __syncwarp();
+      if (on && rank == 0) mine[digit] += __popc(peers);
+      __syncwarp();
+    }
   }
-  cluster.sync();  // every entry moved, every count read
+  if (final)
+    cluster.barrier_wait();
+  else
+    cluster.sync();  // every entry moved, every count read
 }
 
 // The successor may start once every CTA here has seen its predecessor complete:
@@ -316,37 +347,36 @@ __device__ __forceinline__ P load_if(const P* p, bool on) {
   return x;
 }
 
-template <typename T, int E, int U>
-__device__ __forceinline__ void read_row(const SumArgs& a, uint32_t key, bool on, int first,
-                                         int accesses, Pack<T, E> (&old)[U]) {
-  const Pack<T, E>* src =
-      reinterpret_cast<const Pack<T, E>*>(table_row<T>(a.table, on ? key : 0, a.W, a.K));
+// This lane's columns of a row, where `on`.
+template <typename P, int U>
+__device__ __forceinline__ void load_row(const P* row, bool on, int first, int accesses,
+                                         P (&x)[U]) {
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    old[u] = load_if(src + first + u * 32, on && first + u * 32 < accesses);
+    x[u] = load_if(row + first + u * 32, on && first + u * 32 < accesses);
+}
+
+template <typename P>
+__device__ __forceinline__ P* shfl_pointer(P* p, int lane) {
+  return reinterpret_cast<P*>(
+      __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), lane));
 }
 
 // `old`: what the row holds, where it is added to.
 template <bool ADD, typename T, int E, int U>
-__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int first, int accesses,
+__device__ __forceinline__ void write_row(Pack<T, E>* row, float scale, int first, int accesses,
                                           const Columns<T, E, U>& c, const Pack<T, E> (&old)[U]) {
-  using P = Pack<T, E>;
-  P* dst = reinterpret_cast<P*>(table_row<T>(a.table, key, a.W, a.K));
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int i = first + u * 32;
     if (i >= accesses) continue;
-    P x;
-    if (ADD) {
-      x = old[u];
+    Pack<T, E> x;
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        x.v[e] = Elem<T>::down(fmaf(a.scale, c.v[u * E + e], Elem<T>::up(x.v[e])));
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) x.v[e] = Elem<T>::down(a.scale * c.v[u * E + e]);
+    for (int e = 0; e < E; ++e) {
+      const float v = c.v[u * E + e];
+      x.v[e] = Elem<T>::down(ADD ? fmaf(scale, v, Elem<T>::up(old[u].v[e])) : scale * v);
     }
-    dst[i] = x;
+    row[i] = x;
   }
 }
 
@@ -356,10 +386,11 @@ __device__ __forceinline__ float* run_slot(const SumArgs& a, long long chunk, in
 }
 
 template <typename T, int E, int U, bool ADD>
-__global__ void __launch_bounds__(kThreads, E > 1 ? 3 : 2) sum_kernel(const __grid_constant__ SumArgs a) {
+__global__ void __launch_bounds__(kThreads, E == 1 ? 2 : 4)
+    sum_kernel(const __grid_constant__ SumArgs a) {
   wait_for_predecessor();
   let_successor_start();
-  constexpr int kBatch = ADD ? 4 : 8;  // rows whose loads are in flight at once
+  constexpr int kBatch = 4;  // rows whose loads are in flight at once
   using P = Pack<T, E>;
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -372,9 +403,13 @@ __global__ void __launch_bounds__(kThreads, E > 1 ? 3 : 2) sum_kernel(const __gr
   // Lane l holds row l of the chunk; the keys on either side of it.
   const uint32_t none = 0xffffffffu;
   const uint32_t my_key = lane < rows ? a.key[at + lane] : none;
-  const int my_pos = lane < rows ? a.pos[at + lane] : 0;
   const uint32_t prev = at > 0 ? a.key[at - 1] : none;
   const uint32_t next = at + rows < a.N ? a.key[at + rows] : none;
+  const bool real = lane < rows && my_key < (uint32_t)a.vocab;
+  const P* const my_src = reinterpret_cast<const P*>(
+      static_cast<const T*>(a.grad) + (size_t)(real ? a.pos[at + lane] : 0) * a.ld);
+  P* const my_dst =
+      reinterpret_cast<P*>(table_row<T>(a.table, real ? my_key : 0, a.W, a.K));
 
   Columns<T, E, U> sum;
   sum.clear();
@@ -383,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, E > 1 ? 3 : 2) sum_kernel(const __gr
   // run that goes on, nor that of one that began earlier.
   const uint32_t my_next = __shfl_down_sync(0xffffffffu, my_key, 1);
   const bool last = lane == rows - 1;
-  const bool real = lane < rows && my_key < (uint32_t)a.vocab;
+  const unsigned reals = __ballot_sync(0xffffffffu, real);
   const unsigned ends = __ballot_sync(0xffffffffu, real && (last || my_next != my_key));
   unsigned finishes = __ballot_sync(0xffffffffu, real && (last ? next : my_next) != my_key);
   if (continued && finishes) finishes &= ~(ends & (0u - ends));
@@ -391,29 +426,21 @@ __global__ void __launch_bounds__(kThreads, E > 1 ? 3 : 2) sum_kernel(const __gr
     P x[kBatch][U], old[kBatch][U];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const uint32_t key = __shfl_sync(0xffffffffu, my_key, (i0 + b) & 31);
-      const int pos = __shfl_sync(0xffffffffu, my_pos, (i0 + b) & 31);
-      const P* src = reinterpret_cast<const P*>(static_cast<const T*>(a.grad) + (size_t)pos * a.ld);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        x[b][u] = load_if(src + first + u * 32, i0 + b < rows && key < (uint32_t)a.vocab &&
-                                                    first + u * 32 < accesses);
-      if (ADD) read_row<T, E, U>(a, key, finishes >> (i0 + b) & 1, first, accesses, old[b]);
+      const int i = (i0 + b) & 31;
+      load_row(shfl_pointer(my_src, i), reals >> i & 1, first, accesses, x[b]);
+      if (ADD) load_row<P>(shfl_pointer(my_dst, i), finishes >> i & 1, first, accesses, old[b]);
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int i = i0 + b;
-      const uint32_t key = __shfl_sync(0xffffffffu, my_key, i & 31);
-      if (i >= rows || key >= (uint32_t)a.vocab) continue;
+      // What was not loaded is zero.
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (first + u * 32 < accesses) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) sum.v[u * E + e] += Elem<T>::up(x[b][u].v[e]);
-        }
+        for (int e = 0; e < E; ++e) sum.v[u * E + e] += Elem<T>::up(x[b][u].v[e]);
       if (!(ends >> i & 1)) continue;
       if (finishes >> i & 1) {
-        write_row<ADD, T, E, U>(a, key, first, accesses, sum, old[b]);
+        write_row<ADD, T, E, U>(shfl_pointer(my_dst, i), a.scale, first, accesses, sum, old[b]);
       } else {
         float* slot = run_slot<T, E, U>(a, chunk, continued ? 0 : 1);
 #pragma unroll
@@ -458,8 +485,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
       break;
     }
   }
+  Pack<T, E>* const row = reinterpret_cast<Pack<T, E>*>(table_row<T>(a.table, key, a.W, a.K));
   Pack<T, E> old[U];
-  if (ADD) read_row<T, E, U>(a, key, true, first, accesses, old);
+  if (ADD) load_row<Pack<T, E>>(row, true, first, accesses, old);
   Columns<T, E, U> sum;
   const Pack<float, E>* src =
       reinterpret_cast<const Pack<float, E>*>(run_slot<T, E, U>(a, chunk, 1));
@@ -485,7 +513,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
           for (int e = 0; e < E; ++e) sum.v[u * E + e] += x[b][u].v[e];
         }
   }
-  write_row<ADD, T, E, U>(a, key, first, accesses, sum, old);
+  write_row<ADD, T, E, U>(row, a.scale, first, accesses, sum, old);
 }
 
 bool vectors(int K, size_t ld, const void* p, const Table& t, int tp, size_t elem) {
@@ -501,9 +529,9 @@ template <typename T, int E>
 cudaError_t embed_as(const EmbedArgs& args, cudaStream_t stream) {
   EmbedArgs a = args;
   a.units_per_row = (int)div_up(a.K / E, kRowAccesses * 32);
-  const long long blocks = div_up((long long)a.N * a.units_per_row, kWarps);
+  const long long blocks = div_up((long long)a.N * a.units_per_row, kLookupThreads / 32);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_dependent(embed_kernel<T, E>, a, (unsigned)blocks, kThreads, 0, 1, stream);
+  return launch_dependent(embed_kernel<T, E>, a, (unsigned)blocks, kLookupThreads, 0, 1, stream);
 }
 
 template <typename T, int E, int U, bool ADD>
