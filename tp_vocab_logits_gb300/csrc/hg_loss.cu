@@ -38,7 +38,11 @@ constexpr int kMaxStages = 12;
 constexpr uint32_t kBox = 64 * 128;  // a [64 x 64] box of 16-bit elements
 constexpr uint32_t kTmemCols = 2 * kTileN;  // two accumulators
 constexpr int kEpilogueWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpilogueWarps;  // warp 0 TMA, warp 1 MMA
+// Warp 0 copies A and warp 2 copies B: one thread for both kept the tensor cores
+// waiting (V=49999, K=1544: kDw's four copies a stage took a tenth longer when the
+// loop around them was not unrolled). Warp 1 issues the MMAs.
+constexpr int kFirstEpilogueWarp = 3;
+constexpr int kThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
 constexpr uint32_t kStageOut = 32 * 128;  // a warp's staged [32 rows x 128 bytes]
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kFixedSmem = 1024 + 256;  // alignment of the stages, barriers
@@ -48,7 +52,9 @@ constexpr size_t kFixedSmem = 1024 + 256;  // alignment of the stages, barriers
 // at K = 7168 put the logsumexp 1e-6 off), fp32 additions round them.
 constexpr int kSegment = 32;
 constexpr int kGroupM = 8;      // row tiles that share the column tiles of a wave
-constexpr int kSmallRows = 128;  // up to here the loss reads hidden where it lies
+constexpr int kSmallRows = 128;  // up to here a tile of one CTA holds all rows
+constexpr int kOneTileRows = 256;  // and a pair's: packing leaves no tile out
+constexpr int kNarrowRounds = 8;
 constexpr int kMaxSplits = 16;
 constexpr unsigned long long kTimeoutNs = 4000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -64,7 +70,7 @@ struct GemmArgs {
   int rows;
   int tp, W, vocab, K;
   int c0, wc, wcols;  // the piece: first column, its width in prob, its columns
-  int bn;             // columns of a vocabulary tile (kLoss, kProb)
+  int bn;             // columns of a tile
   int stages;         // K blocks in flight
   uint32_t a_bytes;   // of one stage in shared memory
   uint32_t b_bytes;
@@ -364,55 +370,57 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   const int units = (int)gridDim.x / CTAS;
   const int unit = (int)blockIdx.x / CTAS;
   const int row0 = rank * kTileM;             // of this CTA in a tile
-  constexpr int kCols = kTileN / CTAS;        // columns of B in this CTA
+  const int cols = a.bn / CTAS;              // columns of B in this CTA
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     if (lane == 0) {
       // The loss of few rows reads the weights once (evict-first: 1 row at V=163840,
       // K=7168 342 us, against 359 us with the default policy); every other
       // operand is read again by other tiles.
-      const uint64_t keep = policy_evict_normal();
-      const uint64_t weights = KIND == kLoss && CTAS == 1 ? policy_evict_first() : keep;
+      const uint64_t policy = KIND == kLoss && CTAS == 1 && warp == 2 ? policy_evict_first()
+                                                                      : policy_evict_normal();
+      const uint32_t first_full = CTAS == 2 ? in_first_cta(sh->full) : 0;
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int i = unit; i < work.total && ok; i += units) {
         const Tile t = work.at(a, i);
+        // Coordinates of the tile's rows of A or columns of B; kDx walks the shards.
+        const int at = warp == 0 ? t.m * work.kRows + row0 : t.n * a.bn + rank * cols;
+        int r = KIND == kDx ? t.kb0 / work.per_shard : t.r;
+        int b = KIND == kDx ? t.kb0 - r * work.per_shard : 0;
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
           if (!wait_phase(&sh->empty[stage], phase ^ 1u, a.status)) { ok = false; break; }
           uint64_t* bar = &sh->full[stage];
-          unsigned char* A = base + (size_t)stage * stage_bytes;
-          unsigned char* B = A + a.a_bytes;
-          if (rank == 0) mbar_expect_tx(bar, a.load_bytes * CTAS);
-          auto load = [&](unsigned char* dst, const CUtensorMap* tm, int x, int y,
-                          uint64_t policy) {
+          unsigned char* dst = base + (size_t)stage * stage_bytes + (warp == 0 ? 0 : a.a_bytes);
+          auto load = [&](int box, const CUtensorMap* tm, int x, int y) {
             if constexpr (CTAS == 1)
-              tma_load_2d(dst, tm, x, y, bar, policy);
+              tma_load_2d(dst + box * kBox, tm, x, y, bar, policy);
             else
-              tma_load_pair(dst, tm, x, y, in_first_cta(bar), policy);
+              tma_load_pair(dst + box * kBox, tm, x, y, first_full + (uint32_t)stage * 8, policy);
           };
-          if (KIND == kLoss || KIND == kProb) {
-            load(A, &a.x, kb * kBlockK, t.m * work.kRows + row0, keep);
-            load(B, &a.shard[t.r], kb * kBlockK, a.c0 + t.n * a.bn + rank * kCols,
-                 weights);
-          } else if (KIND == kDx) {
-            const int r = kb / work.per_shard;
-            const int b = kb - r * work.per_shard;
-            load(A, &a.p, r * a.wc + b * kBlockK, t.m * work.kRows + row0, keep);
+          if (warp == 0) {
+            if (rank == 0) mbar_expect_tx(bar, a.load_bytes * CTAS);
+            if (KIND == kLoss || KIND == kProb) {
+              load(0, &a.x, kb * kBlockK, at);
+            } else if (KIND == kDx) {
+              load(0, &a.p, r * a.wc + b * kBlockK, at);
+            } else {
 #pragma unroll
-            for (int j = 0; j < kCols / 64; ++j)
-              load(B + j * kBox, &a.shard[r], t.n * kTileN + rank * kCols + j * 64,
-                   a.c0 + b * kBlockK, weights);
+              for (int j = 0; j < kTileM / 64; ++j)
+                load(j, &a.p, r * a.wc + at + j * 64, kb * kBlockK);
+            }
           } else {
+            if (KIND == kLoss || KIND == kProb) {
+              load(0, &a.shard[r], kb * kBlockK, a.c0 + at);
+            } else {
 #pragma unroll
-            for (int j = 0; j < kTileM / 64; ++j)
-              load(A + j * kBox, &a.p, t.r * a.wc + t.m * work.kRows + row0 + j * 64,
-                   kb * kBlockK, keep);
-#pragma unroll
-            for (int j = 0; j < kCols / 64; ++j)
-              load(B + j * kBox, &a.x, t.n * kTileN + rank * kCols + j * 64, kb * kBlockK,
-                   keep);
+              for (int j = 0; j < kTileN / CTAS / 64; ++j)
+                load(j, KIND == kDx ? &a.shard[r] : &a.x, at + j * 64,
+                     KIND == kDx ? a.c0 + b * kBlockK : kb * kBlockK);
+            }
           }
+          if (KIND == kDx && ++b == work.per_shard) { b = 0; ++r; }
           ++issued;
           if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
@@ -470,10 +478,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   } else {
     // Warps w and w + 4 share 32 rows and take half of the columns each.
     const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;
+    const int half = (warp - kFirstEpilogueWarp) >> 2;
     const int first = half * (kTileN / 2);
     const int row = row0 + quarter * 32 + lane;  // in the tile
-    unsigned char* const stage_out = sOut + (size_t)(warp - 2) * kStageOut;
+    unsigned char* const stage_out = sOut + (size_t)(warp - kFirstEpilogueWarp) * kStageOut;
     int acc = 0;
     uint32_t acc_phase = 0;
     const float unscale = KIND == kDw ? *a.unscale : 1.f;
@@ -1016,24 +1024,29 @@ cudaError_t launch(const hg_vocab& h, const Shape& shape, GemmArgs& a, cudaStrea
 // nobody reads).
 Shape row_shape(int N, int columns) {
   Shape s;
-  if (N > kSmallRows) return s;
-  s.ctas = 1;
-  s.a_rows = (int)round_up(N > 0 ? N : 1, 8);
-  s.b_cols = columns;
+  s.ctas = N > kSmallRows ? 2 : 1;
+  s.a_rows = N > kSmallRows ? kTileM : (int)round_up(N > 0 ? N : 1, 8);
+  s.b_cols = columns / s.ctas;
   return s;
 }
 
-// Width of the vocabulary tiles: kTileN, but for few rows, where reading the
-// weights bounds the call, the width that leaves the busiest SM the fewest bytes
-// (a tile also reads the rows, from L2: counted as half).
+// Width of the vocabulary tiles: the one that leaves the busiest SM the least.
+// That is bytes of weights for few rows and MMA columns for many; either way a
+// tile has a part that does not shrink with it: the rows it reads from L2, half
+// as dear as the weights, or the ends of its pipeline. (333 rows at V=49999,
+// K=1000: 224 columns 56 us, 256 columns 60 us.) Where tiles go many times
+// round (kNarrowRounds), the widest.
 int tile_width(const hg_vocab& h, int N, int cols, int step) {
-  if (N > kSmallRows) return kTileN;
-  const int rows = (int)round_up(N > 0 ? N : 1, 8);
+  const int ctas = row_shape(N, kTileN).ctas;
+  const long long row_tiles = div_up(N > 0 ? N : 1, kTileM * ctas);
+  const int fixed = ctas == 1 ? (int)round_up(N > 0 ? N : 1, 8) / 2 : 16;
   int best = kTileN;
+  if (ctas == 2 && row_tiles * h.tp * div_up(cols, kTileN) > kNarrowRounds * h.sms / 2)
+    return best;
   long long least = -1;
-  for (int bn = kTileN; bn >= step; bn -= step) {
-    const long long tiles = (long long)h.tp * div_up(cols, bn);
-    const long long cost = div_up(tiles, h.sms) * (bn + rows / 2);
+  for (int bn = kTileN; bn >= (ctas == 1 ? step : kTileN / 2); bn -= step) {
+    const long long tiles = row_tiles * h.tp * div_up(cols, bn);
+    const long long cost = div_up(tiles * ctas, h.sms) * (bn + fixed);
     if (least < 0 || cost < least) {
       least = cost;
       best = bn;
@@ -1111,6 +1124,7 @@ GemmArgs gemm_args(const hg_vocab& h, const LossCall& c) {
   a.hit = h.hit;
   a.unscale = h.unscale;
   a.splits = 1;
+  a.bn = kTileN;
 
   return a;
 }
@@ -1118,10 +1132,15 @@ GemmArgs gemm_args(const hg_vocab& h, const LossCall& c) {
 }  // namespace
 
 long long loss_partials(const hg_vocab& h) {
-  // Few rows have the narrowest tiles (tile_width steps by 32).
-  const long long few = (h.max_rows < kSmallRows ? h.max_rows : kSmallRows) * div_up(h.W, 32);
-  const long long many = h.max_rows * div_up(h.W, kTileN);
-  return 2ll * h.tp * (few > many ? few : many);
+  // Few rows may have tiles of 32 columns; many the widest, or half as wide where
+  // kNarrowRounds allow no more tiles than that (tile_width).
+  const long long few = (h.max_rows < kSmallRows ? h.max_rows : kSmallRows) * h.tp * div_up(h.W, 32);
+  const long long many = h.max_rows * h.tp * div_up(h.W, kTileN);
+  long long narrow = h.max_rows * h.tp * div_up(h.W, kTileN / 2);
+  const long long most = 2ll * kTileM * 2 * (kNarrowRounds * h.sms / 2 + h.tp);
+  if (narrow > most) narrow = most;
+  const long long least = few > many ? few : many;
+  return 2 * (least > narrow ? least : narrow);
 }
 
 long long loss_rows_pad(long long rows) { return round_up(rows, 256); }
@@ -1138,7 +1157,9 @@ long long loss_accum_rows(const hg_vocab& h) {
 
 cudaError_t loss(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
   GemmArgs a = gemm_args(h, c);
-  const bool pack = c.N > kSmallRows;
+  // Packing pays where it leaves row tiles out, or where rows straddle lines.
+  const bool lines = (c.ld * 2) % 128 == 0 && reinterpret_cast<uintptr_t>(c.hidden) % 128 == 0;
+  const bool pack = c.N > (lines ? kOneTileRows : kSmallRows);
   a.wcols = h.W;
   a.bn = tile_width(h, c.N, h.W, 32);
   const Shape shape = row_shape(c.N, a.bn);
