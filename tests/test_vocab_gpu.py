@@ -14,8 +14,8 @@ Tolerances. u is the unit roundoff of the matrix's type (2^-8 bf16, 2^-11 fp16,
   its exponential, e p with e = 2 dz + 2^-20 (1 + |lse|); the sum over it by
   a random walk as above; the result is rounded once:
   u |y| + (u + s) (|d| |M|) + e (p |M|) + tiny', s = 8 sqrt(terms) 2^-23.
-  In fp16, d is scaled so that its largest factor is in [2^13, 2^14): the
-  floor of its subnormals, 2^-25 / 2^13 of the largest factor, is tiny'.
+  In fp16, d is scaled so that its largest factor is 2^14: the floor of its
+  subnormals, 2^-25 / 2^13 of the largest factor at most, is tiny'.
 """
 
 import math

@@ -53,6 +53,12 @@ constexpr size_t kFixedSmem = 1024 + 256;  // alignment of the stages, barriers
 constexpr int kSegment = 32;
 constexpr int kGroupM = 8;      // row tiles that share the column tiles of a wave
 constexpr int kSmallRows = 128;  // up to here a tile of one CTA holds all rows
+// Up to here d is kept as the sum of two rounded terms, the second's rows
+// kSplitRows below the first's in prob and packed: they fill rows of a tile that would
+// be empty. A row of grad_hidden or grad_weight is mostly one term of d then, and
+// over few rows the roundings of those few terms do not average out (16 rows:
+// 0.0028 off in bf16, against 0.0017 for the rounding of the result alone).
+constexpr int kSplitRows = 64;
 constexpr int kOneTileRows = 256;  // and a pair's: packing leaves no tile out
 constexpr int kNarrowRounds = 8;
 constexpr int kMaxSplits = 16;
@@ -85,6 +91,8 @@ struct GemmArgs {
   float* hit;
   int splits;         // kDx: parts of the sum over the vocabulary
   int accum_rows;     // rows of one part's slab
+  int used_rows;      // rows of a tile that can hold any of the call's
+  int split;          // d in two terms (kSplitRows)
   int add;            // kDx: add to accum; kDw: add to grad_weight
   const float* unscale;
 };
@@ -366,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   let_successor_start();
   const int packed = a.count ? *a.count : a.rows;  // rows that count
   // At least one row tile is made, so that a piece without rows comes out as zeros.
-  const Work<KIND, CTAS> work(a, packed > 0 ? packed : 1);
+  const Work<KIND, CTAS> work(a, KIND == kDw && a.split ? 2 * kSplitRows : packed > 0 ? packed : 1);
   const int units = (int)gridDim.x / CTAS;
   const int unit = (int)blockIdx.x / CTAS;
   const int row0 = rank * kTileM;             // of this CTA in a tile
@@ -597,26 +605,39 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             tmem_ld_x32(acc_at(c + 32), v[1]);
             if (c + 64 >= a.bn || c + 64 == first + kTileN / 2) release();
             if (t.n * a.bn + c >= a.wc) continue;  // beyond the piece's place in prob
-            unsigned char* dst = store_begin();
+            if (a.split && quarter * 32 >= kSplitRows) continue;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              uint32_t w[4];
-#pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                float d[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int j = q * 8 + h * 2 + e;
-                  const float y = __uint_as_float(v[j >> 5][j & 31]);
-                  d[e] = ex2(fmaf(y, a.c1, -lse)) - (at == c + j ? 1.f : 0.f);
-                  d[e] = on && c + j < valid ? d[e] * scale : 0.f;
-                }
-                w[h] = Elem<T>::pack2(d[0], d[1]);
-              }
-              *reinterpret_cast<uint4*>(dst + ((q ^ (lane & 7)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 64; ++j) {
+              const float y = __uint_as_float(v[j >> 5][j & 31]);
+              const float d = (ex2(fmaf(y, a.c1, -lse)) - (at == c + j ? 1.f : 0.f)) * scale;
+              v[j >> 5][j & 31] = __float_as_uint(on && c + j < valid ? d : 0.f);
             }
-            store_end(&a.out, t.r * a.wc + t.n * a.bn + c, t.m * work.kRows + row0 + quarter * 32, false);
+            const int x = t.r * a.wc + t.n * a.bn + c;
+            const int y = t.m * work.kRows + row0 + quarter * 32;
+            auto store = [&](int row) {
+              unsigned char* dst = store_begin();
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                uint32_t w[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                  const int j = q * 8 + h * 2;
+                  uint32_t& lo = v[j >> 5][j & 31];
+                  uint32_t& hi = v[j >> 5][(j & 31) + 1];
+                  w[h] = Elem<T>::pack2(__uint_as_float(lo), __uint_as_float(hi));
+                  if (CTAS == 1) {  // what the rounding left
+                    const float2 kept = Elem<T>::unpack2(w[h]);
+                    lo = __float_as_uint(__uint_as_float(lo) - kept.x);
+                    hi = __float_as_uint(__uint_as_float(hi) - kept.y);
+                  }
+                }
+                *reinterpret_cast<uint4*>(dst + ((q ^ (lane & 7)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+              }
+              store_end(&a.out, x, row, false);
+            };
+            store(y);
+            if (CTAS == 1 && a.split) store(y + kSplitRows);
           }
         }
       } else if (KIND == kDx) {
@@ -625,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           uint32_t v[32];
           tmem_ld_x32(acc_at(c), v);
           if (c + 32 == first + kTileN / 2) release();
-          if (t.n * kTileN + c >= a.K) continue;
+          // Nobody reads the tile's other rows.
+          if (t.n * kTileN + c >= a.K || (CTAS == 1 && quarter * 32 >= a.used_rows)) continue;
           unsigned char* dst = store_begin();
 #pragma unroll
           for (int q = 0; q < 8; ++q)
@@ -699,7 +721,8 @@ struct PackArgs {
   float* lse_out;
   void* grad_hidden;
   size_t ld_grad;
-  int headroom;  // the largest |row_scale| is brought below 2^headroom (0: kept as it is)
+  float headroom;  // the largest |row_scale| is made this
+  int split;       // every row once more, kSplitRows further on
   void* packed;
   int pitch;
   int* count;
@@ -720,7 +743,8 @@ __device__ __forceinline__ bool unmasked(const PackArgs& a, long long id) {
 // [b * N / G, (b + 1) * N / G); each CTA counts the unmasked rows before its own
 // from the targets (a few bytes per row from L2, against K elements copied), so
 // the CTAs need nothing from one another. The rows up to the next multiple of
-// 64 are filled with zeros: kDw sums 64 rows at a time.
+// 64 are filled with zeros: kDw sums 64 rows at a time. Of few rows (`split`)
+// there are two such blocks.
 __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constant__ PackArgs a) {
   __shared__ int warp_sum[2][kPackWarps];
   __shared__ int kept[kPackWarps];
@@ -738,7 +762,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constan
     if (!unmasked(a, load_id(a.targets, n))) continue;
     ++all;
     if (n < lo) ++before;
-    if (a.headroom != 0) most = fmaxf(most, fabsf(a.grad_loss[n] * a.logit_scale));
+    if (a.grad) most = fmaxf(most, fabsf(a.grad_loss[n] * a.logit_scale));
   }
   for (int o = 16; o; o >>= 1) {
     before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -758,17 +782,13 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constan
     all += warp_sum[1][w];
     most = fmaxf(most, warp_max[w]);
   }
-  // A power of two, so that scaling back is exact.
-  float up = 1.f;
-  if (a.headroom != 0 && most > 0.f && most <= FLT_MAX) {
-    int e;
-    frexpf(most, &e);  // most < 2^e
-    e = a.headroom - e;
-    up = ldexpf(1.f, e < -100 ? -100 : e > 100 ? 100 : e);
-  }
+  // The largest row_scale becomes `headroom`, so that equal upstream gradients (a
+  // mean's) give factors that are exact, and d's largest terms (-1 of the target)
+  // with them.
+  const bool rescale = a.grad && most > 1e-30f && most <= FLT_MAX;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *a.count = all;
-    *a.unscale = 1.f / up;
+    *a.unscale = rescale ? most / a.headroom : 1.f;
   }
 
   const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -810,12 +830,17 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constan
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (v + step * j < vecs) dst[v + step * j] = x[j];
+        if (a.split)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (v + step * j < vecs) dst[kSplitRows * (a.pitch / 8) + v + step * j] = x[j];
       }
       if (part == 0) {
         a.row_of[to] = n;
         a.target[to] = id < a.vocab ? (int)id : -1;
         if (a.grad) {
-          a.row_scale[to] = a.grad_loss[n] * a.logit_scale * up;
+          const float g = a.grad_loss[n] * a.logit_scale;
+          a.row_scale[to] = rescale ? g / most * a.headroom : g;
           a.row_lse[to] = a.lse[n] * kLog2e;
         }
       }
@@ -830,9 +855,10 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constan
       a.lse_out[n] = 0.f;
     }
   }
-  const int end = (int)round_up(all > 0 ? all : 1, 64);
+  const int end = a.split ? 2 * kSplitRows : (int)round_up(all > 0 ? all : 1, 64);
   for (int to = all + (int)blockIdx.x * kPackWarps + warp; to < end; to += (int)G * kPackWarps)
-    for (int v = lane; v < vecs; v += 32) packed[(size_t)to * (a.pitch / 8) + v] = zero;
+    if (!a.split || to < kSplitRows || to >= kSplitRows + all)
+      for (int v = lane; v < vecs; v += 32) packed[(size_t)to * (a.pitch / 8) + v] = zero;
 }
 
 struct MergeArgs {
@@ -899,6 +925,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
 struct FinishArgs {
   const float* accum;
   int splits, accum_rows, K, pitch;
+  int split;  // two rows of accum to a row
   const int* count;
   const int* row_of;
   const float* unscale;
@@ -919,11 +946,14 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
     const int v = (int)(i - (long long)row * vecs);
     float s[8] = {};
     for (int p = 0; p < a.splits; ++p) {
-      const float4* src = reinterpret_cast<const float4*>(
-          a.accum + ((size_t)p * a.accum_rows + row) * a.pitch + (size_t)v * 8);
-      const float4 lo = src[0], hi = src[1];
-      s[0] += lo.x; s[1] += lo.y; s[2] += lo.z; s[3] += lo.w;
-      s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
+      for (int half = 0; half <= a.split; ++half) {
+        const float4* src = reinterpret_cast<const float4*>(
+            a.accum + ((size_t)p * a.accum_rows + row + half * kSplitRows) * a.pitch +
+            (size_t)v * 8);
+        const float4 lo = src[0], hi = src[1];
+        s[0] += lo.x; s[1] += lo.y; s[2] += lo.z; s[3] += lo.w;
+        s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
+      }
     }
     uint4 x;
     x.x = Elem<T>::pack2(s[0] * unscale, s[1] * unscale);
@@ -1200,7 +1230,8 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
   const long long pad = loss_rows_pad(c.N > 0 ? c.N : 1);
   PackArgs p = pack_args(h, c);
   p.grad = 1;
-  p.headroom = h.dtype == HG_FP16 ? 14 : 0;  // |d| < 2^14 * 2, small terms kept off fp16's floor
+  p.headroom = h.dtype == HG_FP16 ? 16384.f : 1.f;  // small terms stay off fp16's floor
+  p.split = c.N <= kSplitRows;
   cudaError_t e =
       launch_dependent(pack_kernel, p, row_blocks(h, c.N), kPackThreads, 0, 1, stream);
   if (e != cudaSuccess) return e;
@@ -1210,12 +1241,13 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
   prob.count = h.count;
   prob.targets = Ids{h.target, 4};
   prob.wc = h.piece_cols;
+  prob.split = p.split;
   GemmArgs dx = prob, dw = prob;
   const uint64_t prob_cols = (uint64_t)h.tp * h.piece_cols;
   const int first = h.piece_cols < h.W ? h.piece_cols : h.W;
   prob.bn = tile_width(h, c.N, first, 64);
   const Shape prob_shape = row_shape(c.N, prob.bn);
-  const Shape dx_shape = row_shape(c.N, kTileN);
+  const Shape dx_shape = row_shape(p.split ? kSplitRows + c.N : c.N, kTileN);
   // Of few rows a tile is a K block or two and a store, and the exchange between the
   // CTAs of a pair costs more than sharing B saves: 16 rows at V=163840, K=7168
   // took 382 us by single CTAs, against 480 us.
@@ -1231,6 +1263,7 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
     dx.idesc = instruction(h.dtype, false, true, kTileM * dx_shape.ctas, kTileN);
     dx.tp = real_shards(h);  // 0 * NaN of a padding shard must not be summed
     splits = dx_splits(h, c.N);
+    dx.used_rows = dx_shape.a_rows;
     dx.accum_rows = slab_rows(c.N);
     if (!encode_weights(h, c.weight, kBlockK, dx.shard) ||
         !encode(&dx.p, h.prob, h.dtype, pad, prob_cols, prob_cols, dx_shape.a_rows) ||
@@ -1266,6 +1299,7 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
   FinishArgs f = {};
   f.accum = h.accum;
   f.splits = splits;
+  f.split = p.split;
   f.accum_rows = dx.accum_rows;
   f.K = h.K;
   f.pitch = h.pitch;
