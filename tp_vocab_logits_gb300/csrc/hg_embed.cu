@@ -41,6 +41,16 @@ __device__ __forceinline__ T* table_row(const Table& t, uint32_t id, int W, int 
   return static_cast<T*>(t.shard[r]) + (size_t)(id - r * (uint32_t)W) * K;
 }
 
+// Store of what this kernel does not read again: evicted first, so that L2 keeps
+// the table's rows that other tokens share (32768 rows 111 -> 109 us).
+template <typename P>
+__device__ __forceinline__ void store_streaming(P* p, const P& x) {
+  if constexpr (sizeof(P) == 16)
+    __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&x));
+  else
+    *p = x;
+}
+
 struct EmbedArgs {
   Table table;
   Ids tokens;
@@ -85,7 +95,7 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(const __grid_cons
 #pragma unroll
       for (int e = 0; e < E; ++e) x[j].v[e] = Elem<T>::down(Elem<T>::up(x[j].v[e]) * a.scale);
     }
-    dst[i] = x[j];
+    store_streaming(dst + i, x[j]);
   }
 }
 
@@ -251,6 +261,73 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
   for (int p = 0; p < a.passes; ++p) sort_pass(a, p, sh, place);
 }
 
+// Few tokens are sorted by counting instead: an entry's place is the number of
+// entries before it in the order of (token, position), which one 32-bit word holds
+// where both fit. Every CTA reads all the tokens and places kRankItems of them,
+// its warps counting over a part of the sequence each: N^2 comparisons, spread over
+// the whole GPU, and no exchange between CTAs. (The gradient of 1000 tokens at K=1024,
+// added to a table, 8.9 us against 15.0 us by the radix sort; of 4000, 20.8 against
+// 17.4 us.)
+constexpr int kRankItems = 32;
+constexpr int kRankThreads = 512;
+constexpr int kRankWarps = kRankThreads / 32;
+constexpr int kMaxRankTokens = 2048;
+
+struct RankArgs {
+  Ids tokens;
+  int N, vocab;
+  int pos_bits;
+  uint32_t* key;
+  int* pos;
+};
+
+__global__ void __launch_bounds__(kRankThreads) rank_kernel(const __grid_constant__ RankArgs a) {
+  wait_for_predecessor();
+  let_successor_start();
+  __shared__ uint4 words[kMaxRankTokens / 4];
+  __shared__ int part[kRankWarps][kRankItems];
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  uint32_t* const word = reinterpret_cast<uint32_t*>(words);
+  const int padded = (int)round_up(a.N, 4);
+  constexpr int kLoads = 8;  // tokens of a thread whose loads are in flight at once
+  for (int i0 = threadIdx.x; i0 < padded; i0 += kLoads * kRankThreads) {
+    long long id[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = i0 + j * kRankThreads;
+      id[j] = i < a.N ? load_id(a.tokens, (size_t)i) : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = i0 + j * kRankThreads;
+      const uint32_t key = (uint32_t)(id[j] >= 0 && id[j] < a.vocab ? id[j] : a.vocab);
+      // The padding comes after every entry.
+      if (i < padded) word[i] = i < a.N ? key << a.pos_bits | (uint32_t)i : 0xffffffffu;
+    }
+  }
+  __syncthreads();
+  const int item = (int)blockIdx.x * kRankItems + lane;
+  const uint32_t mine = item < a.N ? word[item] : 0;
+  const int quads = padded / 4;
+  const int per = (quads + kRankWarps - 1) / kRankWarps;
+  const int end = (warp + 1) * per < quads ? (warp + 1) * per : quads;
+  int before = 0;
+#pragma unroll 4
+  for (int q = warp * per; q < end; ++q) {
+    const uint4 w = words[q];
+    before += (w.x < mine) + (w.y < mine) + (w.z < mine) + (w.w < mine);
+  }
+  part[warp][lane] = before;
+  __syncthreads();
+  if (warp || item >= a.N) return;
+  int to = 0;
+#pragma unroll
+  for (int w = 0; w < kRankWarps; ++w) to += part[w][lane];
+  a.key[to] = mine >> a.pos_bits;
+  a.pos[to] = item;
+}
+
 // ---- zeros where no token points ----------------------------------------------
 
 struct ClearArgs {
@@ -278,7 +355,7 @@ __global__ void __launch_bounds__(kThreads) clear_kernel(const __grid_constant__
   const size_t first = (size_t)block * (kThreads * kClearWords) + threadIdx.x;
 #pragma unroll
   for (int j = 0; j < kClearWords; ++j)
-    if (first + j * kThreads < words) body[first + j * kThreads] = make_uint4(0, 0, 0, 0);
+    if (first + j * kThreads < words) __stcs(body + first + j * kThreads, make_uint4(0, 0, 0, 0));
   if (block == 0 && threadIdx.x < 16) {
     const size_t at = threadIdx.x < 8 ? threadIdx.x * 2 : head + words * 16 + (threadIdx.x - 8) * 2;
     if (at < (threadIdx.x < 8 ? head : a.bytes)) *reinterpret_cast<uint16_t*>(p + at) = 0;
@@ -559,6 +636,22 @@ cudaError_t sort(const hg_vocab& h, const Ids& tokens, int N, int* sorted, cudaS
   a.vocab = h.vocab;
   int bits = 1;
   while ((1ll << bits) <= h.vocab) ++bits;  // keys 0 .. vocab
+  int pos_bits = 1;
+  while ((1ll << pos_bits) < N) ++pos_bits;
+  // The largest word, (vocab, N - 1), stays below the padding's 0xffffffff.
+  if (N > 0 && N <= kMaxRankTokens &&
+      ((unsigned long long)h.vocab << pos_bits | (unsigned)(N - 1)) < 0xffffffffull) {
+    RankArgs r = {};
+    r.tokens = tokens;
+    r.N = N;
+    r.vocab = h.vocab;
+    r.pos_bits = pos_bits;
+    r.key = h.key[0];
+    r.pos = h.pos[0];
+    *sorted = 0;
+    return launch_dependent(rank_kernel, r, (unsigned)div_up(N, kRankItems), kRankThreads, 0, 1,
+                            stream);
+  }
   a.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
   a.digit_bits = (bits + a.passes - 1) / a.passes;
   for (int i = 0; i < 2; ++i) {
@@ -566,10 +659,6 @@ cudaError_t sort(const hg_vocab& h, const Ids& tokens, int N, int* sorted, cudaS
     a.pos[i] = h.pos[i];
   }
   *sorted = (a.passes + 1) & 1;
-  const cudaError_t e = cudaFuncSetAttribute(sort_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)sort_smem(kMaxDigitBits));
-  if (e != cudaSuccess) return e;
   return launch_dependent(sort_kernel, a, kSortCtas, kSortThreads, sort_smem(a.digit_bits),
                           kSortCtas, stream);
 }
@@ -613,6 +702,11 @@ cudaError_t embed(const hg_vocab& h, const Ids& tokens, int N, const void* const
     case HG_FP16: return vec ? embed_as<__half, 8>(a, stream) : embed_as<__half, 1>(a, stream);
     default: return vec ? embed_as<float, 4>(a, stream) : embed_as<float, 1>(a, stream);
   }
+}
+
+cudaError_t embed_prepare() {
+  return cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)sort_smem(kMaxDigitBits));
 }
 
 long long embed_grad_chunks(const hg_vocab& h) {

@@ -1024,12 +1024,23 @@ struct Shape {
 
 template <int KIND, int CTAS, typename T>
 cudaError_t launch_as(const GemmArgs& a, int sms, cudaStream_t stream) {
-  auto* kernel = gemm_kernel<KIND, CTAS, T>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)kMaxSmem);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(kernel, a, (unsigned)(sms / CTAS * CTAS), kThreads, kMaxSmem, CTAS,
-                          stream);
+  return launch_dependent(gemm_kernel<KIND, CTAS, T>, a, (unsigned)(sms / CTAS * CTAS), kThreads,
+                          kMaxSmem, CTAS, stream);
+}
+
+template <int KIND, typename T>
+cudaError_t allow_smem() {
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<KIND, 1, T>, attr, (int)kMaxSmem);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(gemm_kernel<KIND, 2, T>, attr, (int)kMaxSmem);
+}
+
+template <typename T>
+cudaError_t allow_smem_all() {
+  cudaError_t e = allow_smem<kLoss, T>();
+  if (e == cudaSuccess) e = allow_smem<kProb, T>();
+  if (e == cudaSuccess) e = allow_smem<kDx, T>();
+  return e == cudaSuccess ? allow_smem<kDw, T>() : e;
 }
 
 template <int KIND>
@@ -1183,6 +1194,10 @@ long long loss_accum_rows(const hg_vocab& h) {
     if (rows > most) most = rows;
     if (n >= h.max_rows) return most;
   }
+}
+
+cudaError_t loss_prepare(const hg_vocab& h) {
+  return h.dtype == HG_BF16 ? allow_smem_all<__nv_bfloat16>() : allow_smem_all<__half>();
 }
 
 cudaError_t loss(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {

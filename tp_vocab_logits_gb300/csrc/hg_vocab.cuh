@@ -140,6 +140,11 @@ cudaError_t launch_dependent(void (*kernel)(Args), const Args& args, unsigned gr
 constexpr int kRunRows = 32;
 constexpr int kFewRunRows = 8;
 
+// Kernel attributes that the calls need on the current device (the shared memory
+// limits), set once, when a handle is made.
+cudaError_t embed_prepare();
+cudaError_t loss_prepare(const hg_vocab& h);
+
 cudaError_t embed(const hg_vocab& h, const Ids& tokens, int N, const void* const* table,
                   float scale, void* out, size_t ld_out, cudaStream_t stream);
 cudaError_t embed_grad(const hg_vocab& h, const Ids& tokens, int N, const void* grad,

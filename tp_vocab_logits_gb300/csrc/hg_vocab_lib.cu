@@ -127,7 +127,9 @@ int hg_vocab_create(int tp, int shard_cols, int vocab, int hidden, int max_rows,
   h->dtype = dtype;
   h->ops = ops;
   if (cudaGetDevice(&h->device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) {
+      cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
+      ((ops & HG_VOCAB_EMBED_GRAD) && hg::vocab::embed_prepare() != cudaSuccess) ||
+      (loss && hg::vocab::loss_prepare(*h) != cudaSuccess)) {
     delete h;
     return HG_ERR_CUDA;
   }

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Sequence
 
 import torch
@@ -426,6 +427,7 @@ class VocabHandle:
         self.ptr = ptr
         self.tp, self.shard_cols, self.vocab = tp, shard_cols, vocab
         self.hidden, self.max_rows, self.dtype = hidden, max_rows, dtype
+        self.desc = struct.pack("Pqqq", ptr, tp, shard_cols, hidden)  # for _hgcall
 
     @property
     def workspace_bytes(self) -> int:
@@ -434,6 +436,7 @@ class VocabHandle:
     def close(self) -> None:
         if self.ptr:
             ptr, self.ptr = self.ptr, 0
+            self.desc = struct.pack("Pqqq", 0, self.tp, self.shard_cols, self.hidden)
             _check(load().hg_vocab_destroy(ptr), "hg_vocab_destroy")
 
     def __del__(self):
@@ -473,63 +476,80 @@ def hg_vocab_sync(h: VocabHandle, stream=None) -> None:
     _check(load().hg_vocab_sync(h.ptr, _stream_ptr(stream)), "hg_vocab_sync")
 
 
-def _vocab_stream(stream, t: torch.Tensor) -> int:
-    """The raw stream of a call on t's device (the current one by default)."""
-    if stream is None:  # torch.cuda.current_stream() builds two objects to say the same
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    return _stream_ptr(stream)
+# The calls below check their tensors and reach the library in _hgcall (in
+# Python the checks cost more than the launch). Where a check fails there it
+# answers None, and the checks here, which are the same, say which.
+_VOCAB_CALL = None
 
 
-def _vocab_ids(t: torch.Tensor, what: str) -> int:
+def _vocab_call():
+    global _VOCAB_CALL
+    if _VOCAB_CALL is None:
+        lib, mod = load(), _pycall()
+        mod.bind_vocab(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.hg_vocab_embed, lib.hg_vocab_embed_grad, lib.hg_vocab_loss,
+            lib.hg_vocab_loss_grad)], torch.int32, torch.int64, torch.float32,
+            getattr(torch._C, "_cuda_getCurrentRawStream", _current_raw_stream))
+        _VOCAB_CALL = mod
+    return _VOCAB_CALL
+
+
+def _current_raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _vocab_refuse(where: str, *checks) -> None:
+    """Run the checks that _hgcall found wanting; one of them raises."""
+    for check in checks:
+        check()
+    raise ValueError(f"{where}: invalid arguments")
+
+
+def _vocab_ids(t: torch.Tensor, what: str) -> None:
     if not t.is_cuda or t.dtype not in (torch.int32, torch.int64) or t.dim() != 1 \
             or not t.is_contiguous():
         raise ValueError(f"{what}: need a contiguous 1-D int32 or int64 CUDA tensor")
-    return t.shape[0]
 
 
-def _vocab_rows(h: VocabHandle, t: torch.Tensor, n: int, what: str) -> int:
-    """Row distance of a token-side [n, hidden] matrix (rows contiguous)."""
+def _vocab_rows(h: VocabHandle, t: torch.Tensor, n: int, what: str) -> None:
+    """A token-side [n, hidden] matrix (rows contiguous)."""
     if not t.is_cuda or t.dtype != h.dtype:
         raise ValueError(f"{what}: need a CUDA tensor of {h.dtype}, got {t.dtype} on {t.device}")
     if t.shape != (n, h.hidden) or (h.hidden > 1 and t.stride(1) != 1):
         raise ValueError(f"{what}: need [{n}, {h.hidden}] with contiguous rows, got "
                          f"{tuple(t.shape)} with strides {t.stride()}")
-    if n <= 1:
-        return h.hidden
-    ld = t.stride(0)
-    if ld < h.hidden:
-        raise ValueError(f"{what}: rows overlap (row stride {ld})")
-    return ld
+    if n > 1 and t.stride(0) < h.hidden:
+        raise ValueError(f"{what}: rows overlap (row stride {t.stride(0)})")
 
 
-def _vocab_shards(h: VocabHandle, ts: Sequence[torch.Tensor], what: str) -> bytes:
-    """Checked shards as an array of device pointers."""
-    ptrs = _pycall().shard_pointers(ts, h.tp, h.dtype, h.shard_cols, h.hidden)
-    if ptrs is not None:
-        return ptrs
+def _vocab_shards(h: VocabHandle, ts: Sequence[torch.Tensor], what: str) -> None:
+    if not isinstance(ts, (list, tuple)):
+        raise ValueError(f"{what}: need a list of {h.tp} shards")
     if len(ts) != h.tp:
         raise ValueError(f"{what}: expected {h.tp} shards, got {len(ts)}")
     for t in ts:
         if not t.is_cuda or t.dtype != h.dtype:
             raise ValueError(f"{what}: need CUDA tensors of {h.dtype}, got {t.dtype} on {t.device}")
-    raise ValueError(f"{what}: need contiguous [{h.shard_cols}, {h.hidden}] shards, got "
-                     f"{[tuple(t.shape) for t in ts]}")
+        if t.shape != (h.shard_cols, h.hidden) or not t.is_contiguous():
+            raise ValueError(f"{what}: need contiguous [{h.shard_cols}, {h.hidden}], got "
+                             f"{tuple(t.shape)}")
 
 
-def _vocab_floats(t: torch.Tensor, n: int, what: str) -> int:
+def _vocab_floats(t: torch.Tensor, n: int, what: str) -> None:
     if not t.is_cuda or t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what}: need a contiguous float32 CUDA tensor [{n}]")
-    return t.data_ptr()
 
 
 def hg_vocab_embed(h: VocabHandle, tokens: torch.Tensor, table: Sequence[torch.Tensor],
                    out: torch.Tensor, scale: float = 1.0, stream=None) -> None:
     """out[n] = scale * table[tokens[n]]; a token outside [0, vocab) gives zeros."""
-    n = _vocab_ids(tokens, "tokens")
-    ld = _vocab_rows(h, out, n, "out")
-    _check(load().hg_vocab_embed(h.ptr, tokens.data_ptr(), tokens.element_size(), n,
-                                 _vocab_shards(h, table, "table"), scale, out.data_ptr(), ld,
-                                 _vocab_stream(stream, out)), "hg_vocab_embed")
+    st = _vocab_call().vocab_embed(h.desc, h.dtype, tokens, table, out, scale,
+                                   None if stream is None else _stream_ptr(stream))
+    if st is None:
+        _vocab_refuse("hg_vocab_embed", lambda: _vocab_ids(tokens, "tokens"),
+                      lambda: _vocab_shards(h, table, "table"),
+                      lambda: _vocab_rows(h, out, tokens.shape[0], "out"))
+    _check(st, "hg_vocab_embed")
 
 
 def hg_vocab_embed_grad(h: VocabHandle, tokens: torch.Tensor, grad_out: torch.Tensor,
@@ -537,13 +557,14 @@ def hg_vocab_embed_grad(h: VocabHandle, tokens: torch.Tensor, grad_out: torch.Te
                         accumulate: bool = False, stream=None) -> None:
     """grad_table[v] = scale * sum of grad_out[n] over tokens[n] = v (every row
     written), or added to grad_table where accumulate."""
-    n = _vocab_ids(tokens, "tokens")
-    ld = _vocab_rows(h, grad_out, n, "grad_out")
-    _check(load().hg_vocab_embed_grad(h.ptr, tokens.data_ptr(), tokens.element_size(), n,
-                                      grad_out.data_ptr(), ld,
-                                      _vocab_shards(h, grad_table, "grad_table"), scale,
-                                      int(bool(accumulate)), _vocab_stream(stream, grad_out)),
-           "hg_vocab_embed_grad")
+    st = _vocab_call().vocab_embed_grad(h.desc, h.dtype, tokens, grad_out, grad_table, scale,
+                                        accumulate,
+                                        None if stream is None else _stream_ptr(stream))
+    if st is None:
+        _vocab_refuse("hg_vocab_embed_grad", lambda: _vocab_ids(tokens, "tokens"),
+                      lambda: _vocab_rows(h, grad_out, tokens.shape[0], "grad_out"),
+                      lambda: _vocab_shards(h, grad_table, "grad_table"))
+    _check(st, "hg_vocab_embed_grad")
 
 
 def hg_vocab_loss(h: VocabHandle, hidden: torch.Tensor, weight: Sequence[torch.Tensor],
@@ -551,12 +572,15 @@ def hg_vocab_loss(h: VocabHandle, hidden: torch.Tensor, weight: Sequence[torch.T
                   logit_scale: float = 1.0, stream=None) -> None:
     """Per-row softmax cross entropy of logit_scale * hidden @ weight.T and its
     logsumexp, without storing logits. A negative target masks its row."""
-    n = _vocab_ids(targets, "targets")
-    ld = _vocab_rows(h, hidden, n, "hidden")
-    _check(load().hg_vocab_loss(h.ptr, hidden.data_ptr(), ld, _vocab_shards(h, weight, "weight"),
-                                targets.data_ptr(), targets.element_size(), n, logit_scale,
-                                _vocab_floats(loss, n, "loss"), _vocab_floats(lse, n, "lse"),
-                                _vocab_stream(stream, hidden)), "hg_vocab_loss")
+    st = _vocab_call().vocab_loss(h.desc, h.dtype, hidden, weight, targets, loss, lse, logit_scale,
+                                  None if stream is None else _stream_ptr(stream))
+    if st is None:
+        _vocab_refuse("hg_vocab_loss", lambda: _vocab_ids(targets, "targets"),
+                      lambda: _vocab_rows(h, hidden, targets.shape[0], "hidden"),
+                      lambda: _vocab_shards(h, weight, "weight"),
+                      lambda: _vocab_floats(loss, targets.shape[0], "loss"),
+                      lambda: _vocab_floats(lse, targets.shape[0], "lse"))
+    _check(st, "hg_vocab_loss")
 
 
 def hg_vocab_loss_grad(h: VocabHandle, hidden: torch.Tensor, weight: Sequence[torch.Tensor],
@@ -567,13 +591,16 @@ def hg_vocab_loss_grad(h: VocabHandle, hidden: torch.Tensor, weight: Sequence[to
     """Gradient of hg_vocab_loss from its logsumexp and the upstream gradient of
     each row's loss, to grad_hidden and grad_weight (either may be None);
     accumulate adds to what grad_weight holds."""
-    n = _vocab_ids(targets, "targets")
-    ld = _vocab_rows(h, hidden, n, "hidden")
-    ld_grad = h.hidden if grad_hidden is None else _vocab_rows(h, grad_hidden, n, "grad_hidden")
-    _check(load().hg_vocab_loss_grad(
-        h.ptr, hidden.data_ptr(), ld, _vocab_shards(h, weight, "weight"), targets.data_ptr(),
-        targets.element_size(), _vocab_floats(lse, n, "lse"),
-        _vocab_floats(grad_loss, n, "grad_loss"), n, logit_scale,
-        None if grad_hidden is None else grad_hidden.data_ptr(), ld_grad,
-        None if grad_weight is None else _vocab_shards(h, grad_weight, "grad_weight"),
-        int(bool(accumulate)), _vocab_stream(stream, hidden)), "hg_vocab_loss_grad")
+    st = _vocab_call().vocab_loss_grad(h.desc, h.dtype, hidden, weight, targets, lse, grad_loss,
+                                       grad_hidden, grad_weight, logit_scale, accumulate,
+                                       None if stream is None else _stream_ptr(stream))
+    if st is None:
+        n = targets.shape[0]
+        _vocab_refuse("hg_vocab_loss_grad", lambda: _vocab_ids(targets, "targets"),
+                      lambda: _vocab_rows(h, hidden, n, "hidden"),
+                      lambda: _vocab_shards(h, weight, "weight"),
+                      lambda: _vocab_floats(lse, n, "lse"),
+                      lambda: _vocab_floats(grad_loss, n, "grad_loss"),
+                      lambda: grad_hidden is None or _vocab_rows(h, grad_hidden, n, "grad_hidden"),
+                      lambda: grad_weight is None or _vocab_shards(h, grad_weight, "grad_weight"))
+    _check(st, "hg_vocab_loss_grad")
