@@ -1251,6 +1251,39 @@ def run_fused_only(args):
     return 0
 
 
+def run_vocab_only(args):
+    """The vocabulary operators on the cases of perf/operators.py, one JSON line
+    per case: us per call of a loop over three sets of inputs, and the share of
+    the measured HBM and bf16 rates in the case's own bytes and operations."""
+    import torch
+
+    from perf import operators
+    from tp_vocab_logits_gb300 import _build
+    _build.build()
+    torch.cuda.set_device(0)
+    stream = torch.cuda.current_stream()
+    pk = peaks()["hbm_gbs"]
+    with open(os.path.join(ROOT, "MEASURED_PEAKS.json")) as f:
+        bf16 = float(json.load(f)["bf16_tflops"])
+    operators.own = True
+    for case in operators.listed():
+        if not case["op"].startswith(args.vocab_op):
+            continue
+        states = [operators.prepare(case, SEED + k) for k in range(3)]
+        fns = [lambda s=s: operators.run(s) for s in states]
+        work = operators.work(case)
+        calls = int(min(args.calls, max(3, 1e13 / max(work["flops"], 50 * work["bytes"]))))
+        t = time_calls(torch, fns, calls, 3, stream, "timed_vocab") * 1e-3 / calls
+        gbs, tf = work["bytes"] / t / 1e9, work["flops"] / t / 1e12
+        print(json.dumps({"vocab": case["name"], "calls": calls, "us_per_call": round(t * 1e6, 2),
+                          "gbs": round(gbs, 1), "tflops": round(tf, 1),
+                          "hbm_frac": round(gbs / pk, 3),
+                          "bf16_frac": round(tf / bf16, 3)}), flush=True)
+        del states, fns
+        torch.cuda.empty_cache()
+    return 0
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawTextHelpFormatter)
     ap.add_argument("--gpus", type=int, default=1)
@@ -1267,6 +1300,9 @@ def main(argv=None):
     ap.add_argument("--stats", action="store_true",
                     help="hg_gather_stats only (TP8, V=163840), one line per M")
     ap.add_argument("--stats-ms", default="1,4,8")
+    ap.add_argument("--vocab", action="store_true",
+                    help="embedding, loss and their gradients only, one line per case")
+    ap.add_argument("--vocab-op", default="", help="--vocab: operators whose name starts so")
     ap.add_argument("--timeline", action="store_true",
                     help="launch timeline of graph-replayed gathers (TP8, V=163840), one line "
                          "per M")
@@ -1303,6 +1339,8 @@ def main(argv=None):
         return run_fused_only(args)
     if args.stats:
         return run_stats_only(args)
+    if args.vocab:
+        return run_vocab_only(args)
     if args.timeline:
         return run_timeline(args)
     if args.fused_timeline:

@@ -26,7 +26,7 @@ namespace hg {
 namespace vocab {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowAccesses = 4;  // accesses per lane of a unit of the lookup
 constexpr int kLookupThreads = 128;
@@ -463,7 +463,7 @@ __device__ __forceinline__ float* run_slot(const SumArgs& a, long long chunk, in
 }
 
 template <typename T, int E, int U, bool ADD>
-__global__ void __launch_bounds__(kThreads, E == 1 ? 2 : 4)
+__global__ void __launch_bounds__(kThreads, E == 1 ? 4 : 8)
     sum_kernel(const __grid_constant__ SumArgs a) {
   wait_for_predecessor();
   let_successor_start();

@@ -50,7 +50,7 @@ constexpr size_t kFixedSmem = 1024 + 256;  // alignment of the stages, barriers
 // K blocks that kLoss sums in the tensor core before the epilogue adds them up in
 // registers: the tensor core drops the low bits of every step's sum (448 steps
 // at K = 7168 put the logsumexp 1e-6 off), fp32 additions round them.
-constexpr int kSegment = 32;
+constexpr int kSegment = 16;
 constexpr int kGroupM = 8;      // row tiles that share the column tiles of a wave
 constexpr int kSmallRows = 128;  // up to here a tile of one CTA holds all rows
 // Up to here d is kept as the sum of two rounded terms, the second's rows
