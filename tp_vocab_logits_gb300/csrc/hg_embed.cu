@@ -2,8 +2,9 @@
 //
 // Lookup: out[n] = scale * table[tokens[n]], a copy of N rows of K elements
 // bound by memory: each row read and each output written once. One warp moves
-// kRowAccesses accesses per lane of one row, all loads in flight before the
-// first store.
+// A accesses per lane of one row, all loads in flight before the first store:
+// four of 16 bytes, eight of 4 bytes where rows are aligned to that only, else
+// sixteen single elements.
 //
 // Gradient: grad_table[v] (+)= scale * sum of grad[n] over tokens[n] = v. The
 // positions are sorted by token (stable, so that a token's rows come in the
@@ -28,7 +29,6 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRowAccesses = 4;  // accesses per lane of a unit of the lookup
 constexpr int kLookupThreads = 128;
 
 struct Table {
@@ -61,7 +61,7 @@ struct EmbedArgs {
   size_t ld;
 };
 
-template <typename T, int E>
+template <typename T, int E, int A>
 __global__ void __launch_bounds__(kLookupThreads) embed_kernel(const __grid_constant__ EmbedArgs a) {
   wait_for_predecessor();
   let_successor_start();
@@ -69,15 +69,15 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(const __grid_cons
   const long long unit = (long long)blockIdx.x * (kLookupThreads / 32) + (threadIdx.x >> 5);
   const long long n = unit / a.units_per_row;
   if (n >= a.N) return;
-  const int first = (int)(unit - n * a.units_per_row) * (kRowAccesses * 32) + lane;
+  const int first = (int)(unit - n * a.units_per_row) * (A * 32) + lane;
   const int accesses = a.K / E;
   using P = Pack<T, E>;
-  P x[kRowAccesses];
+  P x[A];
   const long long id = load_id(a.tokens, (size_t)n);
   const bool inside = id >= 0 && id < a.vocab;
   const P* src = reinterpret_cast<const P*>(table_row<T>(a.table, inside ? (uint32_t)id : 0, a.W, a.K));
 #pragma unroll
-  for (int j = 0; j < kRowAccesses; ++j) {
+  for (int j = 0; j < A; ++j) {
     const int i = first + j * 32;
     if (inside && i < accesses) {
       x[j] = src[i];
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(const __grid_cons
   }
   P* dst = reinterpret_cast<P*>(static_cast<T*>(a.out) + (size_t)n * a.ld);
 #pragma unroll
-  for (int j = 0; j < kRowAccesses; ++j) {
+  for (int j = 0; j < A; ++j) {
     const int i = first + j * 32;
     if (i >= accesses) continue;
     if (a.scale != 1.f && inside) {
@@ -389,9 +389,9 @@ struct Columns {
   }
 };
 
-// Load where `on`, without a branch: between the loads of a batch a branch cost more
-// than the loads (the tied table's 8192 rows: 230 us of sums, against 90 us
-// without the prefetch of the rows added to).
+// Load where `on`, without a branch; elsewhere the value is undefined. Between the
+// loads of a batch a branch cost more than the loads (the tied table's 8192
+// rows: 230 us of sums, against 90 us without the prefetch of the rows added to).
 template <typename P>
 __device__ __forceinline__ P load_if(const P* p, bool on) {
   P x;
@@ -399,38 +399,24 @@ __device__ __forceinline__ P load_if(const P* p, bool on) {
     uint4 w;
     asm volatile(
         "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n"
-        " mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
         " @q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
-        : "=&r"(w.x), "=&r"(w.y), "=&r"(w.z), "=&r"(w.w)
+        : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
         : "l"(p), "r"((int)on));
     *reinterpret_cast<uint4*>(&x) = w;
   } else if constexpr (sizeof(P) == 4) {
     uint32_t w;
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n mov.b32 %0, 0;\n"
-        " @q ld.global.u32 %0, [%1];\n}"
-        : "=&r"(w)
-        : "l"(p), "r"((int)on));
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n @q ld.global.u32 %0, [%1];\n}"
+                 : "=r"(w)
+                 : "l"(p), "r"((int)on));
     *reinterpret_cast<uint32_t*>(&x) = w;
   } else {
     uint16_t w;
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n mov.b16 %0, 0;\n"
-        " @q ld.global.u16 %0, [%1];\n}"
-        : "=&h"(w)
-        : "l"(p), "r"((int)on));
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n @q ld.global.u16 %0, [%1];\n}"
+                 : "=h"(w)
+                 : "l"(p), "r"((int)on));
     *reinterpret_cast<uint16_t*>(&x) = w;
   }
   return x;
-}
-
-// This lane's columns of a row, where `on`.
-template <typename P, int U>
-__device__ __forceinline__ void load_row(const P* row, bool on, int first, int accesses,
-                                         P (&x)[U]) {
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    x[u] = load_if(row + first + u * 32, on && first + u * 32 < accesses);
 }
 
 template <typename P>
@@ -462,8 +448,11 @@ __device__ __forceinline__ float* run_slot(const SumArgs& a, long long chunk, in
   return a.runs + ((size_t)chunk * 2 + slot) * a.K;
 }
 
+// Sums of the chunks. The resident CTAs per SM are bounds on the registers: with
+// the rows added to in flight as well, 6 (8192 rows at K=7168: 64 us, against 70 us
+// with 5 or 8), else 8.
 template <typename T, int E, int U, bool ADD>
-__global__ void __launch_bounds__(kThreads, E == 1 ? 4 : 8)
+__global__ void __launch_bounds__(kThreads, U > 1 ? 4 : ADD ? 6 : 8)
     sum_kernel(const __grid_constant__ SumArgs a) {
   wait_for_predecessor();
   let_successor_start();
@@ -495,22 +484,33 @@ __global__ void __launch_bounds__(kThreads, E == 1 ? 4 : 8)
   // run that goes on, nor that of one that began earlier.
   const uint32_t my_next = __shfl_down_sync(0xffffffffu, my_key, 1);
   const bool last = lane == rows - 1;
-  const unsigned reals = __ballot_sync(0xffffffffu, real);
+  const int reals = __popc(__ballot_sync(0xffffffffu, real));  // padding sorts to the end
   const unsigned ends = __ballot_sync(0xffffffffu, real && (last || my_next != my_key));
   unsigned finishes = __ballot_sync(0xffffffffu, real && (last ? next : my_next) != my_key);
   if (continued && finishes) finishes &= ~(ends & (0u - ends));
-  for (int i0 = 0; i0 < rows; i0 += kBatch) {
+  // Loads go unguarded: past the columns or the rows they repeat the last one.
+  int column[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    column[u] = first + u * 32 < accesses ? first + u * 32 : accesses - 1;
+  for (int i0 = 0; i0 < reals; i0 += kBatch) {
     P x[kBatch][U], old[kBatch][U];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int i = (i0 + b) & 31;
-      load_row(shfl_pointer(my_src, i), reals >> i & 1, first, accesses, x[b]);
-      if (ADD) load_row<P>(shfl_pointer(my_dst, i), finishes >> i & 1, first, accesses, old[b]);
+      const int i = i0 + b < reals ? i0 + b : reals - 1;
+      const P* src = shfl_pointer(my_src, i);
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[b][u] = src[column[u]];
+      if (ADD) {
+        const P* dst = shfl_pointer(my_dst, i);
+#pragma unroll
+        for (int u = 0; u < U; ++u) old[b][u] = load_if(dst + column[u], finishes >> i & 1);
+      }
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int i = i0 + b;
-      // What was not loaded is zero.
+      if (i >= reals) break;
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -564,7 +564,11 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
   }
   Pack<T, E>* const row = reinterpret_cast<Pack<T, E>*>(table_row<T>(a.table, key, a.W, a.K));
   Pack<T, E> old[U];
-  if (ADD) load_row<Pack<T, E>>(row, true, first, accesses, old);
+  if (ADD) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (first + u * 32 < accesses) old[u] = row[first + u * 32];
+  }
   Columns<T, E, U> sum;
   const Pack<float, E>* src =
       reinterpret_cast<const Pack<float, E>*>(run_slot<T, E, U>(a, chunk, 1));
@@ -593,22 +597,20 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
   write_row<ADD, T, E, U>(row, a.scale, first, accesses, sum, old);
 }
 
-bool vectors(int K, size_t ld, const void* p, const Table& t, int tp, size_t elem) {
-  auto fits = [](size_t v) { return v % 16 == 0; };
-  if (!fits((size_t)K * elem) || !fits(ld * elem) || !fits(reinterpret_cast<uintptr_t>(p)))
-    return false;
-  for (int r = 0; r < tp; ++r)
-    if (!fits(reinterpret_cast<uintptr_t>(t.shard[r]))) return false;
-  return true;
+// Widest access that every row of the matrices allows: 16 bytes, 4, or an element.
+int access_bytes(int K, size_t ld, const void* p, const Table& t, int tp, size_t elem) {
+  size_t bits = (size_t)K * elem | ld * elem | reinterpret_cast<uintptr_t>(p);
+  for (int r = 0; r < tp; ++r) bits |= reinterpret_cast<uintptr_t>(t.shard[r]);
+  return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : (int)elem;
 }
 
-template <typename T, int E>
+template <typename T, int E, int A>
 cudaError_t embed_as(const EmbedArgs& args, cudaStream_t stream) {
   EmbedArgs a = args;
-  a.units_per_row = (int)div_up(a.K / E, kRowAccesses * 32);
+  a.units_per_row = (int)div_up(a.K / E, A * 32);
   const long long blocks = div_up((long long)a.N * a.units_per_row, kLookupThreads / 32);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_dependent(embed_kernel<T, E>, a, (unsigned)blocks, kLookupThreads, 0, 1, stream);
+  return launch_dependent(embed_kernel<T, E, A>, a, (unsigned)blocks, kLookupThreads, 0, 1, stream);
 }
 
 template <typename T, int E, int U, bool ADD>
@@ -695,12 +697,18 @@ cudaError_t embed(const hg_vocab& h, const Ids& tokens, int N, const void* const
   a.scale = scale;
   a.out = out;
   a.ld = ld_out;
-  const bool vec = vectors(h.K, ld_out, out, a.table, h.tp, elem_bytes(h.dtype));
+  const int bytes = access_bytes(h.K, ld_out, out, a.table, h.tp, elem_bytes(h.dtype));
   switch (h.dtype) {
     case HG_BF16:
-      return vec ? embed_as<__nv_bfloat16, 8>(a, stream) : embed_as<__nv_bfloat16, 1>(a, stream);
-    case HG_FP16: return vec ? embed_as<__half, 8>(a, stream) : embed_as<__half, 1>(a, stream);
-    default: return vec ? embed_as<float, 4>(a, stream) : embed_as<float, 1>(a, stream);
+      return bytes == 16  ? embed_as<__nv_bfloat16, 8, 4>(a, stream)
+             : bytes == 4 ? embed_as<__nv_bfloat16, 2, 8>(a, stream)
+                          : embed_as<__nv_bfloat16, 1, 16>(a, stream);
+    case HG_FP16:
+      return bytes == 16  ? embed_as<__half, 8, 4>(a, stream)
+             : bytes == 4 ? embed_as<__half, 2, 8>(a, stream)
+                          : embed_as<__half, 1, 16>(a, stream);
+    default:
+      return bytes == 16 ? embed_as<float, 4, 4>(a, stream) : embed_as<float, 1, 8>(a, stream);
   }
 }
 
@@ -741,17 +749,19 @@ cudaError_t embed_grad(const hg_vocab& h, const Ids& tokens, int N, const void* 
   a.ld = ld_grad;
   a.scale = scale;
   a.runs = h.runs;
-  const bool vec = vectors(h.K, ld_grad, grad, a.table, h.tp, e);
+  const int bytes = access_bytes(h.K, ld_grad, grad, a.table, h.tp, e);
   switch (h.dtype) {
     case HG_BF16:
-      return vec ? sum_for<__nv_bfloat16, 8, 1>(a, accumulate, stream)
-                 : sum_for<__nv_bfloat16, 1, 4>(a, accumulate, stream);
+      return bytes == 16  ? sum_for<__nv_bfloat16, 8, 1>(a, accumulate, stream)
+             : bytes == 4 ? sum_for<__nv_bfloat16, 2, 8>(a, accumulate, stream)
+                          : sum_for<__nv_bfloat16, 1, 8>(a, accumulate, stream);
     case HG_FP16:
-      return vec ? sum_for<__half, 8, 1>(a, accumulate, stream)
-                 : sum_for<__half, 1, 4>(a, accumulate, stream);
+      return bytes == 16  ? sum_for<__half, 8, 1>(a, accumulate, stream)
+             : bytes == 4 ? sum_for<__half, 2, 8>(a, accumulate, stream)
+                          : sum_for<__half, 1, 8>(a, accumulate, stream);
     default:
-      return vec ? sum_for<float, 4, 1>(a, accumulate, stream)
-                 : sum_for<float, 1, 4>(a, accumulate, stream);
+      return bytes == 16 ? sum_for<float, 4, 1>(a, accumulate, stream)
+                         : sum_for<float, 1, 4>(a, accumulate, stream);
   }
 }
 
