@@ -62,6 +62,7 @@ constexpr int kSplitRows = 64;
 constexpr int kOneTileRows = 256;  // and a pair's: packing leaves no tile out
 constexpr int kNarrowRounds = 8;
 constexpr int kMaxSplits = 16;
+constexpr int kMinPartBlocks = 8;  // K blocks of a part: fewer, and joining the parts costs more
 constexpr unsigned long long kTimeoutNs = 4000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -934,34 +935,46 @@ struct FinishArgs {
 };
 
 // grad_hidden: the parts' sums in order, rounded once, to the rows they belong to.
+// A thread has four elements; kBatch parts' loads are in flight at once (one
+// after another, 16 parts took 8 us).
 template <typename T>
 __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ FinishArgs a) {
   wait_for_predecessor();
   let_successor_start();
-  const int vecs = a.K / 8;
-  const long long total = (long long)*a.count * vecs;
+  constexpr int kBatch = 8;
+  const int quads = a.K / 4;
+  const long long total = (long long)*a.count * quads;
   const float unscale = *a.unscale;
+  const int halves = a.split ? 2 : 1;
+  const int parts = a.splits * halves;
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int row = (int)(i / vecs);
-    const int v = (int)(i - (long long)row * vecs);
-    float s[8] = {};
-    for (int p = 0; p < a.splits; ++p) {
-      for (int half = 0; half <= a.split; ++half) {
-        const float4* src = reinterpret_cast<const float4*>(
-            a.accum + ((size_t)p * a.accum_rows + row + half * kSplitRows) * a.pitch +
-            (size_t)v * 8);
-        const float4 lo = src[0], hi = src[1];
-        s[0] += lo.x; s[1] += lo.y; s[2] += lo.z; s[3] += lo.w;
-        s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
+    const int row = (int)(i / quads);
+    const int v = (int)(i - (long long)row * quads);
+    const float* const src = a.accum + (size_t)row * a.pitch + (size_t)v * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < parts; p0 += kBatch) {
+      float4 x[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int p = p0 + j < parts ? p0 + j : parts - 1;
+        const int part = p / halves;
+        const size_t at = (size_t)part * a.accum_rows + (p - part * halves) * kSplitRows;
+        x[j] = *reinterpret_cast<const float4*>(src + at * a.pitch);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (p0 + j >= parts) break;
+        s.x += x[j].x;
+        s.y += x[j].y;
+        s.z += x[j].z;
+        s.w += x[j].w;
       }
     }
-    uint4 x;
-    x.x = Elem<T>::pack2(s[0] * unscale, s[1] * unscale);
-    x.y = Elem<T>::pack2(s[2] * unscale, s[3] * unscale);
-    x.z = Elem<T>::pack2(s[4] * unscale, s[5] * unscale);
-    x.w = Elem<T>::pack2(s[6] * unscale, s[7] * unscale);
-    *reinterpret_cast<uint4*>(static_cast<T*>(a.grad) + (size_t)a.row_of[row] * a.ld +
-                              (size_t)v * 8) = x;
+    uint2 x;
+    x.x = Elem<T>::pack2(s.x * unscale, s.y * unscale);
+    x.y = Elem<T>::pack2(s.z * unscale, s.w * unscale);
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.grad) + (size_t)a.row_of[row] * a.ld +
+                              (size_t)v * 4) = x;
   }
 }
 
@@ -1105,7 +1118,7 @@ int dx_splits(const hg_vocab& h, int N) {
   const long long kb = real_shards(h) * div_up(h.piece_cols < h.W ? h.piece_cols : h.W, kBlockK);
   int best = 1;
   double least = 0;
-  for (int s = 1; s <= kMaxSplits && s <= kb; ++s) {
+  for (int s = 1; s <= kMaxSplits && (s == 1 || s * kMinPartBlocks <= kb); ++s) {
     const double cost = (double)div_up(tiles * s, units) / s;
     if (s == 1 || cost < 0.97 * least) {
       least = cost;
@@ -1323,7 +1336,7 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
   f.unscale = h.unscale;
   f.grad = c.grad_hidden;
   f.ld = c.ld_grad;
-  const long long blocks = div_up((long long)c.N * (h.K / 8), 256);
+  const long long blocks = div_up((long long)c.N * (h.K / 4), 256);
   const unsigned grid = (unsigned)(blocks < 8ll * h.sms ? blocks : 8ll * h.sms);
   return h.dtype == HG_BF16
              ? launch_dependent(finish_kernel<__nv_bfloat16>, f, grid, 256, 0, 1, stream)
