@@ -1109,28 +1109,33 @@ int tile_width(const hg_vocab& h, int N, int cols, int step) {
   return best;
 }
 
-// Parts of the sum over the vocabulary in kDx: the number that keeps the SMs
-// busiest, by at least 3 % over a smaller one.
+// Rows of one of kDx's slabs: whole tiles.
+int slab_rows(int N) {
+  return (int)round_up(N > 0 ? N : 1, kTileM * row_shape(N, kTileN).ctas);
+}
+
+// Parts of the sum over the vocabulary in kDx. More of them fill the last round of
+// tiles better, but each is a slab of fp32 that is written and read again: take
+// the least of the two times together, at about 340 ns for a K block of a tile
+// and the copy rate for the slabs (2048 rows at V=16384, K=4096: 520 us with the
+// one part this chooses, 615 us with the four that fill the rounds best).
 int dx_splits(const hg_vocab& h, int N) {
   const int ctas = row_shape(N, kTileN).ctas;
   const long long tiles = div_up(N > 0 ? N : 1, kTileM * ctas) * div_up(h.K, kTileN);
   const long long units = h.sms / ctas;
-  const long long kb = real_shards(h) * div_up(h.piece_cols < h.W ? h.piece_cols : h.W, kBlockK);
+  const int cols = h.piece_cols < h.W ? h.piece_cols : h.W;
+  const long long kb = real_shards(h) * div_up(cols, kBlockK);
+  const double slab_ns = (double)slab_rows(N) * h.K * 8 / 6800;
   int best = 1;
   double least = 0;
   for (int s = 1; s <= kMaxSplits && (s == 1 || s * kMinPartBlocks <= kb); ++s) {
-    const double cost = (double)div_up(tiles * s, units) / s;
-    if (s == 1 || cost < 0.97 * least) {
-      least = cost;
+    const double ns = (double)div_up(tiles * s, units) / s * kb * 340 + s * slab_ns;
+    if (s == 1 || ns < least) {
+      least = ns;
       best = s;
     }
   }
   return best;
-}
-
-// Rows of one of kDx's slabs: whole tiles.
-int slab_rows(int N) {
-  return (int)round_up(N > 0 ? N : 1, kTileM * row_shape(N, kTileN).ctas);
 }
 
 unsigned row_blocks(const hg_vocab& h, int N) {
