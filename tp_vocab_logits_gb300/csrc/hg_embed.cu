@@ -621,7 +621,7 @@ cudaError_t sum_as(const SumArgs& args, cudaStream_t stream) {
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const cudaError_t e =
       launch_dependent(sum_kernel<T, E, U, ADD>, a, (unsigned)blocks, kThreads, 0, 1, stream);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.chunks == 1) return e;
   return launch_dependent(join_kernel<T, E, U, ADD>, a, (unsigned)blocks, kThreads, 0, 1, stream);
 }
 
@@ -677,7 +677,9 @@ cudaError_t clear(const hg_vocab& h, const Table& table, cudaStream_t stream) {
 
 // Rows of a chunk: kRunRows, but fewer where that leaves too few warps to hide
 // the loads' latency (at 3001 rows of 1001 fp32 the sums took 15 us).
+// The fewest rows are one chunk, and need no join.
 int run_rows(const hg_vocab& h, int N) {
+  if (N <= 2 * kFewRunRows) return 2 * kFewRunRows;
   const long long slices = div_up(h.K, 128);
   const long long enough = 16ll * h.sms;
   return div_up(N, kRunRows) * slices >= enough ? kRunRows : kFewRunRows;
