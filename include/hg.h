@@ -523,7 +523,7 @@ int hg_vocab_sync(hg_vocab *h, hg_stream_t stream);
  *   out         [N, K], row distance ld_out
  *
  * Pointers are aligned to their element; where the table, out and the row
- * distances are 16-byte aligned the rows move as 16-byte vectors. Errors,
+ * distances are 16-byte (or 4-byte) aligned the rows move in such words. Errors,
  * before any device work: HG_ERR_ARG, HG_ERR_ROWS (N above max_rows),
  * HG_ERR_CUDA.
  */
@@ -557,7 +557,8 @@ int hg_vocab_embed_grad(hg_vocab *h, const void *tokens, int id_bytes, int N,
  *                row's hidden state has no effect. One >= vocab gives a NaN loss.
  *   loss, lse    N floats each
  *
- * Products are exact in fp32, accumulated in fp32 on the tensor cores. Errors,
+ * Products are exact in fp32 and accumulated in fp32, 1024 of K at a time on the
+ * tensor cores, whose sums lose low bits, the rest in fp32 additions. Errors,
  * before any device work: HG_ERR_ARG (also: the handle was not created for it),
  * HG_ERR_ROWS (N above max_rows), HG_ERR_CUDA.
  */
@@ -580,8 +581,9 @@ int hg_vocab_loss(hg_vocab *h, const void *hidden, size_t ld_hidden,
  *
  * At least one of the two gradients is wanted. A row whose target is negative or
  * >= vocab has no gradient, and its hidden state no effect. d is rounded to the
- * matrix's type before the two products (its error is that of one rounding
- * per term); both products are summed in fp32 and rounded once. Errors as
+ * matrix's type before the two products (its error is that of one rounding per
+ * term; up to 64 rows it is kept as two rounded terms, and has none to speak
+ * of); both products are summed in fp32 and rounded once. Errors as
  * hg_vocab_loss.
  */
 int hg_vocab_loss_grad(hg_vocab *h, const void *hidden, size_t ld_hidden,

@@ -236,6 +236,51 @@ def test_embed_offsets_beyond_32_bits():
     h.close()
 
 
+@pytest.mark.parametrize("dtype", [bf16, fp16, fp32])
+@pytest.mark.parametrize("K,pad,off", [
+    (706, 0, 0),    # rows aligned to 4 bytes
+    (706, 2, 0), (705, 1, 0),  # odd width in an even row distance
+    (704, 3, 0),    # whole vectors in rows that are not aligned
+    (704, 8, 1),    # an unaligned start
+    (2, 0, 0), (1, 0, 0),
+])
+def test_embed_widths_and_alignments(dtype, K, pad, off):
+    g = gen_of(K + pad + off)
+    N, W, vocab = 37, 20, 39
+    tok = ids_of(g, N, vocab, 0.1)
+    whole, shards = table_of(g, 2, W, K, dtype)
+    big = torch.zeros((N, K + pad + off), device="cuda", dtype=dtype)
+    rows = big[:, off:off + K]
+    h = hg.hg_vocab_create(2, W, K, N, vocab=vocab, dtype=dtype, ops=("embed", "embed_grad"))
+    hg.hg_vocab_embed(h, tok, shards, rows, scale=0.7)
+    want = torch.where((tok >= 0)[:, None], (whole[tok.clamp(min=0)].float() * 0.7).to(dtype),
+                       torch.zeros((), device="cuda", dtype=dtype))
+    assert torch.equal(rows.contiguous(), want)
+    rows.copy_(normal(g, (N, K), 1.0, dtype))
+    for accumulate in (True, False):
+        old = whole.clone()
+        hg.hg_vocab_embed_grad(h, tok, rows, shards, scale=1.1, accumulate=accumulate)
+        check_embed_grad(whole, tok, rows, vocab, 1.1, old if accumulate else None)
+    h.close()
+
+
+@pytest.mark.parametrize("vocab", [2 ** 21 - 1, 2 ** 21 - 2, 1000])
+@pytest.mark.parametrize("N", [9, 16, 17, 2047, 2048, 2049])
+def test_embed_grad_between_the_sorts(N, vocab):
+    """Token counts at which the sort and the chunks change, with vocabularies
+    on both sides of what one word holds."""
+    g = gen_of(N)
+    tok = ids_of(g, N, vocab, 0.1)
+    tok[: N // 3] = vocab - 1
+    tok = tok[torch.randperm(N, generator=g, device="cuda")]
+    grad = normal(g, (N, 12), 1.0, fp32)
+    out = torch.empty((vocab, 12), device="cuda")
+    h = hg.hg_vocab_create(1, vocab, 12, N, dtype=fp32, ops=("embed_grad",))
+    hg.hg_vocab_embed_grad(h, tok, grad, [out])
+    check_embed_grad(out, tok, grad, vocab, 1.0)
+    h.close()
+
+
 # ---- loss ----------------------------------------------------------------------
 
 LOSS = [
@@ -249,6 +294,10 @@ LOSS = [
     (4, 2048, 8192, 512, 1000, bf16, 0.1, 1.0),
     (2, 20480, 40957, 1024, 16, bf16, 0.0, 2.0),
     (8, 640, 5120, 7168, 257, bf16, 0.9, 1.0),
+    (1, 999, 999, 136, 64, bf16, 0.2, 1.0),    # the most rows with d in two terms
+    (1, 999, 999, 136, 65, bf16, 0.2, 1.0),    # and one more
+    (2, 700, 1390, 520, 256, fp16, 0.0, 1.0),  # hidden as it lies, one pair of tiles
+    (16, 90, 1431, 264, 600, bf16, 0.4, 0.5),  # many narrow shards
 ]
 
 
