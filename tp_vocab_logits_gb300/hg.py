@@ -456,7 +456,8 @@ def hg_vocab_create(tp: int, shard_cols: int, hidden: int, max_rows: int, *, voc
     "embed", "embed_grad", "loss", "loss_grad" will be called (each needs its
     own workspace). piece_bytes: see include/hg.h."""
     if dtype not in _VOCAB_TYPES:
-        raise ValueError(f"hg_vocab_create: dtype must be bfloat16, float16 or float32, got {dtype}")
+        raise ValueError("hg_vocab_create: dtype must be bfloat16, float16 or float32, got "
+                         f"{dtype}")
     bits = 0
     for op in ops:
         if op not in _VOCAB_OPS:
