@@ -209,6 +209,16 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
         : "memory");
 }
 
+// One lane of the converged warp, the same one every time: commits track the MMAs
+// that the same thread issued.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -397,25 +407,30 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   const int row0 = rank * kTileM;             // of this CTA in a tile
   const int cols = a.bn / CTAS;              // columns of B in this CTA
 
+  // The warps of the two roles below run whole, on values that are the same in
+  // every lane, and one elected lane issues: what copies and MMAs take as operands
+  // then stays in uniform registers (V=2908, K=4544, 1 row, bound by the 71 K blocks'
+  // issue: 23.0 -> 21.5 us).
   if (warp == 0 || warp == 2) {
-    if (lane == 0) {
-      // The loss of few rows reads the weights once (evict-first: 1 row at V=163840,
-      // K=7168 342 us, against 359 us with the default policy); every other
-      // operand is read again by other tiles.
-      const uint64_t policy = KIND == kLoss && CTAS == 1 && warp == 2 ? policy_evict_first()
-                                                                      : policy_evict_normal();
-      const uint32_t first_full = CTAS == 2 ? in_first_cta(sh->full) : 0;
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int i = unit; i < work.total && ok; i += units) {
-        const Tile t = work.at(a, i);
-        // Coordinates of the tile's rows of A or columns of B; kDx walks the shards.
-        const int at = warp == 0 ? t.m * work.kRows + row0 : t.n * a.bn + rank * cols;
-        int r = KIND == kDx ? t.kb0 / work.per_shard : t.r;
-        int b = KIND == kDx ? t.kb0 - r * work.per_shard : 0;
-        for (int kb = t.kb0; kb < t.kb1; ++kb) {
-          if (!wait_phase(&sh->empty[stage], phase ^ 1u, a.status)) { ok = false; break; }
+    // The loss of few rows reads the weights once (evict-first: 1 row at V=163840,
+    // K=7168 342 us, against 359 us with the default policy); every other
+    // operand is read again by other tiles.
+    const uint64_t policy = KIND == kLoss && CTAS == 1 && warp == 2 ? policy_evict_first()
+                                                                    : policy_evict_normal();
+    const uint32_t first_full = CTAS == 2 ? in_first_cta(sh->full) : 0;
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int i = unit; i < work.total && ok; i += units) {
+      const Tile t = work.at(a, i);
+      // Coordinates of the tile's rows of A or columns of B; kDx walks the shards.
+      const int at = warp == 0 ? t.m * work.kRows + row0 : t.n * a.bn + rank * cols;
+      int r = KIND == kDx ? t.kb0 / work.per_shard : t.r;
+      int b = KIND == kDx ? t.kb0 - r * work.per_shard : 0;
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        ok = __all_sync(0xffffffffu, wait_phase(&sh->empty[stage], phase ^ 1u, a.status));
+        if (!ok) break;
+        if (elect_one()) {
           uint64_t* bar = &sh->full[stage];
           unsigned char* dst = base + (size_t)stage * stage_bytes + (warp == 0 ? 0 : a.a_bytes);
           auto load = [&](int box, const CUtensorMap* tm, int x, int y) {
@@ -445,59 +460,63 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                      KIND == kDx ? a.c0 + b * kBlockK : kb * kBlockK);
             }
           }
-          if (KIND == kDx && ++b == work.per_shard) { b = 0; ++r; }
-          ++issued;
-          if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
-      }
-      // Every copy issued must land before the CTA's shared memory goes: fill j
-      // completes the phase of parity (j / stages) & 1 of stage j % stages (of a
-      // pair, on the first CTA's barriers; the second waits for it at the end).
-      const int last = rank == 0 ? issued - 1 : -1;
-      for (int s = 0; s < a.stages && s <= last; ++s) {
-        const int j = last - (last - s) % a.stages;
-        wait_phase(&sh->full[s], (uint32_t)((j / a.stages) & 1), a.status);
+        if (KIND == kDx && ++b == work.per_shard) { b = 0; ++r; }
+        ++issued;
+        if (++stage == a.stages) { stage = 0; phase ^= 1u; }
       }
     }
+    // Every copy issued must land before the CTA's shared memory goes: fill j
+    // completes the phase of parity (j / stages) & 1 of stage j % stages (of a
+    // pair, on the first CTA's barriers; the second waits for it at the end).
+    const int last = rank == 0 ? issued - 1 : -1;
+    for (int s = 0; s < a.stages && s <= last; ++s) {
+      const int j = last - (last - s) % a.stages;
+      wait_phase(&sh->full[s], (uint32_t)((j / a.stages) & 1), a.status);
+    }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
+      const uint32_t A0 = smem_u32(base), B0 = A0 + a.a_bytes;
+      const uint64_t da0 = KIND == kDw ? smem_desc_mn(A0) : smem_desc_sw128(A0);
+      const uint64_t db0 = KIND == kDw || KIND == kDx ? smem_desc_mn(B0) : smem_desc_sw128(B0);
       for (int i = unit; i < work.total && ok; i += units) {
         const Tile t = work.at(a, i);
         int kb = t.kb0;
         while (kb < t.kb1) {
           const int end = KIND == kLoss && kb + kSegment < t.kb1 ? kb + kSegment : t.kb1;
-          if (!wait_phase(&sh->acc_empty[acc], acc_phase ^ 1u, a.status)) { ok = false; break; }
+          ok = __all_sync(0xffffffffu, wait_phase(&sh->acc_empty[acc], acc_phase ^ 1u, a.status));
+          if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + (uint32_t)(acc * kTileN);
           for (uint32_t accumulate = 0; kb < end; ++kb) {
-            if (!wait_phase(&sh->full[stage], phase, a.status)) { ok = false; break; }
+            ok = __all_sync(0xffffffffu, wait_phase(&sh->full[stage], phase, a.status));
+            if (!ok) break;
             tc_fence_after();
-            const uint32_t A = smem_u32(base) + (uint32_t)stage * stage_bytes;
-            const uint32_t B = A + a.a_bytes;
-            const uint64_t da = KIND == kDw ? smem_desc_mn(A) : smem_desc_sw128(A);
-            const uint64_t db = KIND == kDw || KIND == kDx ? smem_desc_mn(B) : smem_desc_sw128(B);
+            const uint64_t da = da0 + (uint64_t)((uint32_t)stage * (stage_bytes >> 4));
+            const uint64_t db = db0 + (uint64_t)((uint32_t)stage * (stage_bytes >> 4));
             // A step of 16 k: 32 bytes along a K-contiguous row, or 16 rows of 128
             // bytes of an operand with one row per k (the address field counts 16).
             constexpr uint64_t step_a = KIND == kDw ? 128 : 2;
             constexpr uint64_t step_b = KIND == kDw || KIND == kDx ? 128 : 2;
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kBlockK / kMmaK; ++k) {
-              mma_f16<CTAS>(d, da + step_a * k, db + step_b * k, a.idesc, accumulate);
-              accumulate = 1;
+              for (int k = 0; k < kBlockK / kMmaK; ++k)
+                mma_f16<CTAS>(d, da + step_a * k, db + step_b * k, a.idesc, k ? 1u : accumulate);
+              commit<CTAS>(&sh->empty[stage]);
             }
-            commit<CTAS>(&sh->empty[stage]);
+            accumulate = 1;
             if (++stage == a.stages) { stage = 0; phase ^= 1u; }
           }
           if (!ok) break;
-          commit<CTAS>(&sh->acc_full[acc]);
+          if (elect_one()) commit<CTAS>(&sh->acc_full[acc]);
           if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
       }
       // Every MMA issued must complete before the tensor memory is freed.
-      commit<CTAS>(&sh->drain);
+      if (elect_one()) commit<CTAS>(&sh->drain);
       wait_phase(&sh->drain, 0, a.status);
     }
   } else {
