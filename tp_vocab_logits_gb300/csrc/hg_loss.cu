@@ -606,10 +606,14 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
             if (c >= a.bn) continue;
             float mx = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              v[q][j] = c + j < valid ? v[q][j] * a.c1 : -INFINITY;
-              mx = fmaxf(mx, v[q][j]);
+            for (int j = 0; j < 32; ++j) v[q][j] *= a.c1;
+            if (c + 32 > valid) {  // the shard's or the vocabulary's last columns
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (c + j >= valid) v[q][j] = -INFINITY;
             }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, v[q][j]);
             const float now = fmaxf(top, mx);
             // Nothing above -inf yet: ex2(-inf - 0) = 0 adds nothing, and a NaN still shows.
             const float ref = now == -INFINITY ? 0.f : now;
@@ -631,6 +635,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
         } else {
           const float scale = on ? a.row_scale[n] : 0.f;
           const float lse = on ? a.row_lse[n] : 0.f;
+          const bool rows_full = __all_sync(0xffffffffu, on);
           if (!acquire()) break;
           if (first >= a.bn) release();
           for (int c = first; c < a.bn && c < first + kTileN / 2; c += 64) {
@@ -640,11 +645,23 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
             if (c + 64 >= a.bn || c + 64 == first + kTileN / 2) release();
             if (t.n * a.bn + c >= a.wc) continue;  // beyond the piece's place in prob
             if (a.split && quarter * 32 >= kSplitRows) continue;
+            // Four instructions an element where nothing is masked; the target, in one
+            // chunk of a row's hundreds, on its own.
 #pragma unroll
-            for (int j = 0; j < 64; ++j) {
-              const float y = __uint_as_float(v[j >> 5][j & 31]);
-              const float d = (ex2(fmaf(y, a.c1, -lse)) - (at == c + j ? 1.f : 0.f)) * scale;
-              v[j >> 5][j & 31] = __float_as_uint(on && c + j < valid ? d : 0.f);
+            for (int j = 0; j < 64; ++j)
+              v[j >> 5][j & 31] = __float_as_uint(
+                  ex2(fmaf(__uint_as_float(v[j >> 5][j & 31]), a.c1, -lse)) * scale);
+            if (at >= c && at < c + 64) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                if (at == c + j)
+                  v[j >> 5][j & 31] =
+                      __float_as_uint(__uint_as_float(v[j >> 5][j & 31]) - scale);
+            }
+            if (!rows_full || c + 64 > valid) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                if (!on || c + j >= valid) v[j >> 5][j & 31] = 0;
             }
             const int x = t.r * a.wc + t.n * a.bn + c;
             const int y = t.m * work.kRows + row0 + quarter * 32;
