@@ -26,7 +26,7 @@
 // 16.8-17.6 ms. Hence 256 x 256 tiles of a CTA pair, which read the fewest bytes
 // from L2 per product, and two accumulators, so that a tile's epilogue runs beside
 // the next one's products. For few rows reading the weights: the loss of one row
-// 339 us for 2.35 GB (6.9 TB/s), the gradient of 16 rows 1107 us for the weights
+// 329-345 us for 2.35 GB (6.8-7.1 TB/s), the gradient of 16 rows 1105 us for the weights
 // twice and grad_weight once. Hence one CTA per tile, stages that hold only the rows there
 // are, and tile widths that leave every SM the same share of the weights.
 
