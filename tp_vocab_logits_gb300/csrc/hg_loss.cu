@@ -28,7 +28,9 @@
 // the next one's products. For few rows reading the weights: the loss of one row
 // 329-345 us for 2.35 GB (6.8-7.1 TB/s), the gradient of 16 rows 1105 us for the weights
 // twice and grad_weight once. Hence one CTA per tile, stages that hold only the rows there
-// are, and tile widths that leave every SM the same share of the weights.
+// are, and tile widths that leave every SM the same share of the weights. In between,
+// where K is short, the epilogues: 4096 rows at V=32768, K=1024 take 151 us
+// (1815 TFLOP/s), at K=80 a tile's products are a tenth of its epilogue.
 
 #include <cfloat>
 
