@@ -1343,10 +1343,11 @@ GemmArgs gemm_args(const hg_vocab& h, const LossCall& c) {
 long long loss_partials(const hg_vocab& h) {
   // Few rows may have tiles of 32 columns; many the widest, or half as wide where
   // kNarrowRounds allow no more tiles than that (tile_width).
-  const long long few_rows = h.max_rows < kSmallRows ? h.max_rows : kSmallRows;
+  const long long rows = h.max_rows;  // rows * tp passes 32 bits in handles that fit the card
+  const long long few_rows = rows < kSmallRows ? rows : kSmallRows;
   const long long few = few_rows * h.tp * div_up(h.W, 32);
-  const long long many = h.max_rows * h.tp * div_up(h.W, kTileN);
-  long long narrow = h.max_rows * h.tp * div_up(h.W, kTileN / 2);
+  const long long many = rows * h.tp * div_up(h.W, kTileN);
+  long long narrow = rows * h.tp * div_up(h.W, kTileN / 2);
   const long long most = 2ll * kTileM * 2 * (kNarrowRounds * h.sms / 2 + h.tp);
   if (narrow > most) narrow = most;
   const long long least = few > many ? few : many;
