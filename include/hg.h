@@ -466,6 +466,9 @@ int hg_gather_stats(hg_handle *h, const void *const *shard_ptrs, void *const *ou
  *    for the device and may be captured into a CUDA graph. The calls of one
  *    handle share its workspace: issue them on one stream, or order them with
  *    events.
+ *  - The device that was current at hg_vocab_create is current at every call, and
+ *    the stream and all pointers are its: with another one current a call answers
+ *    HG_ERR_ARG before any device work. (hg_vocab_destroy takes any.)
  *  - Results do not depend on timing: the same inputs give the same bits.
  *  - Token and target arrays are device pointers to N signed integers of
  *    id_bytes (4 or 8) bytes each, naturally aligned.
@@ -511,7 +514,8 @@ size_t hg_vocab_workspace_bytes(const hg_vocab *h);
 
 /* Wait for `stream`, then report the device status: HG_OK, HG_ERR_TIMEOUT (a
  * kernel's bounded wait gave up; results of that call are undefined, and the
- * status is cleared by this call) or HG_ERR_CUDA. */
+ * status is cleared by this call), HG_ERR_ARG (NULL, another device current) or
+ * HG_ERR_CUDA. */
 int hg_vocab_sync(hg_vocab *h, hg_stream_t stream);
 
 /*

@@ -88,13 +88,24 @@ bool floats_ok(const float* p, int N) { return N == 0 || (p && aligned(p, 4)); }
 
 int as_status(cudaError_t e) { return e == cudaSuccess ? HG_OK : HG_ERR_CUDA; }
 
+// The handle's workspace and the caller's tensors are of one device: with another
+// one current, the kernels would start there, on pointers it cannot reach.
+int check_device(const hg_vocab* h) {
+  int current = -1;
+  if (cudaGetDevice(&current) != cudaSuccess) {
+    cudaGetLastError();
+    return HG_ERR_CUDA;
+  }
+  return current == h->device ? HG_OK : HG_ERR_ARG;
+}
+
 // Checks that hg_vocab_loss and its gradient share.
 int check_loss(const hg_vocab* h, int op, const void* hidden, size_t ld,
                const void* const* weight, const void* targets, int id_bytes, int N) {
   if (!h || N < 0 || !(h->ops & op) || !shards_ok(h, weight, 16) || !ids_ok(targets, id_bytes, N) ||
       !matrix_ok(h, hidden, ld, 16, 8, N))
     return HG_ERR_ARG;
-  return N > h->max_rows ? HG_ERR_ROWS : HG_OK;
+  return N > h->max_rows ? HG_ERR_ROWS : check_device(h);
 }
 
 }  // namespace
@@ -172,7 +183,8 @@ size_t hg_vocab_workspace_bytes(const hg_vocab* h) { return h ? h->bytes : 0; }
 
 int hg_vocab_sync(hg_vocab* h, hg_stream_t stream) {
   if (!h) return HG_ERR_ARG;
-  int st = 0;
+  int st = check_device(h);
+  if (st != HG_OK) return st;
   if (cudaMemcpyAsync(&st, h->status, sizeof st, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
       cudaStreamSynchronize(stream) != cudaSuccess)
     return HG_ERR_CUDA;
@@ -188,7 +200,8 @@ int hg_vocab_embed(hg_vocab* h, const void* tokens, int id_bytes, int N,
   const size_t e = hg::vocab::elem_bytes(h->dtype);
   if (!shards_ok(h, table_ptrs, e) || !matrix_ok(h, out, ld_out, e, 1, N)) return HG_ERR_ARG;
   if (N > h->max_rows) return HG_ERR_ROWS;
-  if (N == 0) return HG_OK;
+  const int st = check_device(h);
+  if (st != HG_OK || N == 0) return st;
   return as_status(hg::vocab::embed(*h, Ids{tokens, id_bytes}, N, table_ptrs, scale, out, ld_out,
                                     stream));
 }
@@ -202,7 +215,8 @@ int hg_vocab_embed_grad(hg_vocab* h, const void* tokens, int id_bytes, int N,
   if (!shards_ok(h, grad_table_ptrs, e) || !matrix_ok(h, grad_out, ld_grad_out, e, 1, N))
     return HG_ERR_ARG;
   if (N > h->max_rows) return HG_ERR_ROWS;
-  if (N == 0 && accumulate) return HG_OK;
+  const int st = check_device(h);
+  if (st != HG_OK || (N == 0 && accumulate)) return st;
   return as_status(hg::vocab::embed_grad(*h, Ids{tokens, id_bytes}, N, grad_out, ld_grad_out,
                                          grad_table_ptrs, scale, accumulate != 0, stream));
 }
