@@ -506,7 +506,7 @@ enum { HG_VOCAB_EMBED = 1, HG_VOCAB_EMBED_GRAD = 2, HG_VOCAB_LOSS = 4, HG_VOCAB_
 int hg_vocab_create(int tp, int shard_cols, int vocab, int hidden, int max_rows, int dtype,
                     int ops, size_t piece_bytes, hg_vocab **out);
 
-/* Free the handle; waits for the device first. NULL is a no-op. */
+/* Free the handle; waits for its device first, whichever is current. NULL is a no-op. */
 int hg_vocab_destroy(hg_vocab *h);
 
 /* Bytes of device memory the handle holds (0 for NULL). */

@@ -173,10 +173,17 @@ int hg_vocab_create(int tp, int shard_cols, int vocab, int hidden, int max_rows,
 
 int hg_vocab_destroy(hg_vocab* h) {
   if (!h) return HG_OK;
-  int st = as_status(cudaDeviceSynchronize());
-  if (cudaFree(h->base) != cudaSuccess) st = HG_ERR_CUDA;
+  // A handle goes whatever device is current (a collector calls this too), but the
+  // device to wait for is its own.
+  int current = -1;
+  bool ok = cudaGetDevice(&current) == cudaSuccess;
+  const bool away = ok && current != h->device;
+  if (away) ok = cudaSetDevice(h->device) == cudaSuccess;
+  ok = ok && cudaDeviceSynchronize() == cudaSuccess;
+  if (cudaFree(h->base) != cudaSuccess) ok = false;
+  if (away && cudaSetDevice(current) != cudaSuccess) ok = false;
   delete h;
-  return st;
+  return ok ? HG_OK : HG_ERR_CUDA;
 }
 
 size_t hg_vocab_workspace_bytes(const hg_vocab* h) { return h ? h->bytes : 0; }
