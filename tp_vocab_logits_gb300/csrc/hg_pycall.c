@@ -151,11 +151,11 @@ static PyObject *call_call(PyObject *obj, PyObject *args, PyObject *kwds) {
   Py_RETURN_NONE;
 }
 
-/* What the binding's VocabHandle packs into its `desc` (struct module, "Pqqq"):
- * the handle, the shards and their sizes. */
+/* What the binding's VocabHandle packs into its `desc` (struct module, "Pqqqq"):
+ * the handle, the shards, their sizes and their device. */
 typedef struct {
   void *h;
-  long long tp, cols, hidden;
+  long long tp, cols, hidden, device;
 } VocabDesc;
 
 #define MAX_SHARDS 32 /* HG_MAX_TP */
@@ -193,11 +193,17 @@ static int is_true_call(PyObject *t, PyObject *name) {
   return x == Py_True;
 }
 
-/* A CUDA tensor: its type, and its data. */
-static int cuda_tensor(PyObject *t, PyObject **dtype, void **ptr) {
+/* A CUDA tensor of the handle's device: its type, and its data. */
+static int cuda_tensor(PyObject *t, const VocabDesc *d, PyObject **dtype, void **ptr) {
   int ok = is_true_attr(t, g_is_cuda);
   if (ok != 1) return ok;
-  PyObject *x = PyObject_GetAttr(t, g_dtype);
+  PyObject *x = PyObject_CallMethodNoArgs(t, g_get_device);
+  if (!x) return -1;
+  ok = PyLong_AsLongLong(x) == d->device;
+  Py_DECREF(x);
+  if (PyErr_Occurred()) return -1;
+  if (!ok) return 0;
+  x = PyObject_GetAttr(t, g_dtype);
   if (!x) return -1;
   Py_DECREF(x); /* torch's types live as long as torch */
   *dtype = x;
@@ -223,7 +229,7 @@ static int shard_list(PyObject *seq, const VocabDesc *d, PyObject *want, void **
   for (Py_ssize_t i = 0; i < (Py_ssize_t)d->tp; ++i) {
     PyObject *t = PySequence_Fast_GET_ITEM(seq, i), *dtype = NULL;
     long long size[2];
-    int ok = cuda_tensor(t, &dtype, &ptrs[i]);
+    int ok = cuda_tensor(t, d, &dtype, &ptrs[i]);
     if (ok == 1) ok = dtype == want;
     if (ok == 1) ok = read_sizes(PyObject_GetAttr(t, g_shape), size, 2);
     if (ok == 1) ok = size[0] == d->cols && size[1] == d->hidden;
@@ -233,10 +239,10 @@ static int shard_list(PyObject *seq, const VocabDesc *d, PyObject *want, void **
   return 1;
 }
 
-static int id_tensor(PyObject *t, void **ptr, int *bytes, int *n) {
+static int id_tensor(PyObject *t, const VocabDesc *d, void **ptr, int *bytes, int *n) {
   PyObject *dtype = NULL;
   long long size[1];
-  int ok = cuda_tensor(t, &dtype, ptr);
+  int ok = cuda_tensor(t, d, &dtype, ptr);
   if (ok == 1) ok = dtype == g_int64 || dtype == g_int32;
   if (ok == 1) ok = read_sizes(PyObject_GetAttr(t, g_shape), size, 1);
   if (ok == 1) ok = size[0] <= 0x7fffffffLL;
@@ -251,7 +257,7 @@ static int row_tensor(PyObject *t, const VocabDesc *d, PyObject *want, int n, vo
                       size_t *ld) {
   PyObject *dtype = NULL;
   long long size[2], stride[2];
-  int ok = cuda_tensor(t, &dtype, ptr);
+  int ok = cuda_tensor(t, d, &dtype, ptr);
   if (ok == 1) ok = dtype == want;
   if (ok == 1) ok = read_sizes(PyObject_GetAttr(t, g_shape), size, 2);
   if (ok == 1) ok = size[0] == n && size[1] == d->hidden;
@@ -263,10 +269,10 @@ static int row_tensor(PyObject *t, const VocabDesc *d, PyObject *want, int n, vo
   return 1;
 }
 
-static int float_tensor(PyObject *t, int n, void **ptr) {
+static int float_tensor(PyObject *t, const VocabDesc *d, int n, void **ptr) {
   PyObject *dtype = NULL;
   long long size[1];
-  int ok = cuda_tensor(t, &dtype, ptr);
+  int ok = cuda_tensor(t, d, &dtype, ptr);
   if (ok == 1) ok = dtype == g_float32;
   if (ok == 1) ok = read_sizes(PyObject_GetAttr(t, g_shape), size, 1);
   if (ok == 1) ok = size[0] == n;
@@ -274,11 +280,11 @@ static int float_tensor(PyObject *t, int n, void **ptr) {
   return ok;
 }
 
-/* The raw stream: an int, or None for the current one of t's device. */
-static int raw_stream(PyObject *stream, PyObject *t, void **out) {
+/* The raw stream: an int, or None for the current one of the handle's device. */
+static int raw_stream(PyObject *stream, const VocabDesc *d, void **out) {
   PyObject *x = NULL;
   if (stream == Py_None) {
-    PyObject *device = PyObject_CallMethodNoArgs(t, g_get_device);
+    PyObject *device = PyLong_FromLongLong(d->device);
     if (!device) return -1;
     x = PyObject_CallOneArg(g_raw_stream, device);
     Py_DECREF(device);
@@ -319,10 +325,10 @@ static PyObject *vocab_embed(PyObject *m, PyObject *const *a, Py_ssize_t n) {
   int bytes = 0, N = 0, st = 0;
   size_t ld = 0;
   int ok = read_desc(a, n, 7, &d);
-  if (ok == 1) ok = id_tensor(a[2], &ids, &bytes, &N);
+  if (ok == 1) ok = id_tensor(a[2], &d, &ids, &bytes, &N);
   if (ok == 1) ok = shard_list(a[3], &d, a[1], shards);
   if (ok == 1) ok = row_tensor(a[4], &d, a[1], N, &out, &ld);
-  if (ok == 1) ok = raw_stream(a[6], a[4], &stream);
+  if (ok == 1) ok = raw_stream(a[6], &d, &stream);
   if (ok == 1) {
     const double scale = PyFloat_AsDouble(a[5]);
     if (PyErr_Occurred()) return NULL;
@@ -339,10 +345,10 @@ static PyObject *vocab_embed_grad(PyObject *m, PyObject *const *a, Py_ssize_t n)
   int bytes = 0, N = 0, st = 0;
   size_t ld = 0;
   int ok = read_desc(a, n, 8, &d);
-  if (ok == 1) ok = id_tensor(a[2], &ids, &bytes, &N);
+  if (ok == 1) ok = id_tensor(a[2], &d, &ids, &bytes, &N);
   if (ok == 1) ok = row_tensor(a[3], &d, a[1], N, &grad, &ld);
   if (ok == 1) ok = shard_list(a[4], &d, a[1], shards);
-  if (ok == 1) ok = raw_stream(a[7], a[3], &stream);
+  if (ok == 1) ok = raw_stream(a[7], &d, &stream);
   if (ok == 1) {
     const double scale = PyFloat_AsDouble(a[5]);
     const int add = PyObject_IsTrue(a[6]);
@@ -361,12 +367,12 @@ static PyObject *vocab_loss(PyObject *m, PyObject *const *a, Py_ssize_t n) {
   int bytes = 0, N = 0, st = 0;
   size_t ld = 0;
   int ok = read_desc(a, n, 9, &d);
-  if (ok == 1) ok = id_tensor(a[4], &ids, &bytes, &N);
+  if (ok == 1) ok = id_tensor(a[4], &d, &ids, &bytes, &N);
   if (ok == 1) ok = row_tensor(a[2], &d, a[1], N, &hidden, &ld);
   if (ok == 1) ok = shard_list(a[3], &d, a[1], shards);
-  if (ok == 1) ok = float_tensor(a[5], N, &loss);
-  if (ok == 1) ok = float_tensor(a[6], N, &lse);
-  if (ok == 1) ok = raw_stream(a[8], a[2], &stream);
+  if (ok == 1) ok = float_tensor(a[5], &d, N, &loss);
+  if (ok == 1) ok = float_tensor(a[6], &d, N, &lse);
+  if (ok == 1) ok = raw_stream(a[8], &d, &stream);
   if (ok == 1) {
     const double scale = PyFloat_AsDouble(a[7]);
     if (PyErr_Occurred()) return NULL;
@@ -385,14 +391,14 @@ static PyObject *vocab_loss_grad(PyObject *m, PyObject *const *a, Py_ssize_t n) 
   int bytes = 0, N = 0, st = 0;
   size_t ld = 0, ld_grad = 0;
   int ok = read_desc(a, n, 12, &d);
-  if (ok == 1) ok = id_tensor(a[4], &ids, &bytes, &N);
+  if (ok == 1) ok = id_tensor(a[4], &d, &ids, &bytes, &N);
   if (ok == 1) ok = row_tensor(a[2], &d, a[1], N, &hidden, &ld);
   if (ok == 1) ok = shard_list(a[3], &d, a[1], shards);
-  if (ok == 1) ok = float_tensor(a[5], N, &lse);
-  if (ok == 1) ok = float_tensor(a[6], N, &up);
+  if (ok == 1) ok = float_tensor(a[5], &d, N, &lse);
+  if (ok == 1) ok = float_tensor(a[6], &d, N, &up);
   if (ok == 1 && a[7] != Py_None) ok = row_tensor(a[7], &d, a[1], N, &grad, &ld_grad);
   if (ok == 1 && a[8] != Py_None) ok = shard_list(a[8], &d, a[1], grads);
-  if (ok == 1) ok = raw_stream(a[11], a[2], &stream);
+  if (ok == 1) ok = raw_stream(a[11], &d, &stream);
   if (ok == 1) {
     const double scale = PyFloat_AsDouble(a[9]);
     const int add = PyObject_IsTrue(a[10]);

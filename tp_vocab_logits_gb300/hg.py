@@ -423,11 +423,16 @@ class VocabHandle:
     by hg_vocab_destroy on close() or collection."""
 
     def __init__(self, ptr: int, tp: int, shard_cols: int, vocab: int, hidden: int, max_rows: int,
-                 dtype: torch.dtype):
+                 dtype: torch.dtype, device: int = 0):
         self.ptr = ptr
         self.tp, self.shard_cols, self.vocab = tp, shard_cols, vocab
         self.hidden, self.max_rows, self.dtype = hidden, max_rows, dtype
-        self.desc = struct.pack("Pqqq", ptr, tp, shard_cols, hidden)  # for _hgcall
+        self.device = torch.device("cuda", device)
+        self._describe()
+
+    def _describe(self) -> None:
+        self.desc = struct.pack("Pqqqq", self.ptr, self.tp, self.shard_cols, self.hidden,
+                                self.device.index)  # for _hgcall
 
     @property
     def workspace_bytes(self) -> int:
@@ -436,7 +441,7 @@ class VocabHandle:
     def close(self) -> None:
         if self.ptr:
             ptr, self.ptr = self.ptr, 0
-            self.desc = struct.pack("Pqqq", 0, self.tp, self.shard_cols, self.hidden)
+            self._describe()
             _check(load().hg_vocab_destroy(ptr), "hg_vocab_destroy")
 
     def __del__(self):
@@ -454,7 +459,8 @@ def hg_vocab_create(tp: int, shard_cols: int, hidden: int, max_rows: int, *, voc
     matrix in tp shards, for calls of up to max_rows rows. vocab: the real
     vocabulary where the last shards are padded (0: all of it). ops: which of
     "embed", "embed_grad", "loss", "loss_grad" will be called (each needs its
-    own workspace). piece_bytes: see include/hg.h."""
+    own workspace). piece_bytes: see include/hg.h. The handle is of the current
+    device; calls take that device's tensors, and want it current."""
     if dtype not in _VOCAB_TYPES:
         raise ValueError("hg_vocab_create: dtype must be bfloat16, float16 or float32, got "
                          f"{dtype}")
@@ -466,7 +472,8 @@ def hg_vocab_create(tp: int, shard_cols: int, hidden: int, max_rows: int, *, voc
     out = ctypes.c_void_p()
     _check(load().hg_vocab_create(tp, shard_cols, vocab, hidden, max_rows, _VOCAB_TYPES[dtype],
                                   bits, piece_bytes, ctypes.byref(out)), "hg_vocab_create")
-    return VocabHandle(out.value, tp, shard_cols, vocab or tp * shard_cols, hidden, max_rows, dtype)
+    return VocabHandle(out.value, tp, shard_cols, vocab or tp * shard_cols, hidden, max_rows, dtype,
+                       torch.cuda.current_device())
 
 
 def hg_vocab_destroy(h: VocabHandle) -> None:
@@ -506,7 +513,13 @@ def _vocab_refuse(where: str, *checks) -> None:
     raise ValueError(f"{where}: invalid arguments")
 
 
-def _vocab_ids(t: torch.Tensor, what: str) -> None:
+def _vocab_device(h: VocabHandle, t: torch.Tensor, what: str) -> None:
+    if t.is_cuda and t.get_device() != h.device.index:
+        raise ValueError(f"{what}: need a tensor on {h.device}, got one on {t.device}")
+
+
+def _vocab_ids(h: VocabHandle, t: torch.Tensor, what: str) -> None:
+    _vocab_device(h, t, what)
     if not t.is_cuda or t.dtype not in (torch.int32, torch.int64) or t.dim() != 1 \
             or not t.is_contiguous():
         raise ValueError(f"{what}: need a contiguous 1-D int32 or int64 CUDA tensor")
@@ -514,6 +527,7 @@ def _vocab_ids(t: torch.Tensor, what: str) -> None:
 
 def _vocab_rows(h: VocabHandle, t: torch.Tensor, n: int, what: str) -> None:
     """A token-side [n, hidden] matrix (rows contiguous)."""
+    _vocab_device(h, t, what)
     if not t.is_cuda or t.dtype != h.dtype:
         raise ValueError(f"{what}: need a CUDA tensor of {h.dtype}, got {t.dtype} on {t.device}")
     if t.shape != (n, h.hidden) or (h.hidden > 1 and t.stride(1) != 1):
@@ -529,6 +543,7 @@ def _vocab_shards(h: VocabHandle, ts: Sequence[torch.Tensor], what: str) -> None
     if len(ts) != h.tp:
         raise ValueError(f"{what}: expected {h.tp} shards, got {len(ts)}")
     for t in ts:
+        _vocab_device(h, t, what)
         if not t.is_cuda or t.dtype != h.dtype:
             raise ValueError(f"{what}: need CUDA tensors of {h.dtype}, got {t.dtype} on {t.device}")
         if t.shape != (h.shard_cols, h.hidden) or not t.is_contiguous():
@@ -536,7 +551,8 @@ def _vocab_shards(h: VocabHandle, ts: Sequence[torch.Tensor], what: str) -> None
                              f"{tuple(t.shape)}")
 
 
-def _vocab_floats(t: torch.Tensor, n: int, what: str) -> None:
+def _vocab_floats(h: VocabHandle, t: torch.Tensor, n: int, what: str) -> None:
+    _vocab_device(h, t, what)
     if not t.is_cuda or t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what}: need a contiguous float32 CUDA tensor [{n}]")
 
@@ -547,7 +563,7 @@ def hg_vocab_embed(h: VocabHandle, tokens: torch.Tensor, table: Sequence[torch.T
     st = _vocab_call().vocab_embed(h.desc, h.dtype, tokens, table, out, scale,
                                    None if stream is None else _stream_ptr(stream))
     if st is None:
-        _vocab_refuse("hg_vocab_embed", lambda: _vocab_ids(tokens, "tokens"),
+        _vocab_refuse("hg_vocab_embed", lambda: _vocab_ids(h, tokens, "tokens"),
                       lambda: _vocab_shards(h, table, "table"),
                       lambda: _vocab_rows(h, out, tokens.shape[0], "out"))
     _check(st, "hg_vocab_embed")
@@ -562,7 +578,7 @@ def hg_vocab_embed_grad(h: VocabHandle, tokens: torch.Tensor, grad_out: torch.Te
                                         accumulate,
                                         None if stream is None else _stream_ptr(stream))
     if st is None:
-        _vocab_refuse("hg_vocab_embed_grad", lambda: _vocab_ids(tokens, "tokens"),
+        _vocab_refuse("hg_vocab_embed_grad", lambda: _vocab_ids(h, tokens, "tokens"),
                       lambda: _vocab_rows(h, grad_out, tokens.shape[0], "grad_out"),
                       lambda: _vocab_shards(h, grad_table, "grad_table"))
     _check(st, "hg_vocab_embed_grad")
@@ -576,11 +592,11 @@ def hg_vocab_loss(h: VocabHandle, hidden: torch.Tensor, weight: Sequence[torch.T
     st = _vocab_call().vocab_loss(h.desc, h.dtype, hidden, weight, targets, loss, lse, logit_scale,
                                   None if stream is None else _stream_ptr(stream))
     if st is None:
-        _vocab_refuse("hg_vocab_loss", lambda: _vocab_ids(targets, "targets"),
+        _vocab_refuse("hg_vocab_loss", lambda: _vocab_ids(h, targets, "targets"),
                       lambda: _vocab_rows(h, hidden, targets.shape[0], "hidden"),
                       lambda: _vocab_shards(h, weight, "weight"),
-                      lambda: _vocab_floats(loss, targets.shape[0], "loss"),
-                      lambda: _vocab_floats(lse, targets.shape[0], "lse"))
+                      lambda: _vocab_floats(h, loss, targets.shape[0], "loss"),
+                      lambda: _vocab_floats(h, lse, targets.shape[0], "lse"))
     _check(st, "hg_vocab_loss")
 
 
@@ -597,11 +613,11 @@ def hg_vocab_loss_grad(h: VocabHandle, hidden: torch.Tensor, weight: Sequence[to
                                        None if stream is None else _stream_ptr(stream))
     if st is None:
         n = targets.shape[0]
-        _vocab_refuse("hg_vocab_loss_grad", lambda: _vocab_ids(targets, "targets"),
+        _vocab_refuse("hg_vocab_loss_grad", lambda: _vocab_ids(h, targets, "targets"),
                       lambda: _vocab_rows(h, hidden, n, "hidden"),
                       lambda: _vocab_shards(h, weight, "weight"),
-                      lambda: _vocab_floats(lse, n, "lse"),
-                      lambda: _vocab_floats(grad_loss, n, "grad_loss"),
+                      lambda: _vocab_floats(h, lse, n, "lse"),
+                      lambda: _vocab_floats(h, grad_loss, n, "grad_loss"),
                       lambda: grad_hidden is None or _vocab_rows(h, grad_hidden, n, "grad_hidden"),
                       lambda: grad_weight is None or _vocab_shards(h, grad_weight, "grad_weight"))
     _check(st, "hg_vocab_loss_grad")
