@@ -105,3 +105,14 @@ def test_a_tensor_of_another_device_is_refused(reached, call, name):
     with pytest.raises(ValueError, match=f"{name}: need a tensor on cuda:1, got one on cuda:0"):
         CALLS[call](handle(1), **args)
     assert reached == []
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_ids_without_a_length_are_named(reached, call):
+    """A scalar of ids: the binding says so before it asks for its length."""
+    args = arguments(call)
+    what = "tokens" if "tokens" in args else "targets"
+    args[what] = Tensor((), torch.int64)
+    with pytest.raises(ValueError, match=f"{what}: need a contiguous 1-D"):
+        CALLS[call](handle(1), **args)
+    assert reached == []

@@ -612,12 +612,12 @@ def hg_vocab_loss_grad(h: VocabHandle, hidden: torch.Tensor, weight: Sequence[to
                                        grad_hidden, grad_weight, logit_scale, accumulate,
                                        None if stream is None else _stream_ptr(stream))
     if st is None:
-        n = targets.shape[0]
         _vocab_refuse("hg_vocab_loss_grad", lambda: _vocab_ids(h, targets, "targets"),
-                      lambda: _vocab_rows(h, hidden, n, "hidden"),
+                      lambda: _vocab_rows(h, hidden, targets.shape[0], "hidden"),
                       lambda: _vocab_shards(h, weight, "weight"),
-                      lambda: _vocab_floats(h, lse, n, "lse"),
-                      lambda: _vocab_floats(h, grad_loss, n, "grad_loss"),
-                      lambda: grad_hidden is None or _vocab_rows(h, grad_hidden, n, "grad_hidden"),
+                      lambda: _vocab_floats(h, lse, targets.shape[0], "lse"),
+                      lambda: _vocab_floats(h, grad_loss, targets.shape[0], "grad_loss"),
+                      lambda: grad_hidden is None or _vocab_rows(h, grad_hidden, targets.shape[0],
+                                                                 "grad_hidden"),
                       lambda: grad_weight is None or _vocab_shards(h, grad_weight, "grad_weight"))
     _check(st, "hg_vocab_loss_grad")
