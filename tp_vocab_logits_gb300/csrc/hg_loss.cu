@@ -60,9 +60,11 @@ constexpr uint32_t kStageOut = 32 * 128;  // a warp's staged [32 rows x 128 byte
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kFixedSmem = 1024 + 256;  // alignment of the stages, barriers
 
-// K blocks that kLoss sums in the tensor core before the epilogue adds them up in
-// registers: the tensor core drops the low bits of every step's sum (448 steps
-// at K = 7168 put the logsumexp 1e-6 off), fp32 additions round them.
+// K blocks that kLoss and kProb sum in the tensor core before the epilogue adds them
+// up in registers: the tensor core drops the low bits of every step's sum (448 steps
+// at K = 7168 put the logsumexp 1e-6 off), fp32 additions round them. In both, so
+// that the gradient has the loss's own logits: without segments in kProb, logits
+// of one sign (16 rows at V=4096, K=7168, fp16) put every term of d 1.6e-3 off.
 constexpr int kSegment = 16;
 // Row tiles that go through the column tiles together, so that both operands of a
 // round of tiles come from L2 (gradient of 4096 rows: 17.65 ms, 17.96 with 4 and
@@ -313,7 +315,7 @@ struct Tile {
   int kb0, kb1;
 };
 
-template <int KIND, int CTAS>
+template <int KIND, int CTAS, bool LONG>
 struct Work {
   static constexpr int kRows = kTileM * CTAS;  // rows of a tile of the pair
   int mt, nt, total, kb, per_shard;
@@ -342,7 +344,7 @@ struct Work {
   }
   // Parts of a tile's sum over K that the epilogue adds up.
   __device__ __forceinline__ int segments() const {
-    return KIND == kLoss ? (kb + kSegment - 1) / kSegment : 1;
+    return KIND == kLoss || LONG ? (kb + kSegment - 1) / kSegment : 1;
   }
   __device__ __forceinline__ Tile at(const GemmArgs& a, int i) const {
     Tile t;
@@ -378,8 +380,10 @@ struct Work {
 // One CTA (CTAS 1) or a pair (CTAS 2) takes tiles i, i + units, ... A pair's tile
 // is 256 x 256: each CTA holds 128 rows of A and 128 columns of B, one thread
 // of the first issues MMAs that read both, and each CTA's tensor memory holds
-// its 128 rows of the sum.
-template <int KIND, int CTAS, typename T>
+// its 128 rows of the sum. LONG (kProb): K is more than one segment, and the tile is
+// gathered in registers first. With one, d is made straight from the accumulator, 64
+// columns at a time (28 rows at V=3391, K=184, fp16: 23.7 us, gathered first 25.6).
+template <int KIND, int CTAS, typename T, bool LONG = false>
 __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
@@ -428,7 +432,8 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
   let_successor_start();
   const int packed = a.count ? *a.count : a.rows;  // rows that count
   // At least one row tile is made, so that a piece without rows comes out as zeros.
-  const Work<KIND, CTAS> work(a, KIND == kDw && a.split ? 2 * kSplitRows : packed > 0 ? packed : 1);
+  const Work<KIND, CTAS, LONG> work(
+      a, KIND == kDw && a.split ? 2 * kSplitRows : packed > 0 ? packed : 1);
   const int row0 = rank * kTileM;             // of this CTA in a tile
   const int cols = a.bn / CTAS;              // columns of B in this CTA
 
@@ -511,7 +516,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
         const Tile t = work.at(a, i);
         int kb = t.kb0;
         while (kb < t.kb1) {
-          const int end = KIND == kLoss && kb + kSegment < t.kb1 ? kb + kSegment : t.kb1;
+          const int end = (KIND == kLoss || LONG) && kb + kSegment < t.kb1 ? kb + kSegment : t.kb1;
           ok = __all_sync(0xffffffffu, wait_phase(&sh->acc_empty[acc], acc_phase ^ 1u, a.status));
           if (!ok) break;
           tc_fence_after();
@@ -594,6 +599,37 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     };
+    // A tile's sums in this warp's columns, its segments added up in registers.
+    auto gather = [&](float (&v)[2][2][32], int segments) {
+      for (int seg = 0; seg < segments; ++seg) {
+        if (!acquire()) return false;
+        if (seg == 0 && first + kTileN / 2 <= a.bn) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            uint32_t r[2][32];
+            tmem_ld_x64(acc_at(first + s * 64), r[0], r[1]);
+#pragma unroll
+            for (int j = 0; j < 64; ++j) v[s][j >> 5][j & 31] = __uint_as_float(r[j >> 5][j & 31]);
+          }
+        } else {
+          // Sixteen columns at a time: with 32 the registers spilled (loss of 4096 rows
+          // at V=32768, K=1024: 160 against 151 us).
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            if (first + g * 16 >= a.bn) continue;
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(acc_at(first + g * 16), r);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float& sum = v[g >> 2][g >> 1 & 1][(g & 1) * 16 + j];
+              sum = seg ? sum + __uint_as_float(r[j]) : __uint_as_float(r[j]);
+            }
+          }
+        }
+        release();
+      }
+      return true;
+    };
     for (int i = unit; i < work.total; i += units) {
       const Tile t = work.at(a, i);
       if (KIND == kLoss || KIND == kProb) {
@@ -608,39 +644,8 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
         if (on) id = load_id(a.targets, (size_t)n) - ((long long)t.r * a.W + col0);
         const int at = id >= 0 && id < valid ? (int)id : -1;
         if (KIND == kLoss) {
-          float v[4][32];
-          const int segments = work.segments();
-          bool ok = true;
-          for (int seg = 0; seg < segments; ++seg) {
-            ok = acquire();
-            if (!ok) break;
-            if (seg == 0 && first + kTileN / 2 <= a.bn) {
-#pragma unroll
-              for (int q = 0; q < 4; q += 2) {
-                uint32_t r[2][32];
-                tmem_ld_x64(acc_at(first + q * 32), r[0], r[1]);
-#pragma unroll
-                for (int j = 0; j < 64; ++j)
-                  v[q + (j >> 5)][j & 31] = __uint_as_float(r[j >> 5][j & 31]);
-              }
-            } else {
-              // Sixteen columns at a time: with 32 the registers spilled (4096 rows
-              // at V=32768, K=1024: 160 against 151 us).
-#pragma unroll
-              for (int g = 0; g < 8; ++g) {
-                if (first + g * 16 >= a.bn) continue;
-                uint32_t r[16];
-                tmem_ld_32x32b_x16(acc_at(first + g * 16), r);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  float& sum = v[g >> 1][(g & 1) * 16 + j];
-                  sum = seg ? sum + __uint_as_float(r[j]) : __uint_as_float(r[j]);
-                }
-              }
-            }
-            release();
-          }
-          if (!ok) break;
+          float v[2][2][32];
+          if (!gather(v, work.segments())) break;
           float top = -INFINITY, sum = 0.f;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -648,27 +653,27 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
             if (c >= a.bn) continue;
             float mx = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[q][j] *= a.c1;
+            for (int j = 0; j < 32; ++j) v[q >> 1][q & 1][j] *= a.c1;
             if (c + 32 > valid) {  // the shard's or the vocabulary's last columns
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (c + j >= valid) v[q][j] = -INFINITY;
+                if (c + j >= valid) v[q >> 1][q & 1][j] = -INFINITY;
             }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, v[q][j]);
+            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, v[q >> 1][q & 1][j]);
             const float now = fmaxf(top, mx);
             // Nothing above -inf yet: ex2(-inf - 0) = 0 adds nothing, and a NaN still shows.
             const float ref = now == -INFINITY ? 0.f : now;
             float part = 0.f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) part += ex2(v[q][j] - ref);
+            for (int j = 0; j < 32; ++j) part += ex2(v[q >> 1][q & 1][j] - ref);
             sum = sum * ex2(top - ref) + part;
             top = now;
             if (at >= c && at < c + 32) {
               float z = 0.f;
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (at == c + j) z = v[q][j];
+                if (at == c + j) z = v[q >> 1][q & 1][j];
               a.hit[n] = z;
             }
           }
@@ -678,35 +683,13 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
           const float scale = on ? a.row_scale[n] : 0.f;
           const float lse = on ? a.row_lse[n] : 0.f;
           const bool rows_full = __all_sync(0xffffffffu, on);
-          if (!acquire()) break;
-          if (first >= a.bn) release();
-          for (int c = first; c < a.bn && c < first + kTileN / 2; c += 64) {
-            uint32_t v[2][32];
-            tmem_ld_x64(acc_at(c), v[0], v[1]);
-            if (c + 64 >= a.bn || c + 64 == first + kTileN / 2) release();
-            if (t.n * a.bn + c >= a.wc) continue;  // beyond the piece's place in prob
-            if (a.split && quarter * 32 >= kSplitRows) continue;
-            // Four instructions an element where nothing is masked; the target, in one
-            // chunk of a row's hundreds, on its own.
-#pragma unroll
-            for (int j = 0; j < 64; ++j)
-              v[j >> 5][j & 31] = __float_as_uint(
-                  ex2(fmaf(__uint_as_float(v[j >> 5][j & 31]), a.c1, -lse)) * scale);
-            if (at >= c && at < c + 64) {
-#pragma unroll
-              for (int j = 0; j < 64; ++j)
-                if (at == c + j)
-                  v[j >> 5][j & 31] =
-                      __float_as_uint(__uint_as_float(v[j >> 5][j & 31]) - scale);
-            }
-            if (!rows_full || c + 64 > valid) {
-#pragma unroll
-              for (int j = 0; j < 64; ++j)
-                if (!on || c + j >= valid) v[j >> 5][j & 31] = 0;
-            }
+          // 64 columns from c on: the logits in v become d, and are stored.
+          auto emit = [&](int c, float (&v)[2][32]) {
+            if (t.n * a.bn + c >= a.wc) return;  // beyond the piece's place in prob
+            if (a.split && quarter * 32 >= kSplitRows) return;
             const int x = t.r * a.wc + t.n * a.bn + c;
             const int y = t.m * work.kRows + row0 + quarter * 32;
-            auto store = [&](int row) {
+            auto store = [&](int term) {
               unsigned char* dst = store_begin();
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
@@ -714,22 +697,56 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                   const int j = q * 8 + h * 2;
-                  uint32_t& lo = v[j >> 5][j & 31];
-                  uint32_t& hi = v[j >> 5][(j & 31) + 1];
-                  w[h] = Elem<T>::pack2(__uint_as_float(lo), __uint_as_float(hi));
-                  if (CTAS == 1) {  // what the rounding left
+                  float& lo = v[j >> 5][j & 31];
+                  float& hi = v[j >> 5][(j & 31) + 1];
+                  w[h] = Elem<T>::pack2(lo, hi);
+                  if (CTAS == 1 && term == 0) {  // what the rounding left
                     const float2 kept = Elem<T>::unpack2(w[h]);
-                    lo = __float_as_uint(__uint_as_float(lo) - kept.x);
-                    hi = __float_as_uint(__uint_as_float(hi) - kept.y);
+                    lo -= kept.x;
+                    hi -= kept.y;
                   }
                 }
                 *reinterpret_cast<uint4*>(dst + ((q ^ (lane & 7)) << 4)) =
                     make_uint4(w[0], w[1], w[2], w[3]);
               }
-              store_end(&a.out, x, row, false);
+              store_end(&a.out, x, y + term * kSplitRows, false);
             };
-            store(y);
-            if (CTAS == 1 && a.split) store(y + kSplitRows);
+            // Four instructions an element where nothing is masked; the target, in one
+            // chunk of a row's hundreds, on its own.
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+              v[j >> 5][j & 31] = ex2(fmaf(v[j >> 5][j & 31], a.c1, -lse)) * scale;
+            if (at >= c && at < c + 64) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                if (at == c + j) v[j >> 5][j & 31] -= scale;
+            }
+            if (!rows_full || c + 64 > valid) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                if (!on || c + j >= valid) v[j >> 5][j & 31] = 0.f;
+            }
+            store(0);
+            if (CTAS == 1 && a.split) store(1);
+          };
+          if constexpr (LONG) {
+            float v[2][2][32];
+            if (!gather(v, work.segments())) break;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+              if (first + s * 64 < a.bn) emit(first + s * 64, v[s]);
+          } else {
+            if (!acquire()) break;
+            if (first >= a.bn) release();
+            for (int c = first; c < a.bn && c < first + kTileN / 2; c += 64) {
+              uint32_t r[2][32];
+              tmem_ld_x64(acc_at(c), r[0], r[1]);
+              if (c + 64 >= a.bn || c + 64 == first + kTileN / 2) release();
+              float v[2][32];
+#pragma unroll
+              for (int j = 0; j < 64; ++j) v[j >> 5][j & 31] = __uint_as_float(r[j >> 5][j & 31]);
+              emit(c, v);
+            }
           }
         }
       } else if (KIND == kDx) {
@@ -794,9 +811,9 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
   }
 }
 
-template <int KIND, int CTAS, typename T>
+template <int KIND, int CTAS, typename T, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a) {
-  gemm_body<KIND, CTAS, T>(a, (int)blockIdx.x / CTAS, (int)gridDim.x / CTAS);
+  gemm_body<KIND, CTAS, T, LONG>(a, (int)blockIdx.x / CTAS, (int)gridDim.x / CTAS);
 }
 
 // Both gradients of a small piece in one launch, the CTAs shared out between them:
@@ -1150,10 +1167,10 @@ struct Shape {
   int b_cols = kTileN / 2;
 };
 
-template <int KIND, int CTAS, typename T>
+template <int KIND, int CTAS, typename T, bool LONG>
 cudaError_t launch_as(const GemmArgs& a, int sms, cudaStream_t stream) {
-  return launch_dependent(gemm_kernel<KIND, CTAS, T>, a, (unsigned)(sms / CTAS * CTAS), kThreads,
-                          kMaxSmem, CTAS, stream);
+  return launch_dependent(gemm_kernel<KIND, CTAS, T, LONG>, a, (unsigned)(sms / CTAS * CTAS),
+                          kThreads, kMaxSmem, CTAS, stream);
 }
 
 // Units (CTAs or pairs) for the hidden gradient when a piece's two gradients share
@@ -1183,17 +1200,20 @@ cudaError_t launch_both(const BothArgs& a, int sms, cudaStream_t stream) {
                           kMaxSmem, CTAS, stream);
 }
 
-template <int KIND, typename T>
+template <int KIND, typename T, bool LONG = false>
 cudaError_t allow_smem() {
   const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<KIND, 1, T>, attr, (int)kMaxSmem);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(gemm_kernel<KIND, 2, T>, attr, (int)kMaxSmem);
+  const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<KIND, 1, T, LONG>, attr, (int)kMaxSmem);
+  return e != cudaSuccess
+             ? e
+             : cudaFuncSetAttribute(gemm_kernel<KIND, 2, T, LONG>, attr, (int)kMaxSmem);
 }
 
 template <typename T>
 cudaError_t allow_smem_all() {
   cudaError_t e = allow_smem<kLoss, T>();
   if (e == cudaSuccess) e = allow_smem<kProb, T>();
+  if (e == cudaSuccess) e = allow_smem<kProb, T, true>();
   if (e == cudaSuccess) e = allow_smem<kDx, T>();
   if (e == cudaSuccess) e = allow_smem<kDw, T>();
   const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
@@ -1211,15 +1231,15 @@ void stage_layout(const Shape& shape, GemmArgs& a) {
   a.stages = (int)(stages < kMaxStages ? stages : kMaxStages);
 }
 
-template <int KIND>
+template <int KIND, bool LONG = false>
 cudaError_t launch(const hg_vocab& h, const Shape& shape, GemmArgs& a, cudaStream_t stream) {
   stage_layout<KIND>(shape, a);
   const bool bf16 = h.dtype == HG_BF16;
   if (shape.ctas == 2)
-    return bf16 ? launch_as<KIND, 2, __nv_bfloat16>(a, h.sms, stream)
-                : launch_as<KIND, 2, __half>(a, h.sms, stream);
-  return bf16 ? launch_as<KIND, 1, __nv_bfloat16>(a, h.sms, stream)
-              : launch_as<KIND, 1, __half>(a, h.sms, stream);
+    return bf16 ? launch_as<KIND, 2, __nv_bfloat16, LONG>(a, h.sms, stream)
+                : launch_as<KIND, 2, __half, LONG>(a, h.sms, stream);
+  return bf16 ? launch_as<KIND, 1, __nv_bfloat16, LONG>(a, h.sms, stream)
+              : launch_as<KIND, 1, __half, LONG>(a, h.sms, stream);
 }
 
 // The shape of a product whose rows are the call's N: for few rows one CTA per
@@ -1469,7 +1489,8 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
     const int left = h.W - c0;
     prob.c0 = dx.c0 = dw.c0 = c0;
     prob.wcols = dx.wcols = dw.wcols = left < h.piece_cols ? left : h.piece_cols;
-    e = launch<kProb>(h, prob_shape, prob, stream);
+    e = h.K > kSegment * kBlockK ? launch<kProb, true>(h, prob_shape, prob, stream)
+                                 : launch<kProb>(h, prob_shape, prob, stream);
     if (e != cudaSuccess) return e;
     int dx_units = 0;
     if (c.grad_hidden) {
