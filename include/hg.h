@@ -584,10 +584,11 @@ int hg_vocab_loss(hg_vocab *h, const void *hidden, size_t ld_hidden,
  *                    piece of the vocabulary (each element once)
  *
  * At least one of the two gradients is wanted. A row whose target is negative or
- * >= vocab has no gradient, and its hidden state no effect. d is rounded to the
- * matrix's type before the two products (its error is that of one rounding per
- * term; up to 64 rows it is kept as two rounded terms, and has none to speak
- * of); both products are summed in fp32 and rounded once. Errors as
+ * >= vocab has no gradient, and its hidden state no effect. The logits are the loss's
+ * own. d is rounded to the matrix's type before the two products (its error is that of
+ * one rounding per term; up to 64 rows it is kept as two rounded terms, and has none to
+ * speak of); both products are summed as the loss's, 1024 terms at a time on the
+ * tensor cores and these in fp32 additions, and rounded once. Errors as
  * hg_vocab_loss.
  */
 int hg_vocab_loss_grad(hg_vocab *h, const void *hidden, size_t ld_hidden,

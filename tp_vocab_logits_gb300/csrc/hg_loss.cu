@@ -60,11 +60,16 @@ constexpr uint32_t kStageOut = 32 * 128;  // a warp's staged [32 rows x 128 byte
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr size_t kFixedSmem = 1024 + 256;  // alignment of the stages, barriers
 
-// K blocks that kLoss and kProb sum in the tensor core before the epilogue adds them
-// up in registers: the tensor core drops the low bits of every step's sum (448 steps
-// at K = 7168 put the logsumexp 1e-6 off), fp32 additions round them. In both, so
-// that the gradient has the loss's own logits: without segments in kProb, logits
-// of one sign (16 rows at V=4096, K=7168, fp16) put every term of d 1.6e-3 off.
+// K blocks that are summed in the tensor core before the epilogue adds them up in
+// registers: the tensor core drops the low bits of every step's sum, always
+// downwards, and fp32 additions round them. In long sums of one sign that shows:
+// without segments the logsumexp was 1e-6 off at K = 7168 (448 steps); every term of
+// d 1.6e-3 (logits of one sign, 16 rows at V=4096, K=7168, fp16; with kProb cut as
+// kLoss is, the gradient has the loss's own logits); the mean of grad_hidden
+// 4.2e-4 over 65536 columns and of grad_weight 4.0e-4 over 65536 rows, in fp16, whose
+// rounding is 4.9e-4 at most. Now 1e-5. The gradient of 4096 rows at V=163840, K=7168
+// takes 16.3-16.4 ms for it against 16.3 ms, of 2048 rows at V=16384, K=4096 526-529
+// against 515-526 us.
 constexpr int kSegment = 16;
 // Row tiles that go through the column tiles together, so that both operands of a
 // round of tiles come from L2 (gradient of 4096 rows: 17.65 ms, 17.96 with 4 and
@@ -313,9 +318,13 @@ struct Tile {
   int r;      // shard (kDx: part of the sum)
   int index;  // kLoss: vocabulary tile
   int kb0, kb1;
+  // Parts of the sum that the epilogue adds up.
+  __device__ __forceinline__ int segments() const {
+    return (kb1 - kb0 + kSegment - 1) / kSegment;
+  }
 };
 
-template <int KIND, int CTAS, bool LONG>
+template <int KIND, int CTAS>
 struct Work {
   static constexpr int kRows = kTileM * CTAS;  // rows of a tile of the pair
   int mt, nt, total, kb, per_shard;
@@ -341,10 +350,6 @@ struct Work {
       kb = (rows + kBlockK - 1) / kBlockK;
       total = mt * nt;
     }
-  }
-  // Parts of a tile's sum over K that the epilogue adds up.
-  __device__ __forceinline__ int segments() const {
-    return KIND == kLoss || LONG ? (kb + kSegment - 1) / kSegment : 1;
   }
   __device__ __forceinline__ Tile at(const GemmArgs& a, int i) const {
     Tile t;
@@ -380,10 +385,10 @@ struct Work {
 // One CTA (CTAS 1) or a pair (CTAS 2) takes tiles i, i + units, ... A pair's tile
 // is 256 x 256: each CTA holds 128 rows of A and 128 columns of B, one thread
 // of the first issues MMAs that read both, and each CTA's tensor memory holds
-// its 128 rows of the sum. LONG (kProb): K is more than one segment, and the tile is
-// gathered in registers first. With one, d is made straight from the accumulator, 64
-// columns at a time (28 rows at V=3391, K=184, fp16: 23.7 us, gathered first 25.6).
-template <int KIND, int CTAS, typename T, bool LONG = false>
+// its 128 rows of the sum. LONG: tiles of more than one segment, which are gathered in
+// registers first. With one, the accumulator is read and stored a few columns at a
+// time (the gradient of 28 rows at V=3391, K=184, fp16: 23.7 us, d gathered first 25.6).
+template <int KIND, int CTAS, typename T, bool LONG>
 __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
@@ -432,7 +437,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
   let_successor_start();
   const int packed = a.count ? *a.count : a.rows;  // rows that count
   // At least one row tile is made, so that a piece without rows comes out as zeros.
-  const Work<KIND, CTAS, LONG> work(
+  const Work<KIND, CTAS> work(
       a, KIND == kDw && a.split ? 2 * kSplitRows : packed > 0 ? packed : 1);
   const int row0 = rank * kTileM;             // of this CTA in a tile
   const int cols = a.bn / CTAS;              // columns of B in this CTA
@@ -516,7 +521,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
         const Tile t = work.at(a, i);
         int kb = t.kb0;
         while (kb < t.kb1) {
-          const int end = (KIND == kLoss || LONG) && kb + kSegment < t.kb1 ? kb + kSegment : t.kb1;
+          const int end = kb + kSegment < t.kb1 ? kb + kSegment : t.kb1;
           ok = __all_sync(0xffffffffu, wait_phase(&sh->acc_empty[acc], acc_phase ^ 1u, a.status));
           if (!ok) break;
           tc_fence_after();
@@ -645,7 +650,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
         const int at = id >= 0 && id < valid ? (int)id : -1;
         if (KIND == kLoss) {
           float v[2][2][32];
-          if (!gather(v, work.segments())) break;
+          if (!gather(v, t.segments())) break;
           float top = -INFINITY, sum = 0.f;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -731,7 +736,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
           };
           if constexpr (LONG) {
             float v[2][2][32];
-            if (!gather(v, work.segments())) break;
+            if (!gather(v, t.segments())) break;
 #pragma unroll
             for (int s = 0; s < 2; ++s)
               if (first + s * 64 < a.bn) emit(first + s * 64, v[s]);
@@ -750,13 +755,9 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
           }
         }
       } else if (KIND == kDx) {
-        if (!acquire()) break;
-        for (int c = first; c < first + kTileN / 2; c += 32) {
-          uint32_t v[32];
-          tmem_ld_x32(acc_at(c), v);
-          if (c + 32 == first + kTileN / 2) release();
+        auto emit = [&](int c, uint32_t (&v)[32]) {
           // Nobody reads the tile's other rows.
-          if (t.n * kTileN + c >= a.K || (CTAS == 1 && quarter * 32 >= a.used_rows)) continue;
+          if (t.n * kTileN + c >= a.K || (CTAS == 1 && quarter * 32 >= a.used_rows)) return;
           unsigned char* dst = store_begin();
 #pragma unroll
           for (int q = 0; q < 8; ++q)
@@ -764,15 +765,30 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
                 make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
           const int y = t.r * a.accum_rows + t.m * work.kRows + row0 + quarter * 32;
           store_end(&a.out, t.n * kTileN + c, y, a.add != 0);
+        };
+        if constexpr (LONG) {
+          float v[2][2][32];
+          if (!gather(v, t.segments())) break;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t r[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(v[q >> 1][q & 1][j]);
+            emit(first + q * 32, r);
+          }
+        } else {
+          if (!acquire()) break;
+          for (int c = first; c < first + kTileN / 2; c += 32) {
+            uint32_t r[32];
+            tmem_ld_x32(acc_at(c), r);
+            if (c + 32 == first + kTileN / 2) release();
+            emit(c, r);
+          }
         }
       } else {
-        if (!acquire()) break;
-        for (int c = first; c < first + kTileN / 2; c += 64) {
-          uint32_t v[2][32];
-          tmem_ld_x64(acc_at(c), v[0], v[1]);
-          if (c + 64 == first + kTileN / 2) release();
+        auto emit = [&](int c, float (&v)[2][32]) {
           const int y = a.c0 + t.m * work.kRows + row0 + quarter * 32;
-          if (t.n * kTileN + c >= a.K || y >= a.W) continue;
+          if (t.n * kTileN + c >= a.K || y >= a.W) return;
           unsigned char* dst = store_begin();
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
@@ -780,13 +796,29 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               const int j = q * 8 + h * 2;
-              w[h] = Elem<T>::pack2(__uint_as_float(v[j >> 5][j & 31]) * unscale,
-                                    __uint_as_float(v[j >> 5][(j & 31) + 1]) * unscale);
+              w[h] = Elem<T>::pack2(v[j >> 5][j & 31] * unscale, v[j >> 5][(j & 31) + 1] * unscale);
             }
             *reinterpret_cast<uint4*>(dst + ((q ^ (lane & 7)) << 4)) =
                 make_uint4(w[0], w[1], w[2], w[3]);
           }
           store_end(&a.shard[t.r], t.n * kTileN + c, y, a.add != 0);
+        };
+        if constexpr (LONG) {
+          float v[2][2][32];
+          if (!gather(v, t.segments())) break;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) emit(first + s * 64, v[s]);
+        } else {
+          if (!acquire()) break;
+          for (int c = first; c < first + kTileN / 2; c += 64) {
+            uint32_t r[2][32];
+            tmem_ld_x64(acc_at(c), r[0], r[1]);
+            if (c + 64 == first + kTileN / 2) release();
+            float v[2][32];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) v[j >> 5][j & 31] = __uint_as_float(r[j >> 5][j & 31]);
+            emit(c, v);
+          }
         }
       }
     }
@@ -824,14 +856,14 @@ struct BothArgs {
   int dx_units;
 };
 
-template <int CTAS, typename T>
+template <int CTAS, typename T, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) both_kernel(const __grid_constant__ BothArgs a) {
   const int unit = (int)blockIdx.x / CTAS;
   const int units = (int)gridDim.x / CTAS;
   if (unit < a.dx_units)
-    gemm_body<kDx, CTAS, T>(a.dx, unit, a.dx_units);
+    gemm_body<kDx, CTAS, T, LONG>(a.dx, unit, a.dx_units);
   else
-    gemm_body<kDw, CTAS, T>(a.dw, unit - a.dx_units, units - a.dx_units);
+    gemm_body<kDw, CTAS, T, LONG>(a.dw, unit - a.dx_units, units - a.dx_units);
 }
 
 // ---- rows ----------------------------------------------------------------------
@@ -1194,31 +1226,30 @@ int both_units(const hg_vocab& h, const GemmArgs& dx, const GemmArgs& dw, int N,
   return (int)(n < 1 ? 1 : n < units ? n : units - 1);
 }
 
-template <int CTAS, typename T>
+template <int CTAS, typename T, bool LONG>
 cudaError_t launch_both(const BothArgs& a, int sms, cudaStream_t stream) {
-  return launch_dependent(both_kernel<CTAS, T>, a, (unsigned)(sms / CTAS * CTAS), kThreads,
+  return launch_dependent(both_kernel<CTAS, T, LONG>, a, (unsigned)(sms / CTAS * CTAS), kThreads,
                           kMaxSmem, CTAS, stream);
 }
 
-template <int KIND, typename T, bool LONG = false>
-cudaError_t allow_smem() {
-  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<KIND, 1, T, LONG>, attr, (int)kMaxSmem);
-  return e != cudaSuccess
-             ? e
-             : cudaFuncSetAttribute(gemm_kernel<KIND, 2, T, LONG>, attr, (int)kMaxSmem);
-}
-
-template <typename T>
+template <int CTAS, typename T>
 cudaError_t allow_smem_all() {
-  cudaError_t e = allow_smem<kLoss, T>();
-  if (e == cudaSuccess) e = allow_smem<kProb, T>();
-  if (e == cudaSuccess) e = allow_smem<kProb, T, true>();
-  if (e == cudaSuccess) e = allow_smem<kDx, T>();
-  if (e == cudaSuccess) e = allow_smem<kDw, T>();
-  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(both_kernel<1, T>, attr, (int)kMaxSmem);
-  return e == cudaSuccess ? cudaFuncSetAttribute(both_kernel<2, T>, attr, (int)kMaxSmem) : e;
+  const void* const kernels[] = {
+      (const void*)gemm_kernel<kLoss, CTAS, T, true>,
+      (const void*)gemm_kernel<kProb, CTAS, T, false>,
+      (const void*)gemm_kernel<kProb, CTAS, T, true>,
+      (const void*)gemm_kernel<kDx, CTAS, T, false>,
+      (const void*)gemm_kernel<kDx, CTAS, T, true>,
+      (const void*)gemm_kernel<kDw, CTAS, T, false>,
+      (const void*)gemm_kernel<kDw, CTAS, T, true>,
+      (const void*)both_kernel<CTAS, T, false>,
+      (const void*)both_kernel<CTAS, T, true>};
+  for (const void* k : kernels) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 template <int KIND>
@@ -1231,8 +1262,8 @@ void stage_layout(const Shape& shape, GemmArgs& a) {
   a.stages = (int)(stages < kMaxStages ? stages : kMaxStages);
 }
 
-template <int KIND, bool LONG = false>
-cudaError_t launch(const hg_vocab& h, const Shape& shape, GemmArgs& a, cudaStream_t stream) {
+template <int KIND, bool LONG>
+cudaError_t launch_cut(const hg_vocab& h, const Shape& shape, GemmArgs& a, cudaStream_t stream) {
   stage_layout<KIND>(shape, a);
   const bool bf16 = h.dtype == HG_BF16;
   if (shape.ctas == 2)
@@ -1240,6 +1271,24 @@ cudaError_t launch(const hg_vocab& h, const Shape& shape, GemmArgs& a, cudaStrea
                 : launch_as<KIND, 2, __half, LONG>(a, h.sms, stream);
   return bf16 ? launch_as<KIND, 1, __nv_bfloat16, LONG>(a, h.sms, stream)
               : launch_as<KIND, 1, __half, LONG>(a, h.sms, stream);
+}
+
+// `blocks`: K blocks of a tile, at most.
+template <int KIND>
+cudaError_t launch(const hg_vocab& h, const Shape& shape, GemmArgs& a, long long blocks,
+                   cudaStream_t stream) {
+  if constexpr (KIND != kLoss)
+    if (blocks <= kSegment) return launch_cut<KIND, false>(h, shape, a, stream);
+  return launch_cut<KIND, true>(h, shape, a, stream);
+}
+
+template <bool LONG>
+cudaError_t launch_both_cut(const hg_vocab& h, int ctas, const BothArgs& a, cudaStream_t stream) {
+  if (h.dtype == HG_BF16)
+    return ctas == 2 ? launch_both<2, __nv_bfloat16, LONG>(a, h.sms, stream)
+                     : launch_both<1, __nv_bfloat16, LONG>(a, h.sms, stream);
+  return ctas == 2 ? launch_both<2, __half, LONG>(a, h.sms, stream)
+                   : launch_both<1, __half, LONG>(a, h.sms, stream);
 }
 
 // The shape of a product whose rows are the call's N: for few rows one CTA per
@@ -1387,7 +1436,10 @@ long long loss_accum_rows(const hg_vocab& h) {
 }
 
 cudaError_t loss_prepare(const hg_vocab& h) {
-  return h.dtype == HG_BF16 ? allow_smem_all<__nv_bfloat16>() : allow_smem_all<__half>();
+  const bool bf16 = h.dtype == HG_BF16;
+  const cudaError_t e = bf16 ? allow_smem_all<1, __nv_bfloat16>() : allow_smem_all<1, __half>();
+  if (e != cudaSuccess) return e;
+  return bf16 ? allow_smem_all<2, __nv_bfloat16>() : allow_smem_all<2, __half>();
 }
 
 cudaError_t loss(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
@@ -1419,7 +1471,7 @@ cudaError_t loss(const hg_vocab& h, const LossCall& c, cudaStream_t stream) {
     if (!encode(&a.x, c.hidden, h.dtype, c.N, h.K, c.ld, shape.a_rows))
       return cudaErrorInvalidValue;
   }
-  e = launch<kLoss>(h, shape, a, stream);
+  e = launch<kLoss>(h, shape, a, div_up(h.K, kBlockK), stream);
   if (e != cudaSuccess) return e;
   m.partial = h.partial;
   m.tiles = a.tiles;
@@ -1485,19 +1537,21 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
         !encode(&dw.x, h.packed, h.dtype, pad, h.K, h.pitch, kBlockK))
       return cudaErrorInvalidValue;
   }
+  const long long dw_blocks = div_up(p.split ? 2 * kSplitRows : c.N, kBlockK);
   for (int c0 = 0; c0 < h.W; c0 += h.piece_cols) {
     const int left = h.W - c0;
     prob.c0 = dx.c0 = dw.c0 = c0;
     prob.wcols = dx.wcols = dw.wcols = left < h.piece_cols ? left : h.piece_cols;
-    e = h.K > kSegment * kBlockK ? launch<kProb, true>(h, prob_shape, prob, stream)
-                                 : launch<kProb>(h, prob_shape, prob, stream);
+    e = launch<kProb>(h, prob_shape, prob, div_up(h.K, kBlockK), stream);
     if (e != cudaSuccess) return e;
     int dx_units = 0;
+    long long dx_blocks = 0;  // K blocks of a part
     if (c.grad_hidden) {
       dx.add = c0 > 0;
       // A short last piece may have fewer K blocks than parts: each part has one.
       const int kb = dx.tp * (int)div_up(dx.wcols, kBlockK);
       dx.splits = splits < kb ? splits : kb;
+      dx_blocks = div_up(kb, dx.splits);
       if (c.grad_weight && c.N > 0) dx_units = both_units(h, dx, dw, c.N, dx_shape.ctas);
     }
     if (dx_units) {
@@ -1507,14 +1561,12 @@ cudaError_t loss_grad(const hg_vocab& h, const LossCall& c, cudaStream_t stream)
       both.dx = dx;
       both.dw = dw;
       both.dx_units = dx_units;
-      const bool bf16 = h.dtype == HG_BF16;
-      e = dx_shape.ctas == 2 ? (bf16 ? launch_both<2, __nv_bfloat16>(both, h.sms, stream)
-                                     : launch_both<2, __half>(both, h.sms, stream))
-                             : (bf16 ? launch_both<1, __nv_bfloat16>(both, h.sms, stream)
-                                     : launch_both<1, __half>(both, h.sms, stream));
+      e = dx_blocks > kSegment || dw_blocks > kSegment
+              ? launch_both_cut<true>(h, dx_shape.ctas, both, stream)
+              : launch_both_cut<false>(h, dx_shape.ctas, both, stream);
     } else {
-      if (c.grad_hidden) e = launch<kDx>(h, dx_shape, dx, stream);
-      if (e == cudaSuccess && c.grad_weight) e = launch<kDw>(h, dw_shape, dw, stream);
+      if (c.grad_hidden) e = launch<kDx>(h, dx_shape, dx, dx_blocks, stream);
+      if (e == cudaSuccess && c.grad_weight) e = launch<kDw>(h, dw_shape, dw, dw_blocks, stream);
     }
     if (e != cudaSuccess) return e;
   }
