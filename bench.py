@@ -63,8 +63,9 @@ def peaks() -> dict:
     if os.path.exists(p):
         with open(p) as f:
             d = json.load(f)
-        return {"hbm_gbs": float(d["hbm_gbs"]), "source": "measured"}
-    return {"hbm_gbs": 6800.0, "source": "fallback"}
+        return {"hbm_gbs": float(d["hbm_gbs"]), "bf16_tflops": float(d["bf16_tflops"]),
+                "source": "measured"}
+    return {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "source": "fallback"}
 
 
 # --------------------------------------------------------------- distributed --
@@ -1262,9 +1263,7 @@ def run_vocab_only(args):
     _build.build()
     torch.cuda.set_device(0)
     stream = torch.cuda.current_stream()
-    pk = peaks()["hbm_gbs"]
-    with open(os.path.join(ROOT, "MEASURED_PEAKS.json")) as f:
-        bf16 = float(json.load(f)["bf16_tflops"])
+    pk = peaks()
     operators.own = True
     for case in operators.listed():
         if not case["op"].startswith(args.vocab_op):
@@ -1277,8 +1276,8 @@ def run_vocab_only(args):
         gbs, tf = work["bytes"] / t / 1e9, work["flops"] / t / 1e12
         print(json.dumps({"vocab": case["name"], "calls": calls, "us_per_call": round(t * 1e6, 2),
                           "gbs": round(gbs, 1), "tflops": round(tf, 1),
-                          "hbm_frac": round(gbs / pk, 3),
-                          "bf16_frac": round(tf / bf16, 3)}), flush=True)
+                          "hbm_frac": round(gbs / pk["hbm_gbs"], 3),
+                          "bf16_frac": round(tf / pk["bf16_tflops"], 3)}), flush=True)
         del states, fns
         torch.cuda.empty_cache()
     return 0
