@@ -23,7 +23,8 @@
  * Conventions for every entry point:
  *  - Return value: HG_OK (0) or one of the HG_ERR_* codes below.
  *  - "device pointer": memory of the device that was current at hg_create;
- *    the caller keeps that device current for every later call.
+ *    the caller keeps that device current for every later call. A gather or
+ *    hg_rearm with another one current answers HG_ERR_ARG.
  *  - Calls on one handle are not thread-safe; every gather of a handle runs on
  *    one stream, in call order (the class docstring's one-stream assumption).
  *  - A call that returns an error other than HG_ERR_TIMEOUT changed nothing:

@@ -397,6 +397,17 @@ int hg_destroy(hg_handle* h) {
 
 namespace {
 
+// The mailboxes and the caller's tensors are of one device: with another one current,
+// the kernel would start there, on pointers it cannot reach.
+int check_device(const hg_handle* h) {
+  int current = -1;
+  if (cudaGetDevice(&current) != cudaSuccess) {
+    cudaGetLastError();
+    return HG_ERR_CUDA;
+  }
+  return current == h->device ? HG_OK : HG_ERR_ARG;
+}
+
 // device_shards: the shards are device memory, whose first units the kernel
 // may prefetch into L2 before it waits on the previous kernel (not for
 // page-locked host memory, which the host may still be writing).
@@ -415,6 +426,7 @@ int gather_impl(hg_handle* h, const void* const* shard_ptrs, void* const* out_pt
     a.shard[r] = shard_ptrs[r];
     a.out[r] = out_ptrs[r];
   }
+  if (const int st = check_device(h); st != HG_OK) return st;
   if (!h->device_parity) {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) return HG_ERR_CUDA;
@@ -747,6 +759,7 @@ int hg_sync(hg_handle* h, hg_stream_t stream) {
 
 int hg_rearm(hg_handle* h, hg_stream_t stream) {
   if (!h) return HG_ERR_ARG;
+  if (const int st = check_device(h); st != HG_OK) return st;
   for (int d = 0; d < h->tp; ++d)
     if (hg::launch_fill_u32(static_cast<uint32_t*>(h->box[d]), h->box_bytes / 4, hg::kSentinel,
                             stream) != cudaSuccess)
@@ -825,6 +838,7 @@ int hg_gather_fused(hg_handle* h, const void* const* hidden_ptrs, const void* co
       return HG_ERR_ARG;
     if (logits_ptrs && logits_ptrs[r] && !aligned(logits_ptrs[r], 4)) return HG_ERR_ARG;
   }
+  if (const int st = check_device(h); st != HG_OK) return st;
   if (!h->device_parity) {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) return HG_ERR_CUDA;
