@@ -498,7 +498,9 @@ enum { HG_VOCAB_EMBED = 1, HG_VOCAB_EMBED_GRAD = 2, HG_VOCAB_LOSS = 4, HG_VOCAB_
  *   dtype        HG_BF16, HG_FP16, or HG_FP32 (embedding and its gradient only)
  *   ops          HG_VOCAB_* bits of the operators that will be called
  *   piece_bytes  HG_VOCAB_LOSS_GRAD: bound on the logits' gradient kept at a
- *                time (at least one piece of 256 columns per shard); 0: 512 MB
+ *                time (at least one piece of 256 columns per shard); 0: 512 MB.
+ *                The columns of a piece follow from it and max_rows, and are those
+ *                of every call: few rows on a handle made for many go piece by piece
  *   out          receives the handle
  *
  * Errors: HG_ERR_ARG (bad sizes or type, size overflow), HG_ERR_CUDA (no

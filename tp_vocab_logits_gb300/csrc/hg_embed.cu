@@ -9,16 +9,16 @@
 // Gradient: grad_table[v] (+)= scale * sum of grad[n] over tokens[n] = v. The
 // positions are sorted by token (stable, so that a token's rows come in the
 // order of their positions), and the sorted sequence is cut into chunks of
-// kRunRows rows whatever the tokens are: text repeats a few tokens thousands
-// of times, and a chunk is the same work for one token as for 32. A warp sums
-// one chunk over the columns of its lanes in fp32 registers. A run of equal
-// tokens that lies within a chunk is finished there; one that crosses a chunk's
-// end leaves its partial sums in `runs` (slot 0: the run a chunk continues, slot
-// 1: the run it starts and does not finish), and join_kernel adds those in chunk
-// order. No atomics, so the order of every sum is fixed. Memory bounds it once the
-// table is written whole (16384 rows of 7168 bf16, V=163840: 385 us, 6.7 TB/s); added
-// to a table, 8192 rows take 64 us, of which the sums are 42 (the rows come in
-// pieces of 512 bytes: 59 % of DRAM throughput) and the sort's latency 13.
+// 32 rows (8 or 16 where there are few: run_rows) whatever the tokens are: text
+// repeats a few tokens thousands of times, and a chunk is the same work for one
+// token as for 32. A warp sums one chunk over the columns of its lanes in fp32
+// registers. A run of equal tokens that lies within a chunk is finished there; one
+// that crosses a chunk's end leaves its partial sums in `runs` (slot 0: the run a
+// chunk continues, slot 1: the run it starts and does not finish), and join_kernel
+// adds those in chunk order. No atomics, so the order of every sum is fixed. Memory
+// bounds it once the table is written whole (16384 rows of 7168 bf16, V=163840: 385 us,
+// 6.7 TB/s); added to a table, 8192 rows take 64 us, of which the sums are 42 (the rows
+// come in pieces of 512 bytes: 59 % of DRAM throughput) and the sort's latency 13.
 
 #include <cooperative_groups.h>
 

@@ -19,18 +19,18 @@
 //
 // Everything in the exponent is kept in base 2: y = z * log2(e), ex2(y - lse2).
 //
-// What bounds them. For many rows the tensor cores: the pipe is busy 89-91 % of the
-// time (1536 rows, V=32768, K=2048), and over milliseconds the power limit
-// sets the clock: the loss of 8192 rows at V=163840, K=7168 takes 11.0-11.9 ms
-// (1620-1755 TFLOP/s; a library GEMM sustains 1714), the gradient of 4096 rows
-// 16.8-17.6 ms. Hence 256 x 256 tiles of a CTA pair, which read the fewest bytes
+// What bounds them. For many rows the tensor cores: the pipe is busy 89-92 % of the
+// time (1536 rows, V=32768, K=2048; gradient of 2048 rows, V=16384, K=4096), and over
+// milliseconds the power limit sets the clock: the loss of 8192 rows at V=163840, K=7168
+// takes 11.1-12.2 ms (1570-1740 TFLOP/s; a library GEMM sustains 1714), the gradient of
+// 4096 rows 16.3-17.6 ms. Hence 256 x 256 tiles of a CTA pair, which read the fewest bytes
 // from L2 per product, and two accumulators, so that a tile's epilogue runs beside
 // the next one's products. For few rows reading the weights: the loss of one row
-// 329-345 us for 2.35 GB (6.8-7.1 TB/s), the gradient of 16 rows 1105 us for the weights
-// twice and grad_weight once. Hence one CTA per tile, stages that hold only the rows there
-// are, and tile widths that leave every SM the same share of the weights. In between,
-// where K is short, the epilogues: 4096 rows at V=32768, K=1024 take 151 us
-// (1815 TFLOP/s); at K=80 the tensor pipe is busy an eighth of the time.
+// 325-345 us for 2.35 GB (6.8-7.2 TB/s), the gradient of 16 rows 1107-1125 us for the
+// weights twice and grad_weight once. Hence one CTA per tile, stages that hold only the
+// rows there are, and tile widths that leave every SM the same share of the weights. In
+// between, where K is short, the epilogues: 4096 rows at V=32768, K=1024 take 150-154 us
+// (1785-1830 TFLOP/s); at K=80 the tensor pipe is busy an eighth of the time.
 
 #include <cfloat>
 
@@ -80,7 +80,9 @@ constexpr int kSmallRows = 128;  // up to here a tile of one CTA holds all rows
 // kSplitRows below the first's in prob and packed: they fill rows of a tile that would
 // be empty. A row of grad_hidden or grad_weight is mostly one term of d then, and
 // over few rows the roundings of those few terms do not average out (16 rows:
-// 0.0028 off in bf16, against 0.0017 for the rounding of the result alone).
+// 0.0028 off in bf16, against 0.0017 for the rounding of the result alone). Above, a
+// second term would double the work of both products, for less and less: the
+// gradient of 600 rows in fp16 is 2.8e-4 off, where the rounding of the result is 2.1e-4.
 constexpr int kSplitRows = 64;
 constexpr int kOneTileRows = 256;  // and a pair's: packing leaves no tile out
 constexpr int kNarrowRounds = 8;  // rounds of tiles up to which narrower ones are tried
@@ -801,6 +803,8 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, int unit, int units
             *reinterpret_cast<uint4*>(dst + ((q ^ (lane & 7)) << 4)) =
                 make_uint4(w[0], w[1], w[2], w[3]);
           }
+          // Added to what is there by the copy engine, in the matrix's type: one
+          // rounding of the gradient and one of the sum, and nothing read back.
           store_end(&a.shard[t.r], t.n * kTileN + c, y, a.add != 0);
         };
         if constexpr (LONG) {
@@ -1045,7 +1049,7 @@ __device__ __forceinline__ void join_stats(float& top, float& sum, float t, floa
 }
 
 // Joins the tiles' statistics of a row: one CTA per row, so that a single row's
-// hundreds of tiles are read at once (about 3 us; a warp took 13 us for the 1520 of
+// hundreds of tiles are read at once (about 3 us; a warp took 13 us for the 1472 of
 // one row at V=163840).
 constexpr int kMergeThreads = 128;
 
@@ -1206,10 +1210,18 @@ cudaError_t launch_as(const GemmArgs& a, int sms, cudaStream_t stream) {
 }
 
 // Units (CTAs or pairs) for the hidden gradient when a piece's two gradients share
-// a launch, in proportion to their K blocks and tiles (a tile's ends cost about
-// as much as kTileEnds blocks); 0 where the piece is large enough for a launch each.
+// a launch, in proportion to their K blocks and tiles; 0 where the piece is large enough
+// for a launch each. A tile's ends count as kTileEnds blocks: with 0, 3 and 12 the
+// gradient of 300 rows at V=30000, K=512 took 73.2, 69.3 and 75.7 us, with 6 69.5
+// (K=128: 53.8, 53.8 and 60.1, with 6 53.8; 600 rows at V=4096, K=512: 32.8, 29.5, 29.5
+// and 29.5); single CTAs would rather have 0 (16 rows at V=32000, K=1024: 65.4 against
+// 72.4 us).
 constexpr int kTileEnds = 6;
-constexpr int kBothBlocks = 64;  // of a unit, up to which the launch is shared
+// Blocks of a unit up to which the launch is shared. Shared against apart: 28 rows at
+// V=3391, K=184 22.7 against 29.5 us, 300 rows at V=30000, K=512 69.5 against 75.6, 1000
+// rows at V=8192, K=512 43.7 against 49.0. Above 64 it still gains, but less of a longer
+// call (1000 rows at V=8192, K=1024: 56.8 against 62.7 us; 2000 rows: 92.3 against 99.0).
+constexpr int kBothBlocks = 64;
 
 int both_units(const hg_vocab& h, const GemmArgs& dx, const GemmArgs& dw, int N, int ctas) {
   const long long rows = div_up(N, kTileM * ctas), cols = div_up(h.K, kTileN);
@@ -1335,9 +1347,17 @@ int slab_rows(int N) {
 
 // Parts of the sum over the vocabulary in kDx. More of them fill the last round of
 // tiles better, but each is a slab of fp32 that is written and read again: take
-// the least of the two times together, at about 340 ns for a K block of a tile
-// and the copy rate for the slabs (2048 rows at V=16384, K=4096: 520 us with the
-// one part this chooses, 615 us with the four that fill the rounds best).
+// the least of the two times together, at kBlockNs for a K block of a tile
+// and the copy rate for the slabs.
+//
+// kBlockNs is a pair's time for 256 x 256 x 64 products at the tensor cores' pace. A CTA
+// of few rows takes half of that from L2 and twice from HBM, but their slabs are small:
+// with a quarter, a half, two and four times of it the hidden gradient of 16 rows
+// at V=163840, K=7168 (with its logits) took 706, 705, 726 and 726 us against 706, of 128
+// rows 715, 715, 738 and 737 against 715, of 2048 rows at V=16384, K=4096 338, 338, 359
+// and 359 against 338, of 2500 rows at V=32768, K=2048 453, 444, 451 and 466 against 443.
+constexpr double kBlockNs = 340;
+
 int dx_splits(const hg_vocab& h, int N) {
   const int ctas = row_shape(N, kTileN).ctas;
   const long long tiles = div_up(N > 0 ? N : 1, kTileM * ctas) * div_up(h.K, kTileN);
@@ -1348,7 +1368,7 @@ int dx_splits(const hg_vocab& h, int N) {
   int best = 1;
   double least = 0;
   for (int s = 1; s <= kMaxSplits && (s == 1 || s * kMinPartBlocks <= kb); ++s) {
-    const double ns = (double)div_up(tiles * s, units) / s * kb * 340 + s * slab_ns;
+    const double ns = (double)div_up(tiles * s, units) / s * kb * kBlockNs + s * slab_ns;
     if (s == 1 || ns < least) {
       least = ns;
       best = s;
