@@ -600,6 +600,202 @@ int hg_vocab_loss_grad(hg_vocab *h, const void *hidden, size_t ld_hidden,
                        void *grad_hidden, size_t ld_grad_hidden, void *const *grad_weight_ptrs,
                        int accumulate, hg_stream_t stream);
 
+/*
+ * Norm of token-side rows: what stands between a model's last layer and
+ * its [V, K] matrix (the hidden states of hg_gather_fused and hg_vocab_loss), and
+ * in front of each product before that. The pages start at the logits;
+ * this has no counterpart there.
+ *
+ *   hg_norm_rows       s[n] = x[n] + residual[n], in the handle's type
+ *                      rstd[n] = 1 / sqrt(mean_k s[n][k]^2 + eps)
+ *                      out[n][k] = s[n][k] * rstd[n] * gain[k]
+ *   hg_norm_rows_grad  d[n][k] = gain[k] * grad_out[n][k]
+ *                      grad_x[n][k] = rstd[n] * d[n][k] - s[n][k] * rstd[n]^3 *
+ *                          mean_j d[n][j] * s[n][j] + grad_sum[n][k]
+ *                      grad_gain[k] (+)= sum_n grad_out[n][k] * s[n][k] * rstd[n]
+ *
+ * grad_x is the gradient of x and of residual alike. All arithmetic is fp32; s is
+ * rounded once to the handle's type, and what follows is the norm of the rounded
+ * rows, those that the gradient is given. Squares and sums that pass the fp32
+ * range give rows of zeros or NaN.
+ *
+ * Conventions as for the vocabulary operators: asynchronous, no allocation, no wait for the
+ * device, capturable; the calls of one handle share its workspace (the gradient's
+ * only: calls of hg_norm_rows may overlap); the handle's device is current at every
+ * call and its the stream and pointers are; the same inputs give the same bits. Where
+ * all pointers and row distances are 16-byte (or 4-byte) aligned, rows move in
+ * such words.
+ */
+typedef struct hg_norm hg_norm;
+
+/* A further element type, for hg_norm_rows's out: 8 bits, 4 of exponent. */
+enum { HG_E4M3 = 3 };
+
+/*
+ * hg_norm_create - the norm of rows of one width
+ *
+ *   hidden    K, >= 1
+ *   max_rows  largest N of any later call, >= 1
+ *   dtype     HG_BF16, HG_FP16 or HG_FP32: x, residual, s, gain and the gradients
+ *
+ * Errors: HG_ERR_ARG, HG_ERR_CUDA. The handle belongs to the current device.
+ */
+int hg_norm_create(int hidden, int max_rows, int dtype, hg_norm **out);
+
+/* Free the handle; waits for its device first, whichever is current. NULL is a no-op. */
+int hg_norm_destroy(hg_norm *h);
+
+/* Bytes of device memory the handle holds (0 for NULL). */
+size_t hg_norm_workspace_bytes(const hg_norm *h);
+
+/*
+ * hg_norm_rows - sum with the residual, norm, and the output's rounding
+ *
+ *   x         [N, K], row distance ld_x
+ *   residual  NULL (s = x), or [N, K], row distance ld_residual
+ *   sum       NULL, or [N, K], row distance ld_sum: receives s. May be x or residual
+ *   gain      [K]
+ *   eps       >= 0
+ *   out       [N, K] of out_type, row distance ld_out; may be x or residual (not
+ *             both they and sum, and not in 8 bits), same row distance
+ *   out_type  the handle's type, or HG_E4M3
+ *   scales    HG_E4M3: [N, blocks] floats, rows contiguous; the values are out * scale
+ *   scale_block  HG_E4M3: 0: one scale per row; 128: one per 128 columns (blocks =
+ *             ceil(K / 128)). A scale is the largest magnitude of its values over
+ *             448, at least 2^-126, and 1 where they are all zero
+ *   rstd      NULL, or N floats
+ *
+ * Errors, before any device work: HG_ERR_ARG, HG_ERR_ROWS (N above max_rows),
+ * HG_ERR_CUDA.
+ */
+int hg_norm_rows(hg_norm *h, const void *x, size_t ld_x, const void *residual,
+                 size_t ld_residual, void *sum, size_t ld_sum, const void *gain, float eps, int N,
+                 void *out, size_t ld_out, int out_type, float *scales, int scale_block,
+                 float *rstd, hg_stream_t stream);
+
+/*
+ * hg_norm_rows_grad - gradient of hg_norm_rows (of its unquantised output)
+ *
+ *   s, rstd    as hg_norm_rows left them (s: its sum, or x where there was no residual)
+ *   grad_out   [N, K], row distance ld_grad_out
+ *   grad_sum   NULL, or [N, K], row distance ld_grad_sum: gradient that reaches s by
+ *              the residual stream
+ *   grad_x     NULL, or [N, K], row distance ld_grad_x; may be grad_out or grad_sum,
+ *              same row distance
+ *   grad_gain  NULL, or [K]
+ *   accumulate 0: grad_gain is overwritten; 1: the sum is added to what it holds
+ *              (rounded once)
+ *
+ * At least one of grad_x and grad_gain is wanted. The sum over rows is taken in
+ * an order that follows from N and K alone. N = 0 writes zeros to grad_gain unless it
+ * is added to. Errors as hg_norm_rows.
+ */
+int hg_norm_rows_grad(hg_norm *h, const void *s, size_t ld_s, const void *gain, const float *rstd,
+                      const void *grad_out, size_t ld_grad_out, const void *grad_sum,
+                      size_t ld_grad_sum, int N, void *grad_x, size_t ld_grad_x, void *grad_gain,
+                      int accumulate, hg_stream_t stream);
+
+/*
+ * Beam search: what follows the gather where several continuations of a sequence
+ * are kept. The pages leave the logits to the caller; this has no counterpart there.
+ *
+ *   hg_beam_select   total = score[beam] + logit - logsumexp of the beam's logits;
+ *                    the `picks` largest over the beams and vocabulary of an item
+ *   hg_beam_reorder  state row j of an item takes what row parents[j] holds
+ *
+ * An item is one sequence of `beams` beams; its rows of the logits, scores and states
+ * are neighbours (row = item * beams + beam).
+ *
+ * Totals are compared in 64 bits. Equal totals: the lower beam first; within a beam
+ * the larger logit, then the lower token. A total that is NaN, or rounds to -inf in
+ * fp32, is no candidate, so a score of -inf takes its beam out of the search (as all
+ * but one beam of an item at the first step, whose rows are the same).
+ *
+ * Conventions as for the vocabulary operators (asynchronous, no allocation, no
+ * wait, capturable, one device, same bits); calls of hg_beam_select of one handle share its workspace,
+ * hg_beam_reorder needs none.
+ */
+typedef struct hg_beam hg_beam;
+
+#define HG_MAX_BEAMS 64  /* beams of an item */
+#define HG_MAX_PICKS 128 /* picks of an item */
+
+/*
+ * hg_beam_create - the workspace of a beam search
+ *
+ *   max_items  largest number of items of any later call, >= 1
+ *   beams      1 to HG_MAX_BEAMS
+ *   vocab      V, >= 1
+ *   picks      1 to HG_MAX_PICKS, at most beams * vocab
+ *   dtype      HG_BF16, HG_FP16 or HG_FP32: the logits
+ *
+ * Errors: HG_ERR_ARG, HG_ERR_CUDA. The handle belongs to the current device.
+ */
+int hg_beam_create(int max_items, int beams, int vocab, int picks, int dtype, hg_beam **out);
+
+/* Free the handle; waits for its device first, whichever is current. NULL is a no-op. */
+int hg_beam_destroy(hg_beam *h);
+
+/* Bytes of device memory the handle holds (0 for NULL). */
+size_t hg_beam_workspace_bytes(const hg_beam *h);
+
+/*
+ * hg_beam_select - the best continuations of each item
+ *
+ *   logits    [items * beams, vocab], row distance ld_logits >= vocab (a rank's output
+ *             of hg_gather); -inf rules a token out
+ *   lse       NULL: computed here, of the logits that are not -inf (a row that holds
+ *             NaN or +inf then has no candidates); or one float per row, lse_stride
+ *             floats apart (logsumexp of hg_row_stats: &stats->logsumexp, 4)
+ *   scores    items * beams floats
+ *   finished  NULL, or items * beams bytes: a beam whose byte is not 0 has one
+ *             candidate, the token `end` with the beam's score as it is (its logits
+ *             are not read)
+ *   end       a token in [0, vocab), or -1 (none; finished is NULL then)
+ *   tokens, parents  [items, picks] signed integers of id_bytes (4 or 8) bytes, best first
+ *   picked    [items, picks] floats: the totals
+ *   picked_finished  NULL, or [items, picks] bytes: 1 where the token is `end` or the
+ *             parent was finished, else 0
+ *
+ * With picks = beams, picked, picked_finished and parents are the next step's
+ * scores, finished and reordering (tokens, hg_vocab_embed's input); with picks = 2 * beams
+ * there are beams of them that do not end. Where fewer candidates are left, the last
+ * picks have token and parent -1, total -inf and are not finished. No output may overlap an input.
+ *
+ * Errors, before any device work: HG_ERR_ARG, HG_ERR_ROWS (items above max_items),
+ * HG_ERR_CUDA.
+ */
+int hg_beam_select(hg_beam *h, const void *logits, size_t ld_logits, const float *lse,
+                   size_t lse_stride, const float *scores, const uint8_t *finished, int end,
+                   int items, void *tokens, void *parents, int id_bytes, float *picked,
+                   uint8_t *picked_finished, hg_stream_t stream);
+
+/* One state of the beams: for every row `outer` x `pieces` runs of piece_bytes bytes,
+ * run (o, p) of row r at data + o * outer_stride + r * row_stride + p * piece_stride
+ * (all in bytes). A cache [layers, rows, heads, length, width] of which t positions are
+ * filled: outer = layers, pieces = heads, piece_bytes = t * width * element. */
+typedef struct hg_beam_state {
+  void *data;
+  size_t outer, outer_stride, row_stride, pieces, piece_stride, piece_bytes;
+} hg_beam_state;
+
+#define HG_MAX_STATES 256 /* states of one call */
+
+/*
+ * hg_beam_reorder - states follow their beams, in place
+ *
+ *   parents   items * beams signed integers of id_bytes (4 or 8) bytes: parents[item *
+ *             beams + j] is a beam of the same item. One outside [0, beams)
+ *             leaves its row as it is
+ *   states    n_states records; the rows of a state and the states do not overlap
+ *
+ * All rows of an item take their parents' contents as they were before the call. Only
+ * rows that change are written. Errors, before any device work: HG_ERR_ARG (also:
+ * runs of one state that overlap by their strides), HG_ERR_ROWS, HG_ERR_CUDA.
+ */
+int hg_beam_reorder(hg_beam *h, const void *parents, int id_bytes, int items,
+                    const hg_beam_state *states, int n_states, hg_stream_t stream);
+
 /* Human-readable text of a status code; never NULL. No counterpart on the
  * pages (HeadGather reports failures as Python exceptions). */
 const char *hg_strerror(int status);

@@ -1,0 +1,53 @@
+// Internal declarations of the beam search's step: the handle, what a call works
+// on, and the launches.
+#pragma once
+
+#include "hg_vocab.cuh"
+
+struct hg_beam {
+  int device = -1;
+  int sms = 0;
+  int max_items = 0;
+  int beams = 0;
+  int vocab = 0;
+  int picks = 0;
+  int dtype = HG_BF16;
+  unsigned char* base = nullptr;
+  size_t bytes = 0;
+  // Parts of the workspace.
+  unsigned long long* list = nullptr;  // [list_slots][picks] best of each slice of a row
+  float2* stats = nullptr;             // [list_slots] maximum and sum of each slice
+};
+
+namespace hg {
+namespace beam {
+
+struct SelectCall {
+  int items = 0;
+  const void* logits = nullptr;
+  size_t ld = 0;
+  const float* lse = nullptr;
+  size_t lse_stride = 0;
+  const float* scores = nullptr;
+  const uint8_t* finished = nullptr;
+  int end = -1;
+  void *tokens = nullptr, *parents = nullptr;
+  int id_bytes = 8;
+  float* picked = nullptr;
+  uint8_t* picked_finished = nullptr;
+};
+
+cudaError_t select(const hg_beam& h, const SelectCall& c, cudaStream_t stream);
+cudaError_t reorder(const hg_beam& h, const void* parents, int id_bytes, int items,
+                    const hg_beam_state* states, int n_states, cudaStream_t stream);
+
+// Kernel attributes that the calls need on the current device, set when a handle is made.
+cudaError_t reorder_prepare();
+
+// Slices that the rows of a call are cut into, and the most that any call of the
+// handle has in all (workspace).
+int slices(const hg_beam& h, int items);
+long long list_slots(const hg_beam& h);
+
+}  // namespace beam
+}  // namespace hg

@@ -19,6 +19,9 @@
  * check failed (the binding then says which). In Python the checks and ctypes
  * cost an embedding call of eight shards 14 us on a Grace core, of which the
  * entry point, launch included, takes 3.
+ *
+ * norm_rows, norm_rows_grad, beam_select and beam_reorder do it for the norm and
+ * the beam search.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -45,7 +48,7 @@ typedef struct {
 static PyObject *g_ptr_name; /* interned "ptr" */
 /* The same for what is asked of a tensor. */
 static PyObject *g_is_cuda, *g_dtype, *g_shape, *g_stride, *g_is_contiguous, *g_data_ptr,
-    *g_get_device;
+    *g_get_device, *g_element_size;
 
 static int read_ptrs(PyObject *seq, void ***out, Py_ssize_t *n) {
   PyObject *fast = PySequence_Fast(seq, "pointer list must be a sequence of ints");
@@ -436,6 +439,333 @@ static PyObject *bind_vocab(PyObject *m, PyObject *args) {
   Py_RETURN_NONE;
 }
 
+/* ---- the norm and the beam search ------------------------------------------- */
+
+/* Their handles' `desc` has the same layout with other sizes in it: for the norm (handle,
+ * element type's code, 0, hidden, device), for the beam search (handle, beams, picks,
+ * vocab, device). */
+typedef int (*norm_rows_fn)(void *h, const void *x, size_t ld_x, const void *residual,
+                            size_t ld_residual, void *sum, size_t ld_sum, const void *gain,
+                            float eps, int N, void *out, size_t ld_out, int out_type,
+                            float *scales, int scale_block, float *rstd, void *stream);
+typedef int (*norm_rows_grad_fn)(void *h, const void *s, size_t ld_s, const void *gain,
+                                 const float *rstd, const void *grad_out, size_t ld_grad_out,
+                                 const void *grad_sum, size_t ld_grad_sum, int N, void *grad_x,
+                                 size_t ld_grad_x, void *grad_gain, int accumulate, void *stream);
+typedef int (*beam_select_fn)(void *h, const void *logits, size_t ld, const float *lse,
+                              size_t lse_stride, const float *scores, const void *finished,
+                              int end, int items, void *tokens, void *parents, int id_bytes,
+                              float *picked, void *picked_finished, void *stream);
+typedef struct { /* hg_beam_state */
+  void *data;
+  size_t outer, outer_stride, row_stride, pieces, piece_stride, piece_bytes;
+} BeamState;
+typedef int (*beam_reorder_fn)(void *h, const void *parents, int id_bytes, int items,
+                               const BeamState *states, int n_states, void *stream);
+
+static void *g_step_entry[4]; /* the four entry points, in the order above */
+static PyObject *g_e4m3, *g_bool, *g_uint8; /* torch's */
+
+#define E4M3_CODE 3     /* HG_E4M3 */
+#define MAX_STATES 256  /* HG_MAX_STATES */
+#define MAX_DIMS 16
+
+static int read_step_desc(PyObject *const *args, Py_ssize_t n, Py_ssize_t want, VocabDesc *d) {
+  if (n != want || !PyBytes_Check(args[0]) || PyBytes_GET_SIZE(args[0]) != sizeof *d) {
+    PyErr_SetString(PyExc_TypeError, "wrong arguments");
+    return -1;
+  }
+  if (!g_step_entry[0]) {
+    PyErr_SetString(PyExc_RuntimeError, "bind_steps has not been called");
+    return -1;
+  }
+  memcpy(d, PyBytes_AS_STRING(args[0]), sizeof *d);
+  return 1;
+}
+
+/* The length of a 2-D tensor. */
+static int row_count(PyObject *t, int *n) {
+  long long size[2];
+  int ok = read_sizes(PyObject_GetAttr(t, g_shape), size, 2);
+  if (ok == 1) ok = size[0] <= 0x7fffffffLL;
+  if (ok == 1) *n = (int)size[0];
+  return ok;
+}
+
+/* A contiguous [rows, cols] tensor of one of two types (b may be NULL). */
+static int table_tensor(PyObject *t, const VocabDesc *d, PyObject *a, PyObject *b, long long rows,
+                        long long cols, void **ptr, PyObject **dtype) {
+  PyObject *type = NULL;
+  long long size[2];
+  int ok = cuda_tensor(t, d, &type, ptr);
+  if (ok == 1) ok = type == a || (b && type == b);
+  if (ok == 1) ok = read_sizes(PyObject_GetAttr(t, g_shape), size, 2);
+  if (ok == 1) ok = size[0] == rows && size[1] == cols;
+  if (ok == 1) ok = is_true_call(t, g_is_contiguous);
+  if (ok == 1 && dtype) *dtype = type;
+  return ok;
+}
+
+/* A contiguous [n] tensor. */
+static int line_tensor(PyObject *t, const VocabDesc *d, PyObject *want, long long n, void **ptr) {
+  PyObject *dtype = NULL;
+  long long size[1];
+  int ok = cuda_tensor(t, d, &dtype, ptr);
+  if (ok == 1) ok = dtype == want;
+  if (ok == 1) ok = read_sizes(PyObject_GetAttr(t, g_shape), size, 1);
+  if (ok == 1) ok = size[0] == n;
+  if (ok == 1) ok = is_true_call(t, g_is_contiguous);
+  return ok;
+}
+
+/* norm_rows(desc, dtype, x, gain, out, residual or None, sum or None, rstd or None,
+ * scales or None, eps, stream) */
+static PyObject *norm_rows(PyObject *m, PyObject *const *a, Py_ssize_t n) {
+  (void)m;
+  VocabDesc d;
+  void *x, *gain, *out, *res = NULL, *sum = NULL, *rstd = NULL, *scales = NULL, *stream;
+  size_t ld_x = 0, ld_out = 0, ld_res = 0, ld_sum = 0;
+  int N = 0, st = 0, block = 0, type = 0;
+  int ok = read_step_desc(a, n, 11, &d);
+  if (ok == 1) ok = row_count(a[2], &N);
+  if (ok == 1) ok = row_tensor(a[2], &d, a[1], N, &x, &ld_x);
+  if (ok == 1) ok = line_tensor(a[3], &d, a[1], d.hidden, &gain);
+  if (ok == 1) {
+    type = a[8] == Py_None ? (int)d.tp : E4M3_CODE;
+    ok = row_tensor(a[4], &d, a[8] == Py_None ? a[1] : g_e4m3, N, &out, &ld_out);
+  }
+  if (ok == 1 && a[5] != Py_None) ok = row_tensor(a[5], &d, a[1], N, &res, &ld_res);
+  if (ok == 1 && a[6] != Py_None) ok = row_tensor(a[6], &d, a[1], N, &sum, &ld_sum);
+  if (ok == 1 && a[7] != Py_None) ok = line_tensor(a[7], &d, g_float32, N, &rstd);
+  if (ok == 1 && a[8] != Py_None) {
+    ok = table_tensor(a[8], &d, g_float32, NULL, N, 1, &scales, NULL);
+    if (ok == 0) {
+      block = 128;
+      ok = table_tensor(a[8], &d, g_float32, NULL, N, (d.hidden + 127) / 128, &scales, NULL);
+    }
+  }
+  if (ok == 1) ok = raw_stream(a[10], &d, &stream);
+  if (ok == 1) {
+    const double eps = PyFloat_AsDouble(a[9]);
+    if (PyErr_Occurred()) return NULL;
+    st = ((norm_rows_fn)g_step_entry[0])(d.h, x, ld_x, res, ld_res, sum, ld_sum, gain, (float)eps,
+                                         N, out, ld_out, type, scales, block, rstd, stream);
+  }
+  return answer(ok, st);
+}
+
+/* norm_rows_grad(desc, dtype, s, gain, rstd, grad_out, grad_x or None, grad_gain or
+ * None, grad_sum or None, accumulate, stream) */
+static PyObject *norm_rows_grad(PyObject *m, PyObject *const *a, Py_ssize_t n) {
+  (void)m;
+  VocabDesc d;
+  void *s, *gain, *rstd, *up, *grad_x = NULL, *grad_gain = NULL, *more = NULL, *stream;
+  size_t ld_s = 0, ld_up = 0, ld_x = 0, ld_more = 0;
+  int N = 0, st = 0;
+  int ok = read_step_desc(a, n, 11, &d);
+  if (ok == 1) ok = row_count(a[2], &N);
+  if (ok == 1) ok = row_tensor(a[2], &d, a[1], N, &s, &ld_s);
+  if (ok == 1) ok = line_tensor(a[3], &d, a[1], d.hidden, &gain);
+  if (ok == 1) ok = line_tensor(a[4], &d, g_float32, N, &rstd);
+  if (ok == 1) ok = row_tensor(a[5], &d, a[1], N, &up, &ld_up);
+  if (ok == 1 && a[6] != Py_None) ok = row_tensor(a[6], &d, a[1], N, &grad_x, &ld_x);
+  if (ok == 1 && a[7] != Py_None) ok = line_tensor(a[7], &d, a[1], d.hidden, &grad_gain);
+  if (ok == 1 && a[8] != Py_None) ok = row_tensor(a[8], &d, a[1], N, &more, &ld_more);
+  if (ok == 1) ok = raw_stream(a[10], &d, &stream);
+  if (ok == 1) {
+    const int add = PyObject_IsTrue(a[9]);
+    if (PyErr_Occurred()) return NULL;
+    st = ((norm_rows_grad_fn)g_step_entry[1])(d.h, s, ld_s, gain, rstd, up, ld_up, more, ld_more,
+                                              N, grad_x, ld_x, grad_gain, add, stream);
+  }
+  return answer(ok, st);
+}
+
+/* beam_select(desc, dtype, logits, scores, tokens, parents, picked, lse or None,
+ * finished or None, end, picked_finished or None, stream) */
+static PyObject *beam_select(PyObject *m, PyObject *const *a, Py_ssize_t n) {
+  (void)m;
+  VocabDesc d;
+  void *logits, *scores, *tokens, *parents, *picked, *lse = NULL, *fin = NULL, *fin_out = NULL;
+  void *stream;
+  size_t ld = 0;
+  long long lse_stride = 1;
+  PyObject *id_type = NULL;
+  int items = 0, st = 0;
+  int ok = read_step_desc(a, n, 12, &d);
+  if (ok == 1) ok = row_count(a[3], &items);
+  if (ok == 1) ok = items * d.tp <= 0x7fffffffLL;
+  if (ok == 1) ok = table_tensor(a[3], &d, g_float32, NULL, items, d.tp, &scores, NULL);
+  if (ok == 1) ok = row_tensor(a[2], &d, a[1], (int)(items * d.tp), &logits, &ld);
+  if (ok == 1) ok = table_tensor(a[4], &d, g_int64, g_int32, items, d.cols, &tokens, &id_type);
+  if (ok == 1) ok = table_tensor(a[5], &d, id_type, NULL, items, d.cols, &parents, NULL);
+  if (ok == 1) ok = table_tensor(a[6], &d, g_float32, NULL, items, d.cols, &picked, NULL);
+  if (ok == 1 && a[7] != Py_None) {
+    PyObject *dtype = NULL;
+    long long size[1];
+    ok = cuda_tensor(a[7], &d, &dtype, &lse);
+    if (ok == 1) ok = dtype == g_float32;
+    if (ok == 1) ok = read_sizes(PyObject_GetAttr(a[7], g_shape), size, 1);
+    if (ok == 1) ok = size[0] == items * d.tp;
+    if (ok == 1) ok = read_sizes(PyObject_CallMethodNoArgs(a[7], g_stride), &lse_stride, 1);
+    if (ok == 1 && size[0] <= 1) lse_stride = 1;
+    if (ok == 1) ok = lse_stride >= 1;
+  }
+  if (ok == 1 && a[8] != Py_None)
+    ok = table_tensor(a[8], &d, g_bool, g_uint8, items, d.tp, &fin, NULL);
+  if (ok == 1 && a[10] != Py_None)
+    ok = table_tensor(a[10], &d, g_bool, g_uint8, items, d.cols, &fin_out, NULL);
+  if (ok == 1) ok = raw_stream(a[11], &d, &stream);
+  if (ok == 1) {
+    int over = 0;
+    const long long end = PyLong_AsLongLongAndOverflow(a[9], &over);
+    if (PyErr_Occurred()) return NULL;
+    if (over || end < -1 || end >= d.hidden) return answer(0, 0);
+    st = ((beam_select_fn)g_step_entry[2])(d.h, logits, ld, lse, (size_t)lse_stride, scores, fin,
+                                           (int)end, items, tokens, parents,
+                                           id_type == g_int64 ? 8 : 4, picked, fin_out, stream);
+  }
+  return answer(ok, st);
+}
+
+/* A state tensor whose dimension `dim` has `rows` rows, as a record. Its other dimensions,
+ * from the longest stride to the shortest and with neighbours that continue one another
+ * taken as one, are at most an outer one, pieces and a contiguous run. */
+static int state_record(PyObject *t, PyObject *dim_obj, const VocabDesc *d, long long rows,
+                        BeamState *out) {
+  PyObject *dtype = NULL, *shape;
+  long long size[MAX_DIMS], stride[MAX_DIMS], count[MAX_DIMS], step[MAX_DIMS];
+  void *ptr;
+  int ok = cuda_tensor(t, d, &dtype, &ptr);
+  if (ok != 1) return ok;
+  shape = PyObject_GetAttr(t, g_shape);
+  if (!shape) return -1;
+  const Py_ssize_t nd = PyTuple_Check(shape) ? PyTuple_GET_SIZE(shape) : 0;
+  if (nd < 1 || nd > MAX_DIMS) {
+    Py_DECREF(shape);
+    return 0;
+  }
+  ok = read_sizes(shape, size, nd);
+  if (ok == 1) ok = read_sizes(PyObject_CallMethodNoArgs(t, g_stride), stride, nd);
+  if (ok != 1) return ok;
+  long long dim = 0;
+  if (dim_obj) {
+    int over = 0;
+    dim = PyLong_AsLongLongAndOverflow(dim_obj, &over);
+    if (PyErr_Occurred()) return -1;
+    if (over) return 0;
+  }
+  if (dim < 0) dim += nd;
+  if (dim < 0 || dim >= nd || size[dim] != rows) return 0;
+  PyObject *x = PyObject_CallMethodNoArgs(t, g_element_size);
+  if (!x) return -1;
+  const long long elem = PyLong_AsLongLong(x);
+  Py_DECREF(x);
+  if (PyErr_Occurred()) return -1;
+  int n = 0;
+  memset(out, 0, sizeof *out);
+  for (Py_ssize_t i = 0; i < nd; ++i) {
+    if (size[i] == 0) return 1; /* nothing in it */
+    if (stride[i] < 0) return 0;
+    if (i == dim || size[i] == 1) continue;
+    int at = n++;
+    for (; at > 0 && step[at - 1] < stride[i]; --at) {
+      step[at] = step[at - 1];
+      count[at] = count[at - 1];
+    }
+    step[at] = stride[i];
+    count[at] = size[i];
+  }
+  int kept = 0;
+  for (int i = 0; i < n; ++i) {
+    if (kept > 0 && step[kept - 1] == step[i] * count[i]) {
+      step[kept - 1] = step[i];
+      count[kept - 1] *= count[i];
+    } else {
+      step[kept] = step[i];
+      count[kept++] = count[i];
+    }
+  }
+  out->data = ptr;
+  out->row_stride = (size_t)(stride[dim] * elem);
+  out->outer = out->pieces = 1;
+  out->piece_bytes = (size_t)elem;
+  if (kept > 0 && step[kept - 1] == 1) out->piece_bytes = (size_t)(count[--kept] * elem);
+  if (kept > 2) return 0;
+  if (kept > 0) {
+    --kept;
+    out->pieces = (size_t)count[kept];
+    out->piece_stride = (size_t)(step[kept] * elem);
+  }
+  if (kept > 0) {
+    out->outer = (size_t)count[0];
+    out->outer_stride = (size_t)(step[0] * elem);
+  }
+  return 1;
+}
+
+/* beam_reorder(desc, parents, states, stream): each state a tensor (rows in dimension
+ * 0) or a pair of a tensor and the dimension of its rows */
+static PyObject *beam_reorder(PyObject *m, PyObject *const *a, Py_ssize_t n) {
+  (void)m;
+  VocabDesc d;
+  void *parents, *stream;
+  PyObject *id_type = NULL;
+  BeamState states[MAX_STATES];
+  int items = 0, st = 0;
+  Py_ssize_t count = 0;
+  int ok = read_step_desc(a, n, 4, &d);
+  if (ok == 1) ok = row_count(a[1], &items);
+  if (ok == 1) ok = table_tensor(a[1], &d, g_int64, g_int32, items, d.tp, &parents, &id_type);
+  if (ok == 1) ok = PyList_Check(a[2]) || PyTuple_Check(a[2]);
+  if (ok == 1) {
+    count = PySequence_Fast_GET_SIZE(a[2]);
+    ok = count <= MAX_STATES;
+  }
+  for (Py_ssize_t i = 0; ok == 1 && i < count; ++i) {
+    PyObject *t = PySequence_Fast_GET_ITEM(a[2], i), *dim = NULL;
+    if (PyTuple_Check(t)) {
+      if (PyTuple_GET_SIZE(t) != 2 || !PyLong_Check(PyTuple_GET_ITEM(t, 1))) return answer(0, 0);
+      dim = PyTuple_GET_ITEM(t, 1);
+      t = PyTuple_GET_ITEM(t, 0);
+    }
+    if (!PyObject_HasAttr(t, g_is_cuda)) return answer(0, 0);
+    ok = state_record(t, dim, &d, items * d.tp, &states[i]);
+  }
+  if (ok == 1) ok = raw_stream(a[3], &d, &stream);
+  if (ok == 1)
+    st = ((beam_reorder_fn)g_step_entry[3])(d.h, parents, id_type == g_int64 ? 8 : 4, items,
+                                            states, (int)count, stream);
+  return answer(ok, st);
+}
+
+/* bind_steps(norm_rows, norm_rows_grad, beam_select, beam_reorder addresses, int32, int64,
+ * float32, float8_e4m3fn, bool, uint8, raw stream getter) */
+static PyObject *bind_steps(PyObject *m, PyObject *args) {
+  PyObject *p[4], *type[6], *getter;
+  PyObject **const held[6] = {&g_int32, &g_int64, &g_float32, &g_e4m3, &g_bool, &g_uint8};
+  void *entry[4];
+  (void)m;
+  if (!PyArg_ParseTuple(args, "OOOOOOOOOOO", &p[0], &p[1], &p[2], &p[3], &type[0], &type[1],
+                        &type[2], &type[3], &type[4], &type[5], &getter))
+    return NULL;
+  for (int i = 0; i < 4; ++i) {
+    entry[i] = PyLong_AsVoidPtr(p[i]);
+    if (!entry[i]) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null function address");
+      return NULL;
+    }
+  }
+  memcpy(g_step_entry, entry, sizeof entry);
+  for (int i = 0; i < 6; ++i) {
+    Py_INCREF(type[i]);
+    Py_XSETREF(*held[i], type[i]);
+  }
+  Py_INCREF(getter);
+  Py_XSETREF(g_raw_stream, getter);
+  Py_RETURN_NONE;
+}
+
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef hgcall_methods[] = {
     {"bind_vocab", bind_vocab, METH_VARARGS, NULL},
@@ -443,6 +773,11 @@ static PyMethodDef hgcall_methods[] = {
     FAST(vocab_embed_grad),
     FAST(vocab_loss),
     FAST(vocab_loss_grad),
+    {"bind_steps", bind_steps, METH_VARARGS, NULL},
+    FAST(norm_rows),
+    FAST(norm_rows_grad),
+    FAST(beam_select),
+    FAST(beam_reorder),
     {NULL, NULL, 0, NULL},
 };
 
@@ -472,7 +807,8 @@ PyMODINIT_FUNC PyInit__hgcall(void) {
   g_data_ptr = PyUnicode_InternFromString("data_ptr");
   g_stride = PyUnicode_InternFromString("stride");
   g_get_device = PyUnicode_InternFromString("get_device");
-  if (!g_ptr_name || !g_is_cuda || !g_dtype || !g_shape || !g_stride || !g_is_contiguous ||
+  g_element_size = PyUnicode_InternFromString("element_size");
+  if (!g_element_size || !g_ptr_name || !g_is_cuda || !g_dtype || !g_shape || !g_stride || !g_is_contiguous ||
       !g_data_ptr || !g_get_device)
     return NULL;
   PyObject *m = PyModule_Create(&hgcall_module);

@@ -20,6 +20,7 @@ from . import _build
 
 HG_OK, HG_ERR_ARG, HG_ERR_ROWS, HG_ERR_CAPTURE, HG_ERR_CUDA, HG_ERR_TIMEOUT, HG_ERR_STATE = range(7)
 HG_MAX_TP = 32
+HG_MAX_BEAMS, HG_MAX_PICKS, HG_MAX_STATES = 64, 128, 256
 
 
 class HGError(RuntimeError):
@@ -82,6 +83,18 @@ def load() -> ctypes.CDLL:
     lib.hg_vocab_embed_grad.argtypes = [vp, vp, i, i, vp, sz, vp, f, i, st]
     lib.hg_vocab_loss.argtypes = [vp, vp, sz, vp, vp, i, i, f, vp, vp, st]
     lib.hg_vocab_loss_grad.argtypes = [vp, vp, sz, vp, vp, i, vp, vp, i, f, vp, sz, vp, i, st]
+    lib.hg_norm_create.argtypes = [i, i, i, vpp]
+    lib.hg_norm_destroy.argtypes = [vp]
+    lib.hg_norm_workspace_bytes.argtypes = [vp]
+    lib.hg_norm_workspace_bytes.restype = sz
+    lib.hg_norm_rows.argtypes = [vp, vp, sz, vp, sz, vp, sz, vp, f, i, vp, sz, i, vp, i, vp, st]
+    lib.hg_norm_rows_grad.argtypes = [vp, vp, sz, vp, vp, vp, sz, vp, sz, i, vp, sz, vp, i, st]
+    lib.hg_beam_create.argtypes = [i, i, i, i, i, vpp]
+    lib.hg_beam_destroy.argtypes = [vp]
+    lib.hg_beam_workspace_bytes.argtypes = [vp]
+    lib.hg_beam_workspace_bytes.restype = sz
+    lib.hg_beam_select.argtypes = [vp, vp, sz, vp, sz, vp, vp, i, i, vp, vp, i, vp, vp, st]
+    lib.hg_beam_reorder.argtypes = [vp, vp, i, i, vp, i, st]
     lib.hg_strerror.argtypes = [i]
     lib.hg_strerror.restype = ctypes.c_char_p
     for name in ("hg_create", "hg_create_ex", "hg_destroy", "hg_gather", "hg_gather_host",
@@ -89,7 +102,9 @@ def load() -> ctypes.CDLL:
                  "hg_parity", "hg_mailbox", "hg_launch_shape", "hg_debug_skip_push",
                  "hg_stock_gather", "hg_gather_fused", "hg_gather_stats", "hg_timeline",
                  "hg_probe", "hg_vocab_create", "hg_vocab_destroy", "hg_vocab_sync",
-                 "hg_vocab_embed", "hg_vocab_embed_grad", "hg_vocab_loss", "hg_vocab_loss_grad"):
+                 "hg_vocab_embed", "hg_vocab_embed_grad", "hg_vocab_loss", "hg_vocab_loss_grad",
+                 "hg_norm_create", "hg_norm_destroy", "hg_norm_rows", "hg_norm_rows_grad",
+                 "hg_beam_create", "hg_beam_destroy", "hg_beam_select", "hg_beam_reorder"):
         getattr(lib, name).restype = i
     _LIB = lib
     return lib
@@ -621,3 +636,286 @@ def hg_vocab_loss_grad(h: VocabHandle, hidden: torch.Tensor, weight: Sequence[to
                                                                  "grad_hidden"),
                       lambda: grad_weight is None or _vocab_shards(h, grad_weight, "grad_weight"))
     _check(st, "hg_vocab_loss_grad")
+
+
+class _StepHandle:
+    """What the handles of the norm and the beam search share: the pointer, the device, and
+    the record that _hgcall reads."""
+
+    _kind = ""
+
+    def __init__(self, ptr: int, dtype: torch.dtype, device: int):
+        self.ptr, self.dtype = ptr, dtype
+        self.device = torch.device("cuda", device)
+        self._describe()
+
+    def _sizes(self) -> tuple:
+        raise NotImplementedError
+
+    def _describe(self) -> None:
+        self.desc = struct.pack("Pqqqq", self.ptr, *self._sizes(), self.device.index)
+
+    @property
+    def workspace_bytes(self) -> int:
+        return int(getattr(load(), f"{self._kind}_workspace_bytes")(self.ptr))
+
+    def close(self) -> None:
+        if self.ptr:
+            ptr, self.ptr = self.ptr, 0
+            self._describe()
+            _check(getattr(load(), f"{self._kind}_destroy")(ptr), f"{self._kind}_destroy")
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class NormHandle(_StepHandle):
+    """Owner of one hg_norm; freed by hg_norm_destroy on close() or collection."""
+
+    _kind = "hg_norm"
+
+    def __init__(self, ptr: int, hidden: int, max_rows: int, dtype: torch.dtype, device: int = 0):
+        self.hidden, self.max_rows = hidden, max_rows
+        super().__init__(ptr, dtype, device)
+
+    def _sizes(self) -> tuple:
+        return _VOCAB_TYPES[self.dtype], 0, self.hidden
+
+
+class BeamHandle(_StepHandle):
+    """Owner of one hg_beam; freed by hg_beam_destroy on close() or collection."""
+
+    _kind = "hg_beam"
+
+    def __init__(self, ptr: int, max_items: int, beams: int, vocab: int, picks: int,
+                 dtype: torch.dtype, device: int = 0):
+        self.max_items, self.beams, self.vocab, self.picks = max_items, beams, vocab, picks
+        super().__init__(ptr, dtype, device)
+
+    def _sizes(self) -> tuple:
+        return self.beams, self.picks, self.vocab
+
+
+_STEP_CALL = None
+
+
+def _step_call():
+    global _STEP_CALL
+    if _STEP_CALL is None:
+        lib, mod = load(), _pycall()
+        mod.bind_steps(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.hg_norm_rows, lib.hg_norm_rows_grad, lib.hg_beam_select, lib.hg_beam_reorder)],
+            torch.int32, torch.int64, torch.float32, torch.float8_e4m3fn, torch.bool, torch.uint8,
+            getattr(torch._C, "_cuda_getCurrentRawStream", _current_raw_stream))
+        _STEP_CALL = mod
+    return _STEP_CALL
+
+
+def _step_dtype(dtype: torch.dtype, where: str) -> int:
+    if dtype not in _VOCAB_TYPES:
+        raise ValueError(f"{where}: dtype must be bfloat16, float16 or float32, got {dtype}")
+    return _VOCAB_TYPES[dtype]
+
+
+def _step_tensor(h: _StepHandle, t: torch.Tensor, types: Sequence[torch.dtype], what: str) -> None:
+    _vocab_device(h, t, what)
+    if not t.is_cuda or t.dtype not in types:
+        raise ValueError(f"{what}: need a CUDA tensor of {' or '.join(map(str, types))}, got "
+                         f"{t.dtype} on {t.device}")
+
+
+def _step_table(h: _StepHandle, t: torch.Tensor, types: Sequence[torch.dtype], shape: tuple,
+                what: str) -> None:
+    _step_tensor(h, t, types, what)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what}: need a contiguous {list(shape)}, got {tuple(t.shape)} with "
+                         f"strides {t.stride()}")
+
+
+def _step_rows(h: _StepHandle, t: torch.Tensor, dtype: torch.dtype, n: int, width: int,
+               what: str) -> None:
+    """An [n, width] matrix, rows contiguous."""
+    _step_tensor(h, t, (dtype,), what)
+    if tuple(t.shape) != (n, width) or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: need [{n}, {width}] with contiguous rows, got "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    if n > 1 and t.stride(0) < width:
+        raise ValueError(f"{what}: rows overlap (row stride {t.stride(0)})")
+
+
+def _step_count(t: torch.Tensor, what: str) -> int:
+    if t.dim() != 2:
+        raise ValueError(f"{what}: need a matrix, got {tuple(t.shape)}")
+    return t.shape[0]
+
+
+def hg_norm_create(hidden: int, max_rows: int, *, dtype: torch.dtype = torch.bfloat16) -> NormHandle:
+    """The norm of rows of `hidden` elements of dtype, for calls of up to max_rows
+    rows. The handle is of the current device; calls take that device's tensors, and
+    want it current."""
+    code = _step_dtype(dtype, "hg_norm_create")
+    out = ctypes.c_void_p()
+    _check(load().hg_norm_create(hidden, max_rows, code, ctypes.byref(out)), "hg_norm_create")
+    return NormHandle(out.value, hidden, max_rows, dtype, torch.cuda.current_device())
+
+
+def hg_norm_destroy(h: NormHandle) -> None:
+    h.close()
+
+
+def _norm_scales(h: NormHandle, t: torch.Tensor, n: int) -> None:
+    blocks = -(-h.hidden // 128)
+    if t.dim() == 2 and t.shape[1] == 1:
+        blocks = 1
+    _step_table(h, t, (torch.float32,), (n, blocks), "scales")
+
+
+def hg_norm_rows(h: NormHandle, x: torch.Tensor, gain: torch.Tensor, out: torch.Tensor,
+                 residual: torch.Tensor | None = None, sum_out: torch.Tensor | None = None,
+                 rstd: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                 eps: float = 1e-6, stream=None) -> None:
+    """s = x + residual (written to sum_out), out = s * rstd * gain with rstd = 1 /
+    sqrt(mean of s^2 + eps) per row. With scales, float32 [N, 1] (one per row) or
+    [N, ceil(hidden / 128)] (one per 128 columns), out is float8_e4m3fn and its values
+    are out * scales."""
+    st = _step_call().norm_rows(h.desc, h.dtype, x, gain, out, residual, sum_out, rstd, scales, eps,
+                                None if stream is None else _stream_ptr(stream))
+    if st is None:
+        n = _step_count(x, "x")
+        out_type = h.dtype if scales is None else torch.float8_e4m3fn
+        _vocab_refuse(
+            "hg_norm_rows", lambda: _step_rows(h, x, h.dtype, n, h.hidden, "x"),
+            lambda: _step_table(h, gain, (h.dtype,), (h.hidden,), "gain"),
+            lambda: _step_rows(h, out, out_type, n, h.hidden, "out"),
+            lambda: residual is None or _step_rows(h, residual, h.dtype, n, h.hidden, "residual"),
+            lambda: sum_out is None or _step_rows(h, sum_out, h.dtype, n, h.hidden, "sum_out"),
+            lambda: rstd is None or _step_table(h, rstd, (torch.float32,), (n,), "rstd"),
+            lambda: scales is None or _norm_scales(h, scales, n))
+    _check(st, "hg_norm_rows")
+
+
+def hg_norm_rows_grad(h: NormHandle, s: torch.Tensor, gain: torch.Tensor, rstd: torch.Tensor,
+                      grad_out: torch.Tensor, grad_x: torch.Tensor | None,
+                      grad_gain: torch.Tensor | None, grad_sum: torch.Tensor | None = None,
+                      accumulate: bool = False, stream=None) -> None:
+    """Gradient of hg_norm_rows from its s and rstd, to grad_x (of x and residual
+    alike) and grad_gain (either may be None); grad_sum is what reaches s by the
+    residual stream, accumulate adds to what grad_gain holds."""
+    st = _step_call().norm_rows_grad(h.desc, h.dtype, s, gain, rstd, grad_out, grad_x, grad_gain,
+                                     grad_sum, accumulate,
+                                     None if stream is None else _stream_ptr(stream))
+    if st is None:
+        n = _step_count(s, "s")
+        _vocab_refuse(
+            "hg_norm_rows_grad", lambda: _step_rows(h, s, h.dtype, n, h.hidden, "s"),
+            lambda: _step_table(h, gain, (h.dtype,), (h.hidden,), "gain"),
+            lambda: _step_table(h, rstd, (torch.float32,), (n,), "rstd"),
+            lambda: _step_rows(h, grad_out, h.dtype, n, h.hidden, "grad_out"),
+            lambda: grad_x is None or _step_rows(h, grad_x, h.dtype, n, h.hidden, "grad_x"),
+            lambda: grad_gain is None or _step_table(h, grad_gain, (h.dtype,), (h.hidden,),
+                                                     "grad_gain"),
+            lambda: grad_sum is None or _step_rows(h, grad_sum, h.dtype, n, h.hidden, "grad_sum"))
+    _check(st, "hg_norm_rows_grad")
+
+
+def hg_beam_create(max_items: int, beams: int, vocab: int, picks: int, *,
+                   dtype: torch.dtype = torch.bfloat16) -> BeamHandle:
+    """The workspace of a beam search of up to max_items items of `beams` beams, with
+    `picks` continuations chosen per item, on logits of dtype. The handle is of the
+    current device; calls take that device's tensors, and want it current."""
+    code = _step_dtype(dtype, "hg_beam_create")
+    out = ctypes.c_void_p()
+    _check(load().hg_beam_create(max_items, beams, vocab, picks, code, ctypes.byref(out)),
+           "hg_beam_create")
+    return BeamHandle(out.value, max_items, beams, vocab, picks, dtype, torch.cuda.current_device())
+
+
+def hg_beam_destroy(h: BeamHandle) -> None:
+    h.close()
+
+
+def _beam_lse(h: BeamHandle, t: torch.Tensor, rows: int) -> None:
+    _step_tensor(h, t, (torch.float32,), "lse")
+    if tuple(t.shape) != (rows,) or (rows > 1 and t.stride(0) < 1):
+        raise ValueError(f"lse: need [{rows}], got {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _beam_end(h: BeamHandle, end: int) -> None:
+    if not -1 <= end < h.vocab:
+        raise ValueError(f"end: need a token in [0, {h.vocab}) or -1, got {end}")
+
+
+def hg_beam_select(h: BeamHandle, logits: torch.Tensor, scores: torch.Tensor, tokens: torch.Tensor,
+                   parents: torch.Tensor, picked: torch.Tensor, lse: torch.Tensor | None = None,
+                   finished: torch.Tensor | None = None, end: int = -1,
+                   picked_finished: torch.Tensor | None = None, stream=None) -> None:
+    """The best continuations of each item, by scores [items, beams] + logits - lse:
+    tokens, parents (int32 or int64), picked (their totals) and picked_finished (bool or
+    uint8), all [items, picks]. logits: [items * beams, vocab]. lse: the logits'
+    logsumexp (the column of unpack_row_stats, say), computed here where it is None.
+    finished [items, beams] (bool or uint8): beams that go on with the token `end` alone."""
+    st = _step_call().beam_select(h.desc, h.dtype, logits, scores, tokens, parents, picked, lse,
+                                  finished, end, picked_finished,
+                                  None if stream is None else _stream_ptr(stream))
+    if st is None:
+        n = _step_count(scores, "scores")
+        ids, flags = (torch.int64, torch.int32), (torch.bool, torch.uint8)
+        _vocab_refuse(
+            "hg_beam_select",
+            lambda: _step_table(h, scores, (torch.float32,), (n, h.beams), "scores"),
+            lambda: _step_rows(h, logits, h.dtype, n * h.beams, h.vocab, "logits"),
+            lambda: _step_table(h, tokens, ids, (n, h.picks), "tokens"),
+            lambda: _step_table(h, parents, (tokens.dtype,), (n, h.picks), "parents"),
+            lambda: _step_table(h, picked, (torch.float32,), (n, h.picks), "picked"),
+            lambda: lse is None or _beam_lse(h, lse, n * h.beams),
+            lambda: finished is None or _step_table(h, finished, flags, (n, h.beams), "finished"),
+            lambda: picked_finished is None or _step_table(h, picked_finished, flags, (n, h.picks),
+                                                           "picked_finished"),
+            lambda: _beam_end(h, end))
+    _check(st, "hg_beam_select")
+
+
+def _beam_steps(t: torch.Tensor, dim: int) -> int:
+    """Strides that step between the contiguous runs of a row."""
+    steps = []
+    others = [(t.stride(i), t.shape[i]) for i in range(t.dim()) if i != dim and t.shape[i] != 1]
+    for stride, size in sorted(others, key=lambda d: -d[0]):
+        if steps and steps[-1][0] == stride * size:
+            steps[-1] = (stride, steps[-1][1] * size)
+        else:
+            steps.append((stride, size))
+    return len(steps) - bool(steps and steps[-1][0] == 1)
+
+
+def _beam_state(h: BeamHandle, state, rows: int) -> None:
+    t, dim = state if isinstance(state, tuple) and len(state) == 2 else (state, 0)
+    if not hasattr(t, "is_cuda") or not isinstance(dim, int):
+        raise ValueError("states: need tensors, or pairs of a tensor and a dimension")
+    _vocab_device(h, t, "states")
+    if not t.is_cuda:
+        raise ValueError(f"states: need CUDA tensors, got one on {t.device}")
+    if not -t.dim() <= dim < t.dim() or t.shape[dim] != rows:
+        raise ValueError(f"states: need {rows} rows in dimension {dim} of {tuple(t.shape)}")
+    if t.numel() and _beam_steps(t, dim % t.dim()) > 2:
+        raise ValueError(f"states: {tuple(t.shape)} with strides {t.stride()} has more than two "
+                         "steps between its contiguous runs")
+
+
+def hg_beam_reorder(h: BeamHandle, parents: torch.Tensor, states: Sequence, stream=None) -> None:
+    """In place, row item * beams + j of every state takes what row item * beams +
+    parents[item, j] held; a parent outside [0, beams) leaves its row. parents: int32 or
+    int64 [items, beams]. states: tensors with their rows in dimension 0, or pairs of a
+    tensor and the dimension of its rows; views of a larger cache are fine."""
+    st = _step_call().beam_reorder(h.desc, parents, states,
+                                   None if stream is None else _stream_ptr(stream))
+    if st is None:
+        n = _step_count(parents, "parents")
+        _step_table(h, parents, (torch.int64, torch.int32), (n, h.beams), "parents")
+        if not isinstance(states, (list, tuple)) or len(states) > HG_MAX_STATES:
+            raise ValueError(f"states: need a list of at most {HG_MAX_STATES}")
+        _vocab_refuse("hg_beam_reorder", *[lambda s=s: _beam_state(h, s, n * h.beams)
+                                           for s in states])
+    _check(st, "hg_beam_reorder")
