@@ -686,8 +686,8 @@ int hg_norm_rows(hg_norm *h, const void *x, size_t ld_x, const void *residual,
  *   accumulate 0: grad_gain is overwritten; 1: the sum is added to what it holds
  *              (rounded once)
  *
- * At least one of grad_x and grad_gain is wanted. The sum over rows is taken in
- * an order that follows from N and K alone. N = 0 writes zeros to grad_gain unless it
+ * At least one of grad_x and grad_gain is wanted. The order of the sum over rows
+ * follows from the sizes and alignments alone. N = 0 writes zeros to grad_gain unless it
  * is added to. Errors as hg_norm_rows.
  */
 int hg_norm_rows_grad(hg_norm *h, const void *s, size_t ld_s, const void *gain, const float *rstd,

@@ -12,7 +12,7 @@ struct hg_norm {
   int dtype = HG_BF16;
   unsigned char* base = nullptr;
   size_t bytes = 0;
-  float* partial = nullptr;  // [grad_parts(max_rows)][K] sums of grad_gain over some rows
+  float* partial = nullptr;  // [grad_parts][K] sums of grad_gain over some rows
 };
 
 namespace hg {
@@ -53,8 +53,8 @@ struct GradCall {
 cudaError_t rows(const hg_norm& h, const NormCall& c, cudaStream_t stream);
 cudaError_t rows_grad(const hg_norm& h, const GradCall& c, cudaStream_t stream);
 
-// Partial sums of grad_gain that a call of N rows writes.
-int grad_parts(const hg_norm& h, int N);
+// The most partial sums of grad_gain that a call writes.
+int grad_parts(const hg_norm& h);
 
 // Widest access that all of these allow: 16 bytes, 4, or an element.
 struct Access {

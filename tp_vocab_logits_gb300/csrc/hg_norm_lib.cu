@@ -58,7 +58,7 @@ int hg_norm_create(int hidden, int max_rows, int dtype, hg_norm** out) {
     delete h;
     return HG_ERR_CUDA;
   }
-  h->bytes = (size_t)hg::norm::grad_parts(*h, max_rows) * hidden * sizeof(float);
+  h->bytes = (size_t)hg::norm::grad_parts(*h) * hidden * sizeof(float);
   void* p = nullptr;
   if (cudaMalloc(&p, h->bytes) != cudaSuccess) {
     cudaGetLastError();  // leave no sticky allocation error behind
