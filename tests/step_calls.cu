@@ -134,7 +134,7 @@ namespace hg {
 namespace norm {
 cudaError_t rows(const hg_norm&, const NormCall&, cudaStream_t) { return launched("rows"); }
 cudaError_t rows_grad(const hg_norm&, const GradCall&, cudaStream_t) { return launched("grad"); }
-cudaError_t prepare() { return cudaSuccess; }
+cudaError_t prepare(const hg_norm&) { return cudaSuccess; }
 int grad_parts(const hg_norm&) { return 1; }
 }  // namespace norm
 }  // namespace hg

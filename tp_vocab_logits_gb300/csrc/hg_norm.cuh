@@ -53,6 +53,9 @@ struct GradCall {
 cudaError_t rows(const hg_norm& h, const NormCall& c, cudaStream_t stream);
 cudaError_t rows_grad(const hg_norm& h, const GradCall& c, cudaStream_t stream);
 
+// Kernel attributes that the calls need on the current device, set when a handle is made.
+cudaError_t prepare(const hg_norm& h);
+
 // The most partial sums of grad_gain that a call writes.
 int grad_parts(const hg_norm& h);
 

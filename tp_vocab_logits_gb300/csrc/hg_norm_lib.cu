@@ -53,7 +53,8 @@ int hg_norm_create(int hidden, int max_rows, int dtype, hg_norm** out) {
   h->max_rows = max_rows;
   h->dtype = dtype;
   if (cudaGetDevice(&h->device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) {
+      cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
+      hg::norm::prepare(*h) != cudaSuccess) {
     cudaGetLastError();
     delete h;
     return HG_ERR_CUDA;
