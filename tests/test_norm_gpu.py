@@ -103,6 +103,10 @@ SHAPES = [
     (1, 7168, bf16, 0, 0), (200, 7168, bf16, 0, 0), (3, 7168, fp16, 2, 0), (3, 7167, bf16, 0, 0),
     (1, 7168, fp32, 0, 0), (2, 9001, bf16, 0, 0), (3, 16384, fp16, 0, 0), (2, 20000, bf16, 2, 1),
     (1, 40000, fp32, 0, 0), (2, 70001, bf16, 0, 0), (1, 140000, bf16, 0, 0),
+    # more rows than SMs, where they are streamed or share a CTA
+    (400, 64, bf16, 0, 0), (1000, 256, fp16, 8, 0), (600, 512, fp32, 0, 0), (330, 4096, bf16, 0, 0),
+    (700, 3000, fp16, 0, 0), (160, 16384, bf16, 0, 0), (200, 2050, bf16, 0, 0),
+    (500, 101, bf16, 0, 0), (3000, 40, bf16, 0, 0), (170, 8192, fp32, 0, 0),
 ]
 
 
@@ -270,7 +274,10 @@ def grad_inputs(g, N, K, dtype, pad=0, off=0):
 
 @pytest.mark.parametrize("N,K,dtype,pad,off", SHAPES + [
     (4000, 64, bf16, 0, 0), (5000, 33, fp32, 0, 0), (1500, 1000, fp16, 0, 0),
-    (700, 7168, bf16, 0, 0), (2000, 513, bf16, 1, 0)])
+    (700, 7168, bf16, 0, 0), (2000, 513, bf16, 1, 0), (64, 7168, bf16, 0, 0),
+    (65, 1000, bf16, 0, 0), (152, 96, fp32, 0, 0), (153, 96, fp32, 0, 0), (64, 333, fp16, 0, 0),
+    (320, 512, bf16, 0, 0), (2500, 1024, fp16, 0, 0), (900, 14336, bf16, 0, 0),
+    (400, 5002, bf16, 0, 0), (400, 12000, fp16, 2, 0), (1000, 2048, fp32, 0, 0)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_gradient(N, K, dtype, pad, off, residual):
     g = gen_of(N * 3 + K)
@@ -306,10 +313,11 @@ def test_gradient_in_place(K):
     h.close()
 
 
-def test_gradient_of_no_rows():
-    h = hg.hg_norm_create(40, 4)
-    none = torch.empty((0, 40), device="cuda", dtype=bf16)
-    gain, gg = (torch.ones(40, device="cuda", dtype=bf16) for _ in range(2))
+@pytest.mark.parametrize("K", [40, 41, 7168, 16384, 50000])
+def test_gradient_of_no_rows(K):
+    h = hg.hg_norm_create(K, 4)
+    none = torch.empty((0, K), device="cuda", dtype=bf16)
+    gain, gg = (torch.ones(K, device="cuda", dtype=bf16) for _ in range(2))
     rstd = torch.empty(0, device="cuda")
     hg.hg_norm_rows(h, none, gain, none.clone())
     hg.hg_norm_rows_grad(h, none, gain, rstd, none, none.clone(), gg, accumulate=True)
