@@ -63,7 +63,8 @@ cudaError_t reorder(const hg_beam&, const void*, int, int, const hg_beam_state*,
                     cudaStream_t) {
   return launched("reorder");
 }
-cudaError_t select_prepare() { return cudaSuccess; }
+
+cudaError_t select_prepare(const hg_beam&) { return cudaSuccess; }
 cudaError_t reorder_prepare() { return cudaSuccess; }
 long long list_slots(const hg_beam&) { return 1; }
 }  // namespace beam

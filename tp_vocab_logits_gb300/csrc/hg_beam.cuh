@@ -15,8 +15,10 @@ struct hg_beam {
   unsigned char* base = nullptr;
   size_t bytes = 0;
   // Parts of the workspace.
-  unsigned long long* list = nullptr;  // [list_slots][picks] best of each slice of a row
-  float2* stats = nullptr;             // [list_slots] maximum and sum of each slice
+  unsigned long long* list = nullptr;  // [list_slots][picks] best of each part of a row
+  float2* stats = nullptr;             // [list_slots] maximum and sum of each part
+  int* beam_of = nullptr;              // [list_slots] whose part it is
+  unsigned* arrived = nullptr;         // [max_items] CTAs that are done with an item, 0 between calls
 };
 
 namespace hg {
@@ -42,11 +44,10 @@ cudaError_t reorder(const hg_beam& h, const void* parents, int id_bytes, int ite
                     const hg_beam_state* states, int n_states, cudaStream_t stream);
 
 // Kernel attributes that the calls need on the current device, set when a handle is made.
+cudaError_t select_prepare(const hg_beam& h);
 cudaError_t reorder_prepare();
 
-// Slices that the rows of a call are cut into, and the most that any call of the
-// handle has in all (workspace).
-int slices(const hg_beam& h, int items);
+// Parts of rows that any call of the handle has at most (workspace).
 long long list_slots(const hg_beam& h);
 
 }  // namespace beam

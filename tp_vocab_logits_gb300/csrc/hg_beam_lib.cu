@@ -72,13 +72,14 @@ int hg_beam_create(int max_items, int beams, int vocab, int picks, int dtype, hg
   h->dtype = dtype;
   if (cudaGetDevice(&h->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
-      hg::beam::reorder_prepare() != cudaSuccess) {
+      hg::beam::select_prepare(*h) != cudaSuccess || hg::beam::reorder_prepare() != cudaSuccess) {
     cudaGetLastError();
     delete h;
     return HG_ERR_CUDA;
   }
   const size_t slots = (size_t)hg::beam::list_slots(*h);
-  h->bytes = slots * picks * sizeof(*h->list) + slots * sizeof(*h->stats);
+  h->bytes = slots * picks * sizeof(*h->list) + slots * sizeof(*h->stats) +
+             slots * sizeof(*h->beam_of) + (size_t)max_items * sizeof(*h->arrived);
   void* p = nullptr;
   if (cudaMalloc(&p, h->bytes) != cudaSuccess) {
     cudaGetLastError();  // leave no sticky allocation error behind
@@ -88,6 +89,14 @@ int hg_beam_create(int max_items, int beams, int vocab, int picks, int dtype, hg
   h->base = static_cast<unsigned char*>(p);
   h->list = static_cast<unsigned long long*>(p);
   h->stats = reinterpret_cast<float2*>(h->list + slots * picks);
+  h->beam_of = reinterpret_cast<int*>(h->stats + slots);
+  h->arrived = reinterpret_cast<unsigned*>(h->beam_of + slots);
+  if (cudaMemset(h->arrived, 0, (size_t)max_items * sizeof(*h->arrived)) != cudaSuccess ||
+      cudaDeviceSynchronize() != cudaSuccess) {
+    cudaFree(p);
+    delete h;
+    return HG_ERR_CUDA;
+  }
   *out = h;
   return HG_OK;
 }
