@@ -66,7 +66,7 @@ cudaError_t reorder(const hg_beam&, const void*, int, int, const hg_beam_state*,
 
 cudaError_t select_prepare(const hg_beam&) { return cudaSuccess; }
 cudaError_t reorder_prepare() { return cudaSuccess; }
-long long list_slots(const hg_beam&) { return 1; }
+long long part_slots(const hg_beam&) { return 1; }
 }  // namespace beam
 }  // namespace hg
 
@@ -122,6 +122,20 @@ int main() {
   reorder("rows outside the layers", {a, 2, 8, 16, 1, 0, 8});
   reorder("nothing in it", {nullptr, 1, 0, 0, 0, 0, 8});
   show("no states", hg_beam_reorder(h, d, 8, 2, nullptr, 0, nullptr));
+  // The workspace's arrays, where odd counts come before them.
+  std::printf("workspaces\n");
+  for (int items = 1; items < 4; ++items)
+    for (int picks = 1; picks < 4; ++picks) {
+      hg_beam* w = nullptr;
+      hg_beam_create(items, 3, 50, picks, HG_BF16, &w);
+      auto off = [&](const void* p) { return (uintptr_t)p - (uintptr_t)w->base; };
+      const bool ok = off(w->maxima) % 16 == 0 && off(w->stats) % 8 == 0 && off(w->list) % 8 == 0 &&
+                      off(w->beam_of) % 4 == 0 &&
+                      off(w->beam_of + hg::beam::part_slots(*w)) == w->bytes;
+      show("aligned", ok);
+      w->base = nullptr;  // not freed: the lines below are compared
+      delete w;
+    }
   std::printf("end\n");
   fakeSetDevice(0);
   show("destroy", hg_beam_destroy(h));

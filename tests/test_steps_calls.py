@@ -50,7 +50,7 @@ def test_refusals(events):
 def test_what_is_served(events):
     """Calls with nothing in them launch nothing, unless a gradient is to be cleared."""
     kind, lines = events
-    served = between(lines, "served", "end")
+    served = between(lines, "served", "workspaces" if kind == "beam" else "end")
     ok = [x for x in served if " on device " not in x]
     assert [x for x in ok if not x.endswith(f" {hg.HG_OK}")] == []
     launched = [served[i + 1].rsplit(" ", 1)[0] for i, x in enumerate(served)
@@ -58,3 +58,10 @@ def test_what_is_served(events):
     want = {"norm": ["no rows", "in place", "one row, other distance", "8 bits", "in place"],
             "beam": ["all", "rows outside the layers", "nothing in it"]}[kind]
     assert launched == want
+
+
+def test_workspaces_are_aligned(events):
+    kind, lines = events
+    if kind == "beam":
+        made = [x for x in between(lines, "workspaces", "end") if x.startswith("aligned")]
+        assert made == ["aligned 1"] * 9

@@ -15,14 +15,18 @@ struct hg_beam {
   unsigned char* base = nullptr;
   size_t bytes = 0;
   // Parts of the workspace.
-  unsigned long long* list = nullptr;  // [list_slots][picks] best of each part of a row
-  float2* stats = nullptr;             // [list_slots] maximum and sum of each part
-  int* beam_of = nullptr;              // [list_slots] whose part it is
-  unsigned* arrived = nullptr;         // [max_items] CTAs that are done with an item, 0 between calls
+  unsigned long long* list = nullptr;  // [max_items * beams][picks]
+  float2* stats = nullptr;             // [part_slots][warps] maximum and sum of exponentials
+  float* maxima = nullptr;             // [part_slots][threads]
+  int* beam_of = nullptr;              // [part_slots] whose part it is
 };
 
 namespace hg {
 namespace beam {
+
+// The threads of a CTA that searches logits.
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 
 struct SelectCall {
   int items = 0;
@@ -48,7 +52,7 @@ cudaError_t select_prepare(const hg_beam& h);
 cudaError_t reorder_prepare();
 
 // Parts of rows that any call of the handle has at most (workspace).
-long long list_slots(const hg_beam& h);
+long long part_slots(const hg_beam& h);
 
 }  // namespace beam
 }  // namespace hg

@@ -77,9 +77,10 @@ int hg_beam_create(int max_items, int beams, int vocab, int picks, int dtype, hg
     delete h;
     return HG_ERR_CUDA;
   }
-  const size_t slots = (size_t)hg::beam::list_slots(*h);
-  h->bytes = slots * picks * sizeof(*h->list) + slots * sizeof(*h->stats) +
-             slots * sizeof(*h->beam_of) + (size_t)max_items * sizeof(*h->arrived);
+  const size_t slots = (size_t)hg::beam::part_slots(*h), rows = (size_t)max_items * beams;
+  h->bytes = slots * (hg::beam::kThreads * sizeof(*h->maxima) +
+                      hg::beam::kWarps * sizeof(*h->stats) + sizeof(*h->beam_of)) +
+             rows * picks * sizeof(*h->list);
   void* p = nullptr;
   if (cudaMalloc(&p, h->bytes) != cudaSuccess) {
     cudaGetLastError();  // leave no sticky allocation error behind
@@ -87,16 +88,11 @@ int hg_beam_create(int max_items, int beams, int vocab, int picks, int dtype, hg
     return HG_ERR_CUDA;
   }
   h->base = static_cast<unsigned char*>(p);
-  h->list = static_cast<unsigned long long*>(p);
-  h->stats = reinterpret_cast<float2*>(h->list + slots * picks);
-  h->beam_of = reinterpret_cast<int*>(h->stats + slots);
-  h->arrived = reinterpret_cast<unsigned*>(h->beam_of + slots);
-  if (cudaMemset(h->arrived, 0, (size_t)max_items * sizeof(*h->arrived)) != cudaSuccess ||
-      cudaDeviceSynchronize() != cudaSuccess) {
-    cudaFree(p);
-    delete h;
-    return HG_ERR_CUDA;
-  }
+  // The most aligned first.
+  h->maxima = static_cast<float*>(p);
+  h->stats = reinterpret_cast<float2*>(h->maxima + slots * hg::beam::kThreads);
+  h->list = reinterpret_cast<unsigned long long*>(h->stats + slots * hg::beam::kWarps);
+  h->beam_of = reinterpret_cast<int*>(h->list + rows * picks);
   *out = h;
   return HG_OK;
 }

@@ -18,7 +18,7 @@ using vocab::let_successor_start;
 using vocab::load_id;
 using vocab::wait_for_predecessor;
 
-constexpr int kThreads = 128;
+constexpr int kMoveThreads = 128;
 constexpr int kInFlight = 8;  // loads of a thread that are under way at once
 constexpr int kStates = 32;   // states of one launch
 
@@ -67,15 +67,15 @@ __device__ __forceinline__ void move(const State& s, size_t row0, unsigned long 
     }
 #pragma unroll
     for (int i = 0; i < kInFlight; ++i)
-      if (b[i] >= 0) held[b[i] * kThreads] = v[i];
+      if (b[i] >= 0) held[b[i] * kMoveThreads] = v[i];
   }
   for (; moved; moved &= moved - 1) {
     const int j = __ffsll((long long)moved) - 1;
-    *reinterpret_cast<W*>(at + j * s.row_stride) = held[parent[j] * kThreads];
+    *reinterpret_cast<W*>(at + j * s.row_stride) = held[parent[j] * kMoveThreads];
   }
 }
 
-__global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant__ ReorderArgs a) {
+__global__ void __launch_bounds__(kMoveThreads) reorder_kernel(const __grid_constant__ ReorderArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int parent[HG_MAX_BEAMS];
   wait_for_predecessor();
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
         needed |= 1ull << parent[j];
         moved |= 1ull << j;
       }
-    const unsigned long long column = (at - item * s.chunks) * kThreads + threadIdx.x;
+    const unsigned long long column = (at - item * s.chunks) * kMoveThreads + threadIdx.x;
     switch (s.bytes) {
       case 16:
         move(s, row0, column, needed, moved, parent, reinterpret_cast<uint4*>(smem) + threadIdx.x);
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const __grid_constant
 
 cudaError_t reorder(const hg_beam& h, const void* parents, int id_bytes, int items,
                     const hg_beam_state* states, int n_states, cudaStream_t stream) {
-  const size_t smem = (size_t)h.beams * kThreads * 16;
+  const size_t smem = (size_t)h.beams * kMoveThreads * 16;
   for (int next = 0; next < n_states;) {
     ReorderArgs a = {};
     a.parents = Ids{parents, id_bytes};
@@ -142,7 +142,7 @@ cudaError_t reorder(const hg_beam& h, const void* parents, int id_bytes, int ite
       s.pieces = in.pieces;
       s.accesses = in.piece_bytes / s.bytes;
       s.columns = in.outer * in.pieces * s.accesses;
-      s.chunks = (unsigned long long)div_up((long long)s.columns, kThreads);
+      s.chunks = (unsigned long long)div_up((long long)s.columns, kMoveThreads);
       s.first_unit = a.units;
       a.units += s.chunks * items;
       ++a.n_states;
@@ -150,7 +150,7 @@ cudaError_t reorder(const hg_beam& h, const void* parents, int id_bytes, int ite
     if (a.units == 0) continue;
     const unsigned long long most = (unsigned long long)h.sms * 16;
     const unsigned grid = (unsigned)(a.units < most ? a.units : most);
-    const cudaError_t e = launch_dependent(reorder_kernel, a, grid, kThreads, smem, 1, stream);
+    const cudaError_t e = launch_dependent(reorder_kernel, a, grid, kMoveThreads, smem, 1, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -158,7 +158,7 @@ cudaError_t reorder(const hg_beam& h, const void* parents, int id_bytes, int ite
 
 cudaError_t reorder_prepare() {
   return cudaFuncSetAttribute(reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              HG_MAX_BEAMS * kThreads * 16);
+                              HG_MAX_BEAMS * kMoveThreads * 16);
 }
 
 }  // namespace beam

@@ -1,19 +1,26 @@
 // Beam search's selection: the best continuations of each item.
 //
-// One pass over the logits. A row's candidates are ordered by their logits alone, whatever
-// its score and logsumexp are, so a part of a row gives its best `picks` as keys (ordered
-// logit, complement of the token) and, where the logsumexp is wanted, the running
-// maximum and sum of its exponentials. The rows' chunks are dealt out to the CTAs in
-// order, the same number to each; the last CTA to finish an item's chunks joins its parts.
-//
-// A thread reads ahead of itself into a ring in shared memory, and keeps the largest logit of
-// each of its cells, the elements that it has of a chunk. At the end of a part, the n-th
-// largest of the threads' maxima bounds the n-th best element from below, so only the cells
-// that reach it, little more than n, are read again (from L2) for the elements that do. What
-// a chunk costs beside its loads is a maximum and the exponentials. (Lists of the best that
-// were kept up to date chunk by chunk, by CTA or by warp, took two to four times as long.)
+// One pass over the logits, whose chunks are dealt out to the CTAs in order, the same number
+// to each. A thread reads ahead of itself into a ring in shared memory, and of a part (what a
+// CTA has of a row) keeps the largest logit and, where the logsumexp is wanted, the running
+// maximum and sum of its exponentials: nothing that a chunk costs depends on the number of
+// picks, and no warp waits for another. A second kernel, a CTA per item, joins the parts:
+// with the rows' scores and logsumexps, the n-th largest of the threads' best totals bounds
+// the item's n-th best from below, so only the threads that reach it, little more than n,
+// have their elements read again (from L2) for the candidates. (Lists of the best that were
+// kept up to date chunk by chunk, by CTA or by warp, took two to four times as long; joined by
+// the last CTA of the first kernel, an item takes 12 to 20 us of dependent steps for 256 threads.)
 
 #include <cmath>
+#ifndef SELFEW
+#define SELFEW 64ll
+#endif
+#ifndef NST
+#define NST 3
+#endif
+#ifndef NCT
+#define NCT 3
+#endif
 #include <cstring>
 
 #include "hg_beam.cuh"
@@ -30,13 +37,16 @@ using vocab::wait_for_predecessor;
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 3;      // chunks in the ring
-constexpr int kCells = 16;      // of a thread, at most, in a part
-constexpr int kList = 512;      // elements of a part, or of an item, that are ranked at once
-constexpr int kCtasPerSm = 3;
-constexpr int kMostEntries = HG_MAX_BEAMS * HG_MAX_PICKS;  // of the lists that one CTA joins
+constexpr int kLogThreads = 8;
+static_assert(1 << kLogThreads == kThreads, "groups of threads are counted in powers of two");
+constexpr int kStages = NST;       // chunks in the ring
+constexpr int kJoinThreads = 1024;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kList = 1024;      // candidates of an item that are ranked at once
+constexpr int kHits = 512;       // groups of threads whose elements are read again
+constexpr int kCtasPerSm = NCT;
+constexpr int kMostValues = 4096;  // maxima that are joined of an item
+constexpr int kLeastGroups = 8;    // of a part's threads, at least, that have a maximum: warps
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr double kLn2 = 0.693147180559945309417;
 constexpr double kLog2eOff = 1.0 - (double)kLog2e * kLn2;
@@ -63,14 +73,15 @@ struct SelectArgs {
   int beams, vocab, picks;
   int chunks;          // of a row
   int each, more;      // chunks of a CTA; the first `more` CTAs have one more
-  Divisor by_chunks, by_each, by_each_and_one, by_picks, by_beams;
+  Divisor by_chunks, by_each, by_each_and_one, by_beams, by_longest;
   int all;             // chunks of the call
   int whole_rows;      // CTAs have whole rows
-  int cell_chunks;     // chunks of a cell
-  u64* list;           // [part][picks], best first
-  float2* stats;       // [part]
+  int longest;         // chunks of a part, at most
+  int log_groups;      // groups of a CTA's threads that have a maximum each
+  float* maxima;       // [part][groups]
+  float2* stats;       // [part][warp]
   int* beam_of;        // [part], kNone where it is not searched or there is no such part
-  unsigned* arrived;   // [item]
+  u64* list;           // [row][picks], of pick_exactly
   __device__ int first_chunk(int cta) const { return min(cta * each + min(cta, more), all); }
   __device__ int cta_of(int chunk) const {
     const int front = more * (each + 1);
@@ -110,24 +121,31 @@ __device__ __forceinline__ bool searched(const SelectCall& c, size_t row) {
   return c.scores[row] > -INFINITY && !(c.finished && c.finished[row]);
 }
 
+// Copies 16 bytes into shared memory, where the thread reads them once its copies are there.
+__device__ __forceinline__ void copy_ahead(uint4* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void close_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits for all but the last N groups of this thread's copies.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // 16 bytes of logits.
 template <typename T>
 struct Access {
   static constexpr int E = 16 / sizeof(T);
   uint4 w;
 
-  // Copies 16 bytes ahead.
-  static __device__ __forceinline__ void copy(uint4* to, const void* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                     (uint32_t)__cvta_generic_to_shared(to)),
-                 "l"(from)
-                 : "memory");
-  }
-  // The same for elements [e0, e0 + E) of a row of `vocab`, some of which may lie outside:
+  // Copies elements [e0, e0 + E) of a row of `vocab` ahead, some of which may lie outside:
   // those are -inf, and are not read.
   static __device__ __forceinline__ void copy_edge(uint4* to, const T* row, int e0, int vocab) {
     if (e0 >= 0 && e0 + E <= vocab) {
-      copy(to, row + e0);
+      copy_ahead(to, row + e0);
       return;
     }
     T v[E];
@@ -269,25 +287,27 @@ __device__ __forceinline__ uint32_t bin_end(int bin) {
 
 struct BoundShared {
   int bins[kBins];
-  uint32_t top[kWarps];
+  uint32_t top[kJoinWarps];
 };
 
-// A value that at least n of the CTA's words (ordered values; 0: none) are not under, and not
-// many more: the end of the bin that the n-th largest is in. words(f) calls f for each word
-// of a thread, `top` is the thread's largest. The least finite value if there are not n.
-template <typename Words>
-__device__ __forceinline__ float bound_of_best(int n, uint32_t top, BoundShared& s, Words words) {
+// A value that at least n of the words (ordered values, K a thread; 0: none) are not under, and
+// not many more: the end of the bin that the n-th largest is in. The least finite value if
+// there are not n.
+template <int K>
+__device__ __forceinline__ float bound_of_best(int n, const uint32_t (&word)[K], BoundShared& s) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < K; ++k) top = max(top, word[k]);
   top = __reduce_max_sync(kAll, top);
   if (lane == 0) s.top[threadIdx.x >> 5] = top;
-  for (int i = threadIdx.x; i < kBins; i += kThreads) s.bins[i] = 0;
+  if (threadIdx.x < kBins) s.bins[threadIdx.x] = 0;
   __syncthreads();
+  top = __reduce_max_sync(kAll, s.top[lane]);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = max(top, s.top[w]);
-  words([&](uint32_t word) {
-    if (word) atomicAdd(&s.bins[bin_of(top - word)], 1);
-  });
+  for (int k = 0; k < K; ++k)
+    if (word[k]) atomicAdd(&s.bins[bin_of(top - word[k])], 1);
   __syncthreads();
   // The first bin up to which there are enough; each warp for itself, eight bins a lane.
   int upto[8];
@@ -302,26 +322,18 @@ __device__ __forceinline__ float bound_of_best(int n, uint32_t top, BoundShared&
   }
   const unsigned reach = __ballot_sync(kAll, before >= n);
   before -= upto[7];
-  int bin = lane * 8 + 7;
+  int bin = lane * 8;
 #pragma unroll
-  for (int i = 6; i >= 0; --i)
-    if (before + upto[i] >= n) bin = lane * 8 + i;
+  for (int i = 0; i < 7; ++i) bin += before + upto[i] < n;
   if (!reach) return kLeast;
   const uint32_t far = bin_end(__shfl_sync(kAll, bin, __ffs(reach) - 1));
-  const uint32_t word = far < top ? top - far : 0;
-  return word < ordered(kLeast) ? kLeast : unordered(word);
+  const uint32_t w = far < top ? top - far : 0;
+  return w < ordered(kLeast) ? kLeast : unordered(w);
 }
 
-struct PartShared {
-  float cell[kCells][kThreads];
-  u64 list[kList];
-  BoundShared bound;
-  float most[kWarps], sum[kWarps];
-  int warp_count[2][kWarps];
-  int count;
-};
+// ---- one CTA's part of a row -------------------------------------------------------
 
-// A part: chunks [first, first + chunks) of a row.
+// Chunks [first, first + chunks) of a row, as the threads of a CTA have them.
 template <typename T, int R>
 struct Part {
   static constexpr int E = Access<T>::E;
@@ -331,19 +343,20 @@ struct Part {
   __device__ __forceinline__ int shift() const {
     return (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
   }
-  // The first element of this thread's access k of chunk i.
-  __device__ __forceinline__ int element(int i, int k) const {
-    return (((first + i) * R + k) * kThreads + (int)threadIdx.x) * E - shift();
+  // The first element of a thread's access k of chunk i.
+  __device__ __forceinline__ int element(int thread, int i, int k) const {
+    return (((first + i) * R + k) * kThreads + thread) * E - shift();
   }
-  // Calls f(logit, token) for the elements of this thread from `least` on, in chunk i.
+  // Calls f(logit, token) for the elements of a thread from `least` on, in chunk i.
   template <typename F>
-  __device__ __forceinline__ void each(int i, float least, F f) const {
+  __device__ __forceinline__ void each(int thread, int i, float least, F f) const {
     uint32_t mask = 0;
-    const int e0 = element(i, 0) - (int)threadIdx.x * E;
+    const int e0 = element(0, i, 0);
     if (e0 >= 0 && e0 + kThreads * R * E <= vocab) {
       Access<T> x[R];  // all loads before the first use
 #pragma unroll
-      for (int k = 0; k < R; ++k) x[k].w = *reinterpret_cast<const uint4*>(row + element(i, k));
+      for (int k = 0; k < R; ++k)
+        x[k].w = *reinterpret_cast<const uint4*>(row + element(thread, i, k));
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         float v[E];
@@ -354,129 +367,65 @@ struct Part {
     } else {
 #pragma unroll 4
       for (int m = 0; m < R * E; ++m) {
-        const int at = element(i, m / E) + m % E;
+        const int at = element(thread, i, m / E) + m % E;
         if (at >= 0 && at < vocab && Elem<T>::up(row[at]) >= least) mask |= 1u << m;
       }
     }
     for (; mask; mask &= mask - 1) {
-      const int m = __ffs(mask) - 1, at = element(i, m / E) + m % E;
+      const int m = __ffs(mask) - 1, at = element(thread, i, m / E) + m % E;
       f(Elem<T>::up(row[at]), at);
     }
   }
 };
 
-__device__ __forceinline__ int count_all(int c, int turn, PartShared& s) {
-  c = __reduce_add_sync(0xffffffffu, c);
-  if ((threadIdx.x & 31) == 0) s.warp_count[turn][threadIdx.x >> 5] = c;
-  __syncthreads();
-  c = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) c += s.warp_count[turn][w];
-  return c;
-}
-
-// Where too many elements of a part are alike for the list: the key of its n-th best, one
-// bit after another, and the keys from that on. Reads the part again for each bit.
-template <typename T, int R>
-__device__ __noinline__ void list_exactly(const Part<T, R> part, int n, PartShared& s) {
-  u64 bound = 0;
-  for (int bit = 63; bit >= 0; --bit) {
-    const u64 next = bound | 1ull << bit;
-    int c = 0;
-    for (int i = 0; i < part.chunks; ++i)
-      part.each(i, kLeast, [&](float x, int token) { c += key_of(x, token) >= next; });
-    if (count_all(c, bit & 1, s) >= n) bound = next;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) s.count = 0;
-  __syncthreads();
-  for (int i = 0; i < part.chunks; ++i)
-    part.each(i, kLeast, [&](float x, int token) {
-      if (key_of(x, token) >= bound) s.list[atomicAdd(&s.count, 1)] = key_of(x, token);
-    });
-  __syncthreads();
-}
-
-template <typename T, int R>
-__device__ __forceinline__ void finish_part(const SelectArgs& a, int number, int beam,
-                                            const Part<T, R>& part, Exponentials& sums,
-                                            PartShared& s) {
-  constexpr unsigned kAll = 0xffffffffu;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  u64* out = a.list + (size_t)number * a.picks;
-  if (threadIdx.x == 0) a.beam_of[number] = part.row ? beam : kNone;
-  if (!part.row) return;
-  if (!a.c.lse) {
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1)
-      sums.join(__shfl_xor_sync(kAll, sums.most, m), __shfl_xor_sync(kAll, sums.sum, m));
-    if (lane == 0) {
-      s.most[warp] = sums.most;
-      s.sum[warp] = sums.sum;
-    }
-  }
-  if (threadIdx.x == 0) s.count = 0;
-  const int cells = (part.chunks + a.cell_chunks - 1) / a.cell_chunks;
-  float most = -INFINITY;
-  for (int i = 0; i < cells; ++i) most = fmaxf(most, s.cell[i][threadIdx.x]);
-  const uint32_t word = most > -INFINITY ? ordered(most) : 0;
-  const float from = bound_of_best(a.picks, word, s.bound, [&](auto f) { f(word); });
-  if (!a.c.lse && threadIdx.x == 0) {
-    for (int w = 1; w < kWarps; ++w) sums.join(s.most[w], s.sum[w]);
-    a.stats[number] = make_float2(sums.most, sums.sum);
-  }
-  if (most >= from)
-    for (int i = 0; i < cells; ++i) {
-      if (!(s.cell[i][threadIdx.x] >= from)) continue;
-      for (int j = i * a.cell_chunks; j < min((i + 1) * a.cell_chunks, part.chunks); ++j)
-        part.each(j, from, [&](float x, int token) {
-          const int at = atomicAdd(&s.count, 1);
-          if (at < kList) s.list[at] = key_of(x, token);
-        });
-    }
-  __syncthreads();
-  int all = s.count;
-  if (all > kList) {
-    list_exactly(part, a.picks, s);
-    all = s.count;
-  }
-  // Each key's rank among them; eight lanes count what is above it.
-  const int eighth = threadIdx.x % 8;
-  for (int i0 = 0; i0 < all; i0 += kThreads / 8) {
-    const int i = i0 + threadIdx.x / 8;
-    const u64 mine = i < all ? s.list[i] : ~0ull;
-    int rank = 0;
-#pragma unroll 4
-    for (int j = eighth; j < all; j += 8) rank += s.list[j] > mine;
-#pragma unroll
-    for (int m = 4; m > 0; m >>= 1) rank += __shfl_xor_sync(kAll, rank, m);
-    if (eighth == 0 && i < all && rank < a.picks) out[rank] = mine;
-  }
-  for (int i = all + threadIdx.x; i < a.picks; i += kThreads) out[i] = 0;
-  __syncthreads();
-  sums = Exponentials();
-}
-
 // ---- joining an item's parts -------------------------------------------------------
+
+// A group of threads whose largest logit reaches the bound: what it has of a row.
+struct Hit {
+  int row, first, chunks, thread;
+};
 
 struct JoinShared {
   u64 total[kList], key[kList];
   unsigned char beam[kList];
+  Hit hit[kHits];
+  BoundShared bound;
   double lse[HG_MAX_BEAMS];
   float score[HG_MAX_BEAMS];
   float near[HG_MAX_BEAMS];  // score - logsumexp in fp32
   bool done[HG_MAX_BEAMS];   // finished, and still a candidate
   float largest[2];          // magnitude of near, below kHuge, of 32 beams each
-  BoundShared bound;
-  double top_total[kWarps];
-  u64 top_key[kWarps];
-  int top_beam[kWarps];
-  int count;
-};
+  bool reaches[HG_MAX_BEAMS];  // the bound, by a logit
+  int warp_count[2][kJoinWarps];
+  double top_total[kJoinWarps];
+  u64 top_key[kJoinWarps];
+  int top_beam[kJoinWarps];
+  int hits, count;
 
-union Shared {
-  PartShared part;
-  JoinShared join;
+  // The total of a beam's logit, as it is compared.
+  __device__ __forceinline__ double sum(int b, float x) const {
+    return (double)score[b] + ((double)x - lse[b]);
+  }
+  // The same to within `off` of it in fp32 (64-bit additions are slow, and few candidates
+  // come near the best).
+  __device__ __forceinline__ float nearly(int b, float x) const {
+    const float t = x + near[b];
+    return fabsf(near[b]) < kHuge && fabsf(t) < kHuge ? t : (float)sum(b, x);
+  }
+  // Three roundings of at most half a unit in the last place of the two terms and of the sum.
+  __device__ __forceinline__ float off(float t) const {
+    const float most = fmaxf(largest[0], largest[1]);
+    return fabsf(t) < INFINITY ? 3.f * 5.9604645e-8f * (most + fabsf(t)) : 0.f;
+  }
+  // Lists a candidate that fp32 can tell from -inf.
+  __device__ __noinline__ void add(double t, int b, u64 k) {
+    if (!((float)t > -INFINITY)) return;
+    const int at = atomicAdd(&count, 1);
+    if (at >= kList) return;
+    total[at] = ordered(t);
+    key[at] = k;
+    beam[at] = (unsigned char)b;
+  }
 };
 
 // A candidate of an item, in the order of the picks.
@@ -499,8 +448,8 @@ __device__ __forceinline__ void put_id(void* p, int bytes, size_t i, int v) {
     static_cast<int*>(p)[i] = v;
 }
 
-__device__ void put_pick(const SelectArgs& a, int item, int rank, bool there, double total,
-                         int beam, u64 key) {
+__device__ __forceinline__ void put_pick(const SelectArgs& a, int item, int rank, bool there,
+                                         double total, int beam, u64 key) {
   const SelectCall& c = a.c;
   const size_t at = (size_t)item * a.picks + rank;
   const int token = there ? (int)~(uint32_t)key : -1;
@@ -512,13 +461,13 @@ __device__ void put_pick(const SelectArgs& a, int item, int rank, bool there, do
         there && (token == c.end || (c.finished && c.finished[(size_t)item * a.beams + beam]));
 }
 
-// Logsumexp of a row from its parts, by one warp. The logarithm of the sum's exponent is
-// exact to 64 bits, that of its mantissa, below 0.35, to 32.
+// Logsumexp of a row from what its parts' warps have, by one warp. The logarithm of the
+// sum's exponent is exact to 64 bits, that of its mantissa, below 0.35, to 32.
 __device__ __forceinline__ double row_lse(const SelectArgs& a, int part0, int parts) {
   const int lane = threadIdx.x & 31;
   Exponentials t;
-  for (int i = lane; i < parts; i += 32) {
-    const float2 s = __ldcg(a.stats + part0 + i);
+  for (int i = lane; i < parts * kWarps; i += 32) {
+    const float2 s = __ldcg(a.stats + (size_t)part0 * kWarps + i);
     t.join(s.x, s.y);
   }
 #pragma unroll
@@ -538,171 +487,73 @@ __device__ __forceinline__ double row_lse(const SelectArgs& a, int part0, int pa
                      : -INFINITY;
 }
 
-// What join_item compares: the entries of the parts' lists, and behind them one of each
-// finished beam.
-struct Entries {
-  const SelectArgs& a;
-  const JoinShared& s;
-  int listed, all;
-  const u64* list;     // of the item's first part
-  const int* beam_of;
+__device__ __forceinline__ int count_all(int c, int turn, JoinShared& s) {
+  c = __reduce_add_sync(0xffffffffu, c);
+  if ((threadIdx.x & 31) == 0) s.warp_count[turn][threadIdx.x >> 5] = c;
+  __syncthreads();
+  return __reduce_add_sync(0xffffffffu, s.warp_count[turn][threadIdx.x & 31]);
+}
 
-  // Entry i's beam (kNone: no candidate) and key; both loads are in flight together.
-  __device__ __forceinline__ void get(int i, int& beam, u64& key) const {
-    const int in = min(i, listed - 1);
-    key = __ldcg(list + in);
-    beam = __ldcg(beam_of + a.by_picks.divide(in));
-    if (key == 0) beam = kNone;
-    if (i >= listed) {
-      key = (uint32_t)~a.c.end;
-      beam = i < all && s.done[i - listed] ? i - listed : kNone;
-    }
-  }
-  __device__ __forceinline__ double total(int i, int beam, u64 key) const {
-    const double score = s.score[beam];
-    return i < listed ? score + ((double)unordered((uint32_t)(key >> 32)) - s.lse[beam]) : score;
-  }
-  // A total to within `off` of it in fp32 (64-bit additions are slow, and few entries come
-  // near the best).
-  __device__ __forceinline__ float near(int i, int beam, u64 key) const {
-    if (i >= listed) return s.score[beam];
-    const float near = s.near[beam], t = unordered((uint32_t)(key >> 32)) + near;
-    return fabsf(near) < kHuge && fabsf(t) < kHuge ? t : (float)total(i, beam, key);
-  }
-  // Three roundings of at most half a unit in the last place of the two terms and of the sum.
-  __device__ __forceinline__ float off(float t) const {
-    const float near = fmaxf(s.largest[0], s.largest[1]);
-    return fabsf(t) < INFINITY ? 3.f * 5.9604645e-8f * (near + fabsf(t)) : 0.f;
-  }
-};
-
-__device__ __noinline__ void join_item(const SelectArgs& a, int item, JoinShared& s,
-                                       float* value) {
-  const SelectCall& c = a.c;
+// Where too many candidates are alike for the list: the best of each row that has some,
+// exactly (the key of the n-th best, one bit after another, reading the row again for each),
+// and of those one pick after another.
+template <typename T, int R>
+__device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinShared& s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row0 = item * a.beams, row_last = row0 + a.beams - 1;
-  const int part0 = a.part_of(a.cta_of(row0 * a.chunks), row0);
-  const int parts = a.part_of(a.cta_of((row_last + 1) * a.chunks - 1), row_last) - part0 + 1;
-  const int listed = parts * a.picks;
-  const Entries entries{a, s, listed, listed + (c.finished ? a.beams : 0),
-                        a.list + (size_t)part0 * a.picks, a.beam_of + part0};
-  // What of the entries is loaded at once, and first of all.
-  constexpr int kBatch = 4;
-  u64 key[kBatch];
-  int beam[kBatch];
-  auto load = [&](int i0) {
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) entries.get(i0 + k * kThreads, beam[k], key[k]);
-  };
-  float near = 0.f;
-  if (threadIdx.x < a.beams) {
-    const int b = threadIdx.x, row = row0 + b;
-    const float score = c.scores[row];
-    s.score[b] = score;
-    s.done[b] = c.finished && c.finished[row] && score > -INFINITY;
-    if (c.lse) {
-      const double lse = c.lse[row * c.lse_stride];
-      s.lse[b] = lse;
-      near = (float)((double)score - lse);
-      s.near[b] = near;
-    }
-  }
-  if (threadIdx.x == 0) s.count = 0;
-  if (!c.lse) {
-    for (int b = warp; b < a.beams; b += kWarps) {
-      const int row = row0 + b, first = a.part_of(a.cta_of(row * a.chunks), row);
-      const double lse =
-          searched(c, row)
-              ? row_lse(a, first, a.part_of(a.cta_of((row + 1) * a.chunks - 1), row) - first + 1)
-              : 0.0;
-      if (lane == 0) {
-        s.lse[b] = lse;
-        s.near[b] = (float)((double)c.scores[row] - lse);
+  const int thread = threadIdx.x % kThreads, first = threadIdx.x / kThreads;
+  constexpr int kStep = kJoinThreads / kThreads;
+  const int row0 = item * a.beams, n = a.picks;
+  for (int b = 0; b < a.beams; ++b) {
+    u64* list = a.list + (size_t)(row0 + b) * n;
+    for (int i = threadIdx.x; i < n; i += kJoinThreads) list[i] = 0;
+    if (!s.reaches[b]) continue;
+    const Part<T, R> part = {static_cast<const T*>(a.c.logits) + (size_t)(row0 + b) * a.c.ld, 0,
+                             a.chunks, a.vocab};
+    // All tokens' complements have the bits above the vocabulary's.
+    const int low = 32 - __clz(a.vocab);
+    u64 bound = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+      if (bit == 31) {
+        bound |= ~0u << low;
+        bit = low - 1;
       }
+      const u64 next = bound | 1ull << bit;
+      int c = 0;
+      for (int i = first; i < part.chunks; i += kStep)
+        part.each(thread, i, kLeast, [&](float x, int token) { c += key_of(x, token) >= next; });
+      c = count_all(c, bit & 1, s);
+      if (c >= n) bound = next;
+      if (c == n) break;
     }
+    __syncthreads();
+    if (threadIdx.x == 0) s.count = 0;
+    __syncthreads();
+    for (int i = first; i < part.chunks; i += kStep)
+      part.each(thread, i, kLeast, [&](float x, int token) {
+        if (key_of(x, token) < bound) return;
+        const int at = atomicAdd(&s.count, 1);
+        if (at < n) list[at] = key_of(x, token);
+      });
   }
-  __syncthreads();
-  load(threadIdx.x);
-  // How large the terms of a total are at most, for its rounding.
-  if (!c.lse && threadIdx.x < a.beams) near = s.near[threadIdx.x];
-  near = fabsf(near) < kHuge ? fabsf(near) : 0.f;
-  const uint32_t largest = __reduce_max_sync(0xffffffffu, __float_as_uint(near));
-  if (lane == 0 && warp < 2) s.largest[warp] = __uint_as_float(largest);
-  static_assert(HG_MAX_BEAMS <= 64, "two warps have the beams");
-  __syncthreads();
-  // The entries' totals, nearly; the words of a bound from below.
-  uint32_t top = 0;
-  for (int i0 = threadIdx.x;;) {
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * kThreads;
-      if (i >= entries.all) break;
-      const float t = beam[k] != kNone ? entries.near(i, beam[k], key[k]) : -INFINITY;
-      value[i] = t;
-      if (t > -INFINITY) top = max(top, ordered(t - entries.off(t)));
-    }
-    i0 += kBatch * kThreads;
-    if (i0 >= entries.all) break;
-    load(i0);
-  }
-  const float from = bound_of_best(a.picks, top, s.bound, [&](auto f) {
-#pragma unroll 4
-    for (int i = threadIdx.x; i < entries.all; i += kThreads)
-      f(value[i] > -INFINITY ? ordered(value[i] - entries.off(value[i])) : 0);
-  });
-  for (int i = threadIdx.x; i < entries.all; i += kThreads) {
-    if (!(value[i] + entries.off(value[i]) >= from)) continue;
-    int beam;
-    u64 key;
-    entries.get(i, beam, key);
-    if (beam == kNone) continue;
-    const double total = entries.total(i, beam, key);
-    if (!((float)total > -INFINITY)) continue;
-    const int at = atomicAdd(&s.count, 1);
-    if (at >= kList) continue;
-    s.total[at] = ordered(total);
-    s.key[at] = key;
-    s.beam[at] = (unsigned char)beam;
-  }
-  __syncthreads();
-  const int all = s.count;
-  if (all <= kList) {
-    // Eight lanes count what comes before a candidate.
-    const int eighth = threadIdx.x % 8;
-    for (int i0 = 0; i0 < all; i0 += kThreads / 8) {
-      const int i = i0 + threadIdx.x / 8;
-      const bool there = i < all;
-      const u64 total = there ? s.total[i] : ~0ull, key = there ? s.key[i] : ~0ull;
-      const int beam = there ? s.beam[i] : 0;
-      int rank = 0;
-#pragma unroll 4
-      for (int j = eighth; j < all; j += 8) {
-        const u64 t = s.total[j], k = s.key[j];
-        const int b = s.beam[j];
-        rank += (t > total) | ((t == total) & ((b < beam) | ((b == beam) & (k > key))));
-      }
-#pragma unroll
-      for (int m = 4; m > 0; m >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, m);
-      if (there && eighth == 0 && rank < a.picks) {
-        const double d =
-            __longlong_as_double((long long)(total >> 63 ? total & ~(1ull << 63) : ~total));
-        put_pick(a, item, rank, true, d, beam, key);
-      }
-    }
-    for (int i = all + threadIdx.x; i < a.picks; i += kThreads)
-      put_pick(a, item, i, false, 0.0, -1, 0);
-    return;
-  }
-  // Too many alike: one pick after another.
+  __syncthreads();  // the lists are this CTA's own
+  const int listed = a.beams * n, all = listed + (a.c.finished ? a.beams : 0);
   Candidate under;
-  for (int i = 0; i < a.picks; ++i) {
+  for (int i = 0; i < n; ++i) {
     Candidate top;
     top.beam = -1;
-    for (int j = threadIdx.x; j < entries.all; j += kThreads) {
+    for (int j = threadIdx.x; j < all; j += kJoinThreads) {
       Candidate t;
-      entries.get(j, t.beam, t.key);
-      if (t.beam == kNone) continue;
-      t.total = entries.total(j, t.beam, t.key);
+      if (j < listed) {
+        t.beam = j / n;
+        t.key = a.list[(size_t)row0 * n + j];
+        if (!t.key) continue;
+        t.total = s.sum(t.beam, unordered((uint32_t)(t.key >> 32)));
+      } else {
+        t.beam = j - listed;
+        t.key = (uint32_t)~a.c.end;
+        if (!s.done[t.beam]) continue;
+        t.total = s.score[t.beam];
+      }
       if (!((float)t.total > -INFINITY)) continue;
       if ((i == 0 || under.before(t)) && t.before(top)) top = t;
     }
@@ -721,7 +572,7 @@ __device__ __noinline__ void join_item(const SelectArgs& a, int item, JoinShared
       s.top_key[warp] = top.key;
     }
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kJoinWarps; ++w) {
       const Candidate o = {s.top_total[w], s.top_beam[w], s.top_key[w]};
       if (o.before(top)) top = o;
     }
@@ -730,16 +581,165 @@ __device__ __noinline__ void join_item(const SelectArgs& a, int item, JoinShared
   }
 }
 
+constexpr int kValues = kMostValues / kJoinThreads + 1;  // of a thread: groups, a finished beam
+
+template <typename T, int R>
+__global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const __grid_constant__ SelectArgs a) {
+  __shared__ JoinShared s;
+  wait_for_predecessor();
+  let_successor_start();
+  const SelectCall& c = a.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int item = blockIdx.x, row0 = item * a.beams, row_last = row0 + a.beams - 1;
+  const int part0 = a.part_of(a.cta_of(row0 * a.chunks), row0);
+  const int parts = a.part_of(a.cta_of((row_last + 1) * a.chunks - 1), row_last) - part0 + 1;
+  // The groups' maxima; the last value of a thread is a finished beam's score.
+  const int listed = parts << a.log_groups;
+  const float* maxima = a.maxima + ((size_t)part0 << a.log_groups);
+  float value[kValues];
+  int beam[kValues];
+#pragma unroll
+  for (int k = 0; k < kValues - 1; ++k) {
+    const int i = min((int)threadIdx.x + k * kJoinThreads, listed - 1);
+    value[k] = __ldcg(maxima + i);
+    beam[k] = __ldcg(a.beam_of + part0 + (i >> a.log_groups));
+  }
+  float near = 0.f;
+  value[kValues - 1] = -INFINITY;
+  if ((int)threadIdx.x < a.beams) {
+    const int b = threadIdx.x, row = row0 + b;
+    const float score = c.scores[row];
+    const bool done = c.finished && c.finished[row] && score > -INFINITY;
+    const double lse = c.lse ? (double)c.lse[row * c.lse_stride] : 0.0;
+    near = (float)((double)score - lse);
+    s.score[b] = score;
+    s.done[b] = done;
+    s.lse[b] = lse;
+    s.near[b] = near;
+    s.reaches[b] = false;
+    if (done) value[kValues - 1] = score;
+  }
+  if (threadIdx.x == 0) s.hits = s.count = 0;
+  if (!c.lse) {
+    __syncthreads();
+    for (int b = warp; b < a.beams; b += kJoinWarps) {
+      const int row = row0 + b, first = a.part_of(a.cta_of(row * a.chunks), row);
+      if (!searched(c, row)) continue;
+      const double lse =
+          row_lse(a, first, a.part_of(a.cta_of((row + 1) * a.chunks - 1), row) - first + 1);
+      if (lane == 0) {
+        s.lse[b] = lse;
+        s.near[b] = (float)((double)s.score[b] - lse);
+      }
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < a.beams) near = s.near[threadIdx.x];
+  }
+  // How large the terms of a total are at most, for its rounding.
+  near = fabsf(near) < kHuge ? fabsf(near) : 0.f;
+  const uint32_t largest = __reduce_max_sync(0xffffffffu, __float_as_uint(near));
+  if (lane == 0 && warp < 2) s.largest[warp] = __uint_as_float(largest);
+  static_assert(HG_MAX_BEAMS <= 64, "two warps have the beams");
+  __syncthreads();
+
+  // The groups' best totals, nearly, and their words from below.
+  uint32_t word[kValues];
+#pragma unroll
+  for (int k = 0; k < kValues; ++k) {
+    float t = value[k];
+    if (k < kValues - 1) {
+      const bool there = (int)threadIdx.x + k * kJoinThreads < listed && beam[k] != kNone;
+      t = there && t > -INFINITY ? s.nearly(beam[k], t) : -INFINITY;
+    }
+    value[k] = t;
+    word[k] = t > -INFINITY ? ordered(t - s.off(t)) : 0;
+  }
+  const float from = bound_of_best(a.picks, word, s.bound);
+#pragma unroll
+  for (int k = 0; k < kValues; ++k) {
+    if (!(value[k] + s.off(value[k]) >= from)) continue;
+    if (k == kValues - 1) {
+      s.add(value[k], threadIdx.x, (uint32_t)~c.end);
+      continue;
+    }
+    s.reaches[beam[k]] = true;
+    const int at = atomicAdd(&s.hits, 1);
+    if (at >= kHits) continue;
+    const int i = threadIdx.x + k * kJoinThreads;
+    const int part = i >> a.log_groups, group = i - (part << a.log_groups);
+    const int row = row0 + beam[k], begin = row * a.chunks, end = begin + a.chunks;
+    int first = begin, last = end;
+    if (!a.whole_rows) {
+      first = max(begin, a.first_chunk(part0 + part - row));
+      last = min(end, a.first_chunk(part0 + part - row + 1));
+    }
+    s.hit[at] = {row, first - begin, last - first, group << (kLogThreads - a.log_groups)};
+  }
+  __syncthreads();
+  const int hits = s.hits;
+  if (hits <= kHits) {
+    // The groups' elements, a thread's of a chunk each.
+    const int log_width = kLogThreads - a.log_groups;
+    const int units = (hits * a.longest) << log_width;
+    for (int u = threadIdx.x; u < units; u += kJoinThreads) {
+      const int pair = u >> log_width, h = a.by_longest.divide(pair);
+      const Hit hit = s.hit[h];
+      const int chunk = pair - h * a.longest, b = hit.row - row0;
+      if (chunk >= hit.chunks) continue;
+      const Part<T, R> part = {static_cast<const T*>(c.logits) + (size_t)hit.row * c.ld, hit.first,
+                               hit.chunks, a.vocab};
+      // From which logit on a total may reach the bound: well below it.
+      const float least = from - s.near[b];
+      const bool plain = fabsf(s.near[b]) < kHuge && fabsf(least) < kHuge;
+      part.each(hit.thread + (u & ((1 << log_width) - 1)), chunk,
+                plain ? least - 4.f * s.off(fabsf(from) + fabsf(least)) : kLeast,
+                [&](float x, int token) {
+                  const float t = s.nearly(b, x);
+                  if (t + s.off(t) >= from) s.add(s.sum(b, x), b, key_of(x, token));
+                });
+    }
+  }
+  __syncthreads();
+  const int found = s.count;
+  if (hits > kHits || found > kList) {
+    pick_exactly<T, R>(a, item, s);
+    return;
+  }
+  // Each candidate's rank; eight lanes count what comes before it.
+  const int eighth = threadIdx.x % 8;
+  for (int i0 = 0; i0 < found; i0 += kJoinThreads / 8) {
+    const int i = i0 + threadIdx.x / 8;
+    const bool there = i < found;
+    const u64 total = there ? s.total[i] : ~0ull, key = there ? s.key[i] : ~0ull;
+    const int b = there ? s.beam[i] : 0;
+    int rank = 0;
+#pragma unroll 4
+    for (int j = eighth; j < found; j += 8) {
+      const u64 t = s.total[j], k = s.key[j];
+      const int o = s.beam[j];
+      rank += (t > total) | ((t == total) & ((o < b) | ((o == b) & (k > key))));
+    }
+#pragma unroll
+    for (int m = 4; m > 0; m >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, m);
+    if (there && eighth == 0 && rank < a.picks) {
+      const double d =
+          __longlong_as_double((long long)(total >> 63 ? total & ~(1ull << 63) : ~total));
+      put_pick(a, item, rank, true, d, b, key);
+    }
+  }
+  for (int i = found + threadIdx.x; i < a.picks; i += kJoinThreads)
+    put_pick(a, item, i, false, 0.0, -1, 0);
+}
+
 template <typename T, int R>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     select_kernel(const __grid_constant__ SelectArgs a) {
   constexpr int E = Access<T>::E;
   extern __shared__ uint4 ring[];  // [stage][R][threads]: a thread reads what it copied
-  __shared__ Shared s;
-  __shared__ bool last;
   wait_for_predecessor();
   let_successor_start();
   const int g0 = a.first_chunk(blockIdx.x), g1 = a.first_chunk(blockIdx.x + 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
   // The chunk that is copied next, and its row (null: its logits do not count).
   int ahead = g0, ahead_row = a.by_chunks.divide(g0), ahead_chunk = g0 - ahead_row * a.chunks;
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (e0 >= 0 && e0 + kThreads * R * E <= a.vocab) {
           const uint4* from = reinterpret_cast<const uint4*>(ahead_at + e0) + threadIdx.x;
 #pragma unroll
-          for (int k = 0; k < R; ++k) Access<T>::copy(to + k * kThreads, from + k * kThreads);
+          for (int k = 0; k < R; ++k) copy_ahead(to + k * kThreads, from + k * kThreads);
         } else {
 #pragma unroll 1
           for (int k = 0; k < R; ++k)
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         ++ahead_row;
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    close_copies();
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) copy(i);
@@ -780,52 +780,44 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   // A part's number that the last CTA's end and this one's beginning leave out.
   if (chunk == 0 && blockIdx.x > 0 && !a.whole_rows && threadIdx.x == 0)
     a.beam_of[a.part_of(blockIdx.x, row) - 1] = kNone;
-  const T* at = enter(row);
   Exponentials sums;
-  Part<T, R> part = {enter(row), chunk, 0, a.vocab};
-  float cell = -INFINITY;
-  int in_cell = 0, cells = 0;
+  float best = -INFINITY;
+  bool on = enter(row) != nullptr;
   for (int g = g0; g < g1; ++g) {
     copy(stage == 0 ? kStages - 1 : stage - 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-    if (part.row) {
+    wait_copies<kStages - 1>();
+    if (on) {
       const uint4* mine = ring + stage * R * kThreads + threadIdx.x;
       Access<T> x[R];
 #pragma unroll
       for (int k = 0; k < R; ++k) x[k].w = mine[k * kThreads];
       const float most = largest<T, R>(x);
       if (!a.c.lse) sums.add(x, mine, most);
-      cell = fmaxf(cell, most);
+      best = fmaxf(best, most);
     }
     if (++stage == kStages) stage = 0;
-    ++part.chunks;
-    const bool ends = ++chunk == a.chunks || g + 1 == g1;
-    if (++in_cell == a.cell_chunks || ends) {
-      s.part.cell[cells++][threadIdx.x] = cell;
-      cell = -INFINITY;
-      in_cell = 0;
+    if (++chunk < a.chunks && g + 1 < g1) continue;
+    // The part's end: its warps leave what they have, without waiting for one another.
+    const int part = a.part_of(blockIdx.x, row);
+    if (threadIdx.x == 0) a.beam_of[part] = on ? row - a.by_beams.divide(row) * a.beams : kNone;
+    if (on) {
+      if (!a.c.lse) {
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1)
+          sums.join(__shfl_xor_sync(0xffffffffu, sums.most, m),
+                    __shfl_xor_sync(0xffffffffu, sums.sum, m));
+        if (lane == 0) a.stats[(size_t)part * kWarps + warp] = make_float2(sums.most, sums.sum);
+      }
+      const int log_width = kLogThreads - a.log_groups;
+      for (int m = 1; m < 1 << log_width; m <<= 1)
+        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, m));
+      if ((threadIdx.x & ((1 << log_width) - 1)) == 0)
+        a.maxima[((size_t)part << a.log_groups) + (threadIdx.x >> log_width)] = best;
     }
-    if (ends) {
-      finish_part(a, a.part_of(blockIdx.x, row), row - a.by_beams.divide(row) * a.beams, part, sums,
-                  s.part);
-      cells = chunk = 0;
-      if (g + 1 < g1) part = {enter(++row), 0, 0, a.vocab};
-    }
-  }
-  __threadfence();
-  const int item_chunks = a.beams * a.chunks;
-  const int last_item = a.by_beams.divide(a.by_chunks.divide(g1 - 1));
-  for (int item = a.by_beams.divide(a.by_chunks.divide(g0)); item <= last_item; ++item) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      const int from = item * item_chunks;
-      const unsigned before = (unsigned)(a.cta_of(from + item_chunks - 1) - a.cta_of(from));
-      last = atomicInc(a.arrived + item, before) == before;  // and back to 0
-    }
-    __syncthreads();
-    if (!last) continue;
-    __threadfence();
-    join_item(a, item, s.join, reinterpret_cast<float*>(ring));
+    sums = Exponentials();
+    best = -INFINITY;
+    chunk = 0;
+    if (g + 1 < g1) on = enter(++row) != nullptr;
   }
 }
 
@@ -837,41 +829,41 @@ cudaError_t select_as(const hg_beam& h, SelectArgs& a, cudaStream_t stream) {
   const long long all = rows * a.chunks;
   if (all > 0x3fffffffLL) return cudaErrorInvalidValue;  // more logits than any device holds
   const long long full = (long long)kCtasPerSm * h.sms;
-  // An item's parts, of its beams and CTAs, are joined by one CTA: where that would be
-  // too many entries, CTAs have whole rows.
-  const long long per_item = kMostEntries / h.picks - h.beams - 2;
-  long long ctas = per_item * a.c.items < full ? per_item * a.c.items : full;
-  if (ctas > all) ctas = all;
-  a.whole_rows = per_item < h.beams;
+  long long ctas = full < all ? full : all;
   a.all = (int)all;
+  a.each = (int)(all / ctas);
+  a.more = (int)(all % ctas);
+  // An item's parts at most: a CTA's share may end in its rows, and begin, anywhere.
+  long long parts = div_up((long long)h.beams * a.chunks, a.each) + 1 + h.beams;
+  a.whole_rows = parts > kMostValues / kLeastGroups;
   if (a.whole_rows) {
     a.each = (int)div_up(rows, full) * a.chunks;
+    a.more = 0;
     ctas = div_up(all, a.each);
-  } else {
-    a.each = (int)(all / ctas);
-    a.more = (int)(all % ctas);
+    parts = h.beams;
   }
-  const int longest = a.each + (a.more > 0) < a.chunks ? a.each + (a.more > 0) : a.chunks;
-  a.cell_chunks = (longest + kCells - 1) / kCells;
+  // As many groups of threads as there is room for values of their maxima.
+  a.log_groups = kLogThreads;
+  while (parts << a.log_groups > kMostValues) --a.log_groups;
+  a.longest = a.each + (a.more > 0) < a.chunks ? a.each + (a.more > 0) : a.chunks;
   a.by_chunks = Divisor(a.chunks);
   a.by_each = Divisor(a.each);
   a.by_each_and_one = Divisor(a.each + 1);
-  a.by_picks = Divisor(h.picks);
   a.by_beams = Divisor(h.beams);
-  // The ring, or the entries of an item (join_item).
-  const size_t held = (size_t)kStages * R * kThreads * 16;
-  const size_t joined = (size_t)(kMostEntries + HG_MAX_BEAMS) * sizeof(float);
-  const size_t smem = held > joined ? held : joined;
-  return launch_dependent(select_kernel<T, R>, a, (unsigned)ctas, kThreads, smem, 1, stream);
+  a.by_longest = Divisor(a.longest);
+  const cudaError_t e =
+      launch_dependent(select_kernel<T, R>, a, (unsigned)ctas, kThreads,
+                       (size_t)kStages * R * kThreads * 16, 1, stream);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(join_kernel<T, R>, a, (unsigned)a.c.items, kJoinThreads, 0, 1, stream);
 }
 
-// Chunks of 16 KB, or smaller ones where there would be few: the more parts, the more there
-// is to join.
+// Chunks of 16 KB, or smaller ones where there would be few.
 template <typename T>
 cudaError_t select_by(const hg_beam& h, SelectArgs& a, cudaStream_t stream) {
   const long long rows = (long long)a.c.items * h.beams;
   const long long bytes = rows * h.vocab * (long long)sizeof(T);
-  const long long few = 64ll * kThreads * 16;
+  const long long few = SELFEW * kThreads * 16;
   if (bytes >= 4 * few) return select_as<T, 4>(h, a, stream);
   return bytes >= 2 * few ? select_as<T, 2>(h, a, stream) : select_as<T, 1>(h, a, stream);
 }
@@ -894,7 +886,7 @@ cudaError_t select_prepare(const hg_beam& h) {
                               : prepare_as<float>();
 }
 
-long long list_slots(const hg_beam& h) {
+long long part_slots(const hg_beam& h) {
   return (long long)h.max_items * h.beams + (long long)kCtasPerSm * h.sms;
 }
 
@@ -906,8 +898,8 @@ cudaError_t select(const hg_beam& h, const SelectCall& c, cudaStream_t stream) {
   a.picks = h.picks;
   a.list = h.list;
   a.stats = h.stats;
+  a.maxima = h.maxima;
   a.beam_of = h.beam_of;
-  a.arrived = h.arrived;
   switch (h.dtype) {
     case HG_BF16:
       return select_by<__nv_bfloat16>(h, a, stream);
