@@ -28,6 +28,21 @@ namespace beam {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
+// Division of numbers below 2^31 by one that is known when the kernel is launched.
+struct Divisor {
+  uint32_t by = 1, factor = 0;
+  int shift = 0;
+  Divisor() = default;
+  explicit Divisor(uint32_t d) : by(d) {
+    while ((1ull << shift) < d) ++shift;
+    factor = (uint32_t)((1ull << (31 + shift)) / d + 1);
+    shift += 31;
+  }
+  __device__ int divide(int n) const {
+    return by == 1 ? n : (int)((unsigned long long)(uint32_t)n * factor >> shift);
+  }
+};
+
 struct SelectCall {
   int items = 0;
   const void* logits = nullptr;

@@ -12,15 +12,6 @@
 // the last CTA of the first kernel, an item takes 12 to 20 us of dependent steps for 256 threads.)
 
 #include <cmath>
-#ifndef SELFEW
-#define SELFEW 64ll
-#endif
-#ifndef NST
-#define NST 3
-#endif
-#ifndef NCT
-#define NCT 3
-#endif
 #include <cstring>
 
 #include "hg_beam.cuh"
@@ -39,34 +30,19 @@ typedef unsigned long long u64;
 
 constexpr int kLogThreads = 8;
 static_assert(1 << kLogThreads == kThreads, "groups of threads are counted in powers of two");
-constexpr int kStages = NST;       // chunks in the ring
-constexpr int kJoinThreads = 1024;
-constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kStages = 2;       // chunks in the ring
+constexpr int kMostJoinWarps = 32;
 constexpr int kList = 1024;      // candidates of an item that are ranked at once
 constexpr int kHits = 512;       // groups of threads whose elements are read again
-constexpr int kCtasPerSm = NCT;
-constexpr int kMostValues = 4096;  // maxima that are joined of an item
+constexpr int kCtasPerSm = 4;
+constexpr int kValues = 5;  // of a thread in join_kernel: groups, and a finished beam's
+constexpr int kMostValues = 1024 * (kValues - 1);  // maxima that are joined of an item
 constexpr int kLeastGroups = 8;    // of a part's threads, at least, that have a maximum: warps
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr double kLn2 = 0.693147180559945309417;
 constexpr double kLog2eOff = 1.0 - (double)kLog2e * kLn2;
 
 constexpr int kNone = 255;
-
-// Division of numbers below 2^31 by one that is known when the kernel is launched.
-struct Divisor {
-  uint32_t by = 1, factor = 0;
-  int shift = 0;
-  Divisor() = default;
-  explicit Divisor(uint32_t d) : by(d) {
-    while ((1ull << shift) < d) ++shift;
-    factor = (uint32_t)((1ull << (31 + shift)) / d + 1);
-    shift += 31;
-  }
-  __device__ int divide(int n) const {
-    return by == 1 ? n : (int)((unsigned long long)(uint32_t)n * factor >> shift);
-  }
-};
 
 struct SelectArgs {
   SelectCall c;
@@ -114,6 +90,23 @@ __device__ __forceinline__ float exp2_of(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ u64 pair(float lo, float hi) {
+  return (u64)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ float low(u64 p) { return __uint_as_float((uint32_t)p); }
+__device__ __forceinline__ float high(u64 p) { return __uint_as_float((uint32_t)(p >> 32)); }
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 // A row whose logits count.
@@ -214,13 +207,16 @@ __device__ __forceinline__ float largest(const Access<T> (&x)[R]) {
 }
 
 // Sum of 2^(log2e x - shift) by thread, shift = rint(log2e most): as it is whole, one rounding
-// is in each exponent, and rescaling as the maximum rises is exact. From kHuge on, where
-// neighbours are further apart than exponentials reach, the largest elements count one each.
-// NaN and +inf give NaN.
+// is in each exponent, and rescaling is exact. `most` need not be the maximum: it follows
+// where that is kRise above it (to rescale at every new maximum took a third of the
+// instructions). From kHuge on, where neighbours are further apart than exponentials reach, the
+// largest elements count one each. NaN and +inf give NaN.
 constexpr float kHuge = 1e30f;
+constexpr float kRise = 40.f;  // 2^58
 
 struct Exponentials {
   float most = -INFINITY, sum = 0.f;
+  float limit = -INFINITY;  // up to which logits are added as they are
 
   static __device__ __forceinline__ bool plain(float most) {
     return fabsf(most) < kHuge || most == -INFINITY;
@@ -251,19 +247,29 @@ struct Exponentials {
   template <typename T, int R>
   __device__ __forceinline__ void add(const Access<T> (&x)[R], const uint4* ring,
                                       float chunk_most) {
-    raise(chunk_most);
+    if (!(chunk_most <= limit)) {
+      raise(chunk_most);
+      limit = plain(most) ? most + kRise : most;
+    }
     if (!plain(most)) {
       sum += count_huge<T>(ring, R, most);
       return;
     }
     const float s = shift(most);
+    const u64 scale = pair(kLog2e, kLog2e), back = pair(-s, -s);
+    u64 sums[2] = {pair(sum, 0.f), 0};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float v[Access<T>::E];
       x[r].widen(v);
 #pragma unroll
-      for (int e = 0; e < Access<T>::E; ++e) sum += exp2_of(fmaf(v[e], kLog2e, -s));
+      for (int e = 0; e < Access<T>::E; e += 2) {
+        const u64 p = fma2(pair(v[e], v[e + 1]), scale, back);
+        sums[e / 2 % 2] = add2(sums[e / 2 % 2], pair(exp2_of(low(p)), exp2_of(high(p))));
+      }
     }
+    const u64 both = add2(sums[0], sums[1]);
+    sum = low(both) + high(both);
   }
   __device__ __forceinline__ void join(float other_most, float other_sum) {
     raise(other_most);
@@ -287,27 +293,23 @@ __device__ __forceinline__ uint32_t bin_end(int bin) {
 
 struct BoundShared {
   int bins[kBins];
-  uint32_t top[kJoinWarps];
+  uint32_t top[kMostJoinWarps];
 };
 
-// A value that at least n of the words (ordered values, K a thread; 0: none) are not under, and
+// A value that at least n of the threads' words (ordered values; 0: none) are not under, and
 // not many more: the end of the bin that the n-th largest is in. The least finite value if
 // there are not n.
-template <int K>
-__device__ __forceinline__ float bound_of_best(int n, const uint32_t (&word)[K], BoundShared& s) {
+template <int WARPS>
+__device__ __forceinline__ float bound_of_best(int n, uint32_t word, BoundShared& s) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  uint32_t top = 0;
-#pragma unroll
-  for (int k = 0; k < K; ++k) top = max(top, word[k]);
+  uint32_t top = word;
   top = __reduce_max_sync(kAll, top);
   if (lane == 0) s.top[threadIdx.x >> 5] = top;
   if (threadIdx.x < kBins) s.bins[threadIdx.x] = 0;
   __syncthreads();
-  top = __reduce_max_sync(kAll, s.top[lane]);
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-    if (word[k]) atomicAdd(&s.bins[bin_of(top - word[k])], 1);
+  top = __reduce_max_sync(kAll, s.top[lane % WARPS]);
+  if (word) atomicAdd(&s.bins[bin_of(top - word)], 1);
   __syncthreads();
   // The first bin up to which there are enough; each warp for itself, eight bins a lane.
   int upto[8];
@@ -396,10 +398,10 @@ struct JoinShared {
   bool done[HG_MAX_BEAMS];   // finished, and still a candidate
   float largest[2];          // magnitude of near, below kHuge, of 32 beams each
   bool reaches[HG_MAX_BEAMS];  // the bound, by a logit
-  int warp_count[2][kJoinWarps];
-  double top_total[kJoinWarps];
-  u64 top_key[kJoinWarps];
-  int top_beam[kJoinWarps];
+  int warp_count[2][kMostJoinWarps];
+  double top_total[kMostJoinWarps];
+  u64 top_key[kMostJoinWarps];
+  int top_beam[kMostJoinWarps];
   int hits, count;
 
   // The total of a beam's logit, as it is compared.
@@ -410,8 +412,10 @@ struct JoinShared {
   // come near the best).
   __device__ __forceinline__ float nearly(int b, float x) const {
     const float t = x + near[b];
-    return fabsf(near[b]) < kHuge && fabsf(t) < kHuge ? t : (float)sum(b, x);
+    return fabsf(near[b]) < kHuge && fabsf(t) < kHuge ? t : exactly(b, x);
   }
+  // Not inlined: it would be computed for every value, to be thrown away (8000 cycles an item).
+  __device__ __noinline__ float exactly(int b, float x) const { return (float)sum(b, x); }
   // Three roundings of at most half a unit in the last place of the two terms and of the sum.
   __device__ __forceinline__ float off(float t) const {
     const float most = fmaxf(largest[0], largest[1]);
@@ -487,25 +491,26 @@ __device__ __forceinline__ double row_lse(const SelectArgs& a, int part0, int pa
                      : -INFINITY;
 }
 
+template <int WARPS>
 __device__ __forceinline__ int count_all(int c, int turn, JoinShared& s) {
   c = __reduce_add_sync(0xffffffffu, c);
   if ((threadIdx.x & 31) == 0) s.warp_count[turn][threadIdx.x >> 5] = c;
   __syncthreads();
-  return __reduce_add_sync(0xffffffffu, s.warp_count[turn][threadIdx.x & 31]);
+  return __reduce_add_sync(0xffffffffu, (threadIdx.x & 31) < WARPS ? s.warp_count[turn][threadIdx.x & 31] : 0);
 }
 
 // Where too many candidates are alike for the list: the best of each row that has some,
 // exactly (the key of the n-th best, one bit after another, reading the row again for each),
 // and of those one pick after another.
-template <typename T, int R>
+template <typename T, int R, int THREADS>
 __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinShared& s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int thread = threadIdx.x % kThreads, first = threadIdx.x / kThreads;
-  constexpr int kStep = kJoinThreads / kThreads;
+  constexpr int kStep = THREADS / kThreads;
   const int row0 = item * a.beams, n = a.picks;
   for (int b = 0; b < a.beams; ++b) {
     u64* list = a.list + (size_t)(row0 + b) * n;
-    for (int i = threadIdx.x; i < n; i += kJoinThreads) list[i] = 0;
+    for (int i = threadIdx.x; i < n; i += THREADS) list[i] = 0;
     if (!s.reaches[b]) continue;
     const Part<T, R> part = {static_cast<const T*>(a.c.logits) + (size_t)(row0 + b) * a.c.ld, 0,
                              a.chunks, a.vocab};
@@ -521,7 +526,7 @@ __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinSha
       int c = 0;
       for (int i = first; i < part.chunks; i += kStep)
         part.each(thread, i, kLeast, [&](float x, int token) { c += key_of(x, token) >= next; });
-      c = count_all(c, bit & 1, s);
+      c = count_all<THREADS / 32>(c, bit & 1, s);
       if (c >= n) bound = next;
       if (c == n) break;
     }
@@ -541,7 +546,7 @@ __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinSha
   for (int i = 0; i < n; ++i) {
     Candidate top;
     top.beam = -1;
-    for (int j = threadIdx.x; j < all; j += kJoinThreads) {
+    for (int j = threadIdx.x; j < all; j += THREADS) {
       Candidate t;
       if (j < listed) {
         t.beam = j / n;
@@ -572,7 +577,7 @@ __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinSha
       s.top_key[warp] = top.key;
     }
     __syncthreads();
-    for (int w = 0; w < kJoinWarps; ++w) {
+    for (int w = 0; w < (THREADS / 32); ++w) {
       const Candidate o = {s.top_total[w], s.top_beam[w], s.top_key[w]};
       if (o.before(top)) top = o;
     }
@@ -581,13 +586,9 @@ __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinSha
   }
 }
 
-constexpr int kValues = kMostValues / kJoinThreads + 1;  // of a thread: groups, a finished beam
-
-template <typename T, int R>
-__global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const __grid_constant__ SelectArgs a) {
+template <typename T, int R, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant__ SelectArgs a) {
   __shared__ JoinShared s;
-  wait_for_predecessor();
-  let_successor_start();
   const SelectCall& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int item = blockIdx.x, row0 = item * a.beams, row_last = row0 + a.beams - 1;
@@ -596,11 +597,13 @@ __global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const __grid_cons
   // The groups' maxima; the last value of a thread is a finished beam's score.
   const int listed = parts << a.log_groups;
   const float* maxima = a.maxima + ((size_t)part0 << a.log_groups);
+  wait_for_predecessor();
+  let_successor_start();
   float value[kValues];
   int beam[kValues];
 #pragma unroll
   for (int k = 0; k < kValues - 1; ++k) {
-    const int i = min((int)threadIdx.x + k * kJoinThreads, listed - 1);
+    const int i = min((int)threadIdx.x + k * THREADS, listed - 1);
     value[k] = __ldcg(maxima + i);
     beam[k] = __ldcg(a.beam_of + part0 + (i >> a.log_groups));
   }
@@ -622,7 +625,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const __grid_cons
   if (threadIdx.x == 0) s.hits = s.count = 0;
   if (!c.lse) {
     __syncthreads();
-    for (int b = warp; b < a.beams; b += kJoinWarps) {
+    for (int b = warp; b < a.beams; b += (THREADS / 32)) {
       const int row = row0 + b, first = a.part_of(a.cta_of(row * a.chunks), row);
       if (!searched(c, row)) continue;
       const double lse =
@@ -643,18 +646,18 @@ __global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const __grid_cons
   __syncthreads();
 
   // The groups' best totals, nearly, and their words from below.
-  uint32_t word[kValues];
+  uint32_t word = 0;
 #pragma unroll
   for (int k = 0; k < kValues; ++k) {
     float t = value[k];
     if (k < kValues - 1) {
-      const bool there = (int)threadIdx.x + k * kJoinThreads < listed && beam[k] != kNone;
+      const bool there = (int)threadIdx.x + k * THREADS < listed && beam[k] != kNone;
       t = there && t > -INFINITY ? s.nearly(beam[k], t) : -INFINITY;
     }
     value[k] = t;
-    word[k] = t > -INFINITY ? ordered(t - s.off(t)) : 0;
+    if (t > -INFINITY) word = max(word, ordered(t - s.off(t)));
   }
-  const float from = bound_of_best(a.picks, word, s.bound);
+  const float from = bound_of_best<THREADS / 32>(a.picks, word, s.bound);
 #pragma unroll
   for (int k = 0; k < kValues; ++k) {
     if (!(value[k] + s.off(value[k]) >= from)) continue;
@@ -665,7 +668,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const __grid_cons
     s.reaches[beam[k]] = true;
     const int at = atomicAdd(&s.hits, 1);
     if (at >= kHits) continue;
-    const int i = threadIdx.x + k * kJoinThreads;
+    const int i = threadIdx.x + k * THREADS;
     const int part = i >> a.log_groups, group = i - (part << a.log_groups);
     const int row = row0 + beam[k], begin = row * a.chunks, end = begin + a.chunks;
     int first = begin, last = end;
@@ -681,7 +684,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const __grid_cons
     // The groups' elements, a thread's of a chunk each.
     const int log_width = kLogThreads - a.log_groups;
     const int units = (hits * a.longest) << log_width;
-    for (int u = threadIdx.x; u < units; u += kJoinThreads) {
+    for (int u = threadIdx.x; u < units; u += THREADS) {
       const int pair = u >> log_width, h = a.by_longest.divide(pair);
       const Hit hit = s.hit[h];
       const int chunk = pair - h * a.longest, b = hit.row - row0;
@@ -702,12 +705,12 @@ __global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const __grid_cons
   __syncthreads();
   const int found = s.count;
   if (hits > kHits || found > kList) {
-    pick_exactly<T, R>(a, item, s);
+    pick_exactly<T, R, THREADS>(a, item, s);
     return;
   }
   // Each candidate's rank; eight lanes count what comes before it.
   const int eighth = threadIdx.x % 8;
-  for (int i0 = 0; i0 < found; i0 += kJoinThreads / 8) {
+  for (int i0 = 0; i0 < found; i0 += THREADS / 8) {
     const int i = i0 + threadIdx.x / 8;
     const bool there = i < found;
     const u64 total = there ? s.total[i] : ~0ull, key = there ? s.key[i] : ~0ull;
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const __grid_cons
       put_pick(a, item, rank, true, d, b, key);
     }
   }
-  for (int i = found + threadIdx.x; i < a.picks; i += kJoinThreads)
+  for (int i = found + threadIdx.x; i < a.picks; i += THREADS)
     put_pick(a, item, i, false, 0.0, -1, 0);
 }
 
@@ -802,6 +805,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (threadIdx.x == 0) a.beam_of[part] = on ? row - a.by_beams.divide(row) * a.beams : kNone;
     if (on) {
       if (!a.c.lse) {
+        sums.raise(best);
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1)
           sums.join(__shfl_xor_sync(0xffffffffu, sums.most, m),
@@ -842,9 +846,11 @@ cudaError_t select_as(const hg_beam& h, SelectArgs& a, cudaStream_t stream) {
     ctas = div_up(all, a.each);
     parts = h.beams;
   }
-  // As many groups of threads as there is room for values of their maxima.
+  // As many groups of threads as there is room for values of their maxima; less where that
+  // lets small CTAs join, which more items than SMs need (256 items: 29 and 23 us).
+  const int joiners = a.c.items > h.sms && parts * kLeastGroups <= 256 * (kValues - 1) ? 256 : 1024;
   a.log_groups = kLogThreads;
-  while (parts << a.log_groups > kMostValues) --a.log_groups;
+  while (parts << a.log_groups > joiners * (kValues - 1)) --a.log_groups;
   a.longest = a.each + (a.more > 0) < a.chunks ? a.each + (a.more > 0) : a.chunks;
   a.by_chunks = Divisor(a.chunks);
   a.by_each = Divisor(a.each);
@@ -855,7 +861,10 @@ cudaError_t select_as(const hg_beam& h, SelectArgs& a, cudaStream_t stream) {
       launch_dependent(select_kernel<T, R>, a, (unsigned)ctas, kThreads,
                        (size_t)kStages * R * kThreads * 16, 1, stream);
   if (e != cudaSuccess) return e;
-  return launch_dependent(join_kernel<T, R>, a, (unsigned)a.c.items, kJoinThreads, 0, 1, stream);
+  return parts << a.log_groups <= 256 * (kValues - 1)
+             ? launch_dependent(join_kernel<T, R, 256>, a, (unsigned)a.c.items, 256, 0, 1, stream)
+             : launch_dependent(join_kernel<T, R, 1024>, a, (unsigned)a.c.items, 1024, 0, 1,
+                                stream);
 }
 
 // Chunks of 16 KB, or smaller ones where there would be few.
@@ -863,7 +872,7 @@ template <typename T>
 cudaError_t select_by(const hg_beam& h, SelectArgs& a, cudaStream_t stream) {
   const long long rows = (long long)a.c.items * h.beams;
   const long long bytes = rows * h.vocab * (long long)sizeof(T);
-  const long long few = SELFEW * kThreads * 16;
+  const long long few = 64ll * kThreads * 16;
   if (bytes >= 4 * few) return select_as<T, 4>(h, a, stream);
   return bytes >= 2 * few ? select_as<T, 2>(h, a, stream) : select_as<T, 1>(h, a, stream);
 }
