@@ -619,12 +619,13 @@ int hg_vocab_loss_grad(hg_vocab *h, const void *hidden, size_t ld_hidden,
  * rows, those that the gradient is given. Squares and sums that pass the fp32
  * range give rows of zeros or NaN.
  *
- * Conventions as for the vocabulary operators: asynchronous, no allocation, no wait for the
- * device, capturable; the calls of one handle share its workspace (the gradient's
- * only: calls of hg_norm_rows may overlap); the handle's device is current at every
- * call and its the stream and pointers are; the same inputs give the same bits. Where
- * all pointers and row distances are 16-byte (or 4-byte) aligned, rows move in
- * such words.
+ * Conventions as for the vocabulary operators (asynchronous, no allocation, no wait for the
+ * device, capturable, the handle's device current at every call and the stream and pointers
+ * of that device, the same inputs give the same bits). The gradients of one handle share
+ * its workspace: they, and graphs that hold them, run one after another. Calls of hg_norm_rows
+ * need none and may overlap. No output overlaps an input or another output, but where that
+ * is allowed below. Where all pointers and row distances are 16-byte (or 4-byte) aligned,
+ * rows move in such words.
  */
 typedef struct hg_norm hg_norm;
 
@@ -712,8 +713,9 @@ int hg_norm_rows_grad(hg_norm *h, const void *s, size_t ld_s, const void *gain, 
  * but one beam of an item at the first step, whose rows are the same).
  *
  * Conventions as for the vocabulary operators (asynchronous, no allocation, no
- * wait, capturable, one device, same bits); calls of hg_beam_select of one handle share its workspace,
- * hg_beam_reorder needs none.
+ * wait, capturable, one device, same bits). Calls of hg_beam_select of one handle share
+ * its workspace: they, and graphs that hold them, run one after another. hg_beam_reorder
+ * needs none: its calls may overlap, on other states.
  */
 typedef struct hg_beam hg_beam;
 
@@ -760,7 +762,9 @@ size_t hg_beam_workspace_bytes(const hg_beam *h);
  * With picks = beams, picked, picked_finished and parents are the next step's
  * scores, finished and reordering (tokens, hg_vocab_embed's input); with picks = 2 * beams
  * there are beams of them that do not end. Where fewer candidates are left, the last
- * picks have token and parent -1, total -inf and are not finished. No output may overlap an input.
+ * picks have token and parent -1, total -inf and are not finished. No output overlaps an
+ * input or another output. An item with more than 1000 equal candidates at the last pick
+ * (a row of zeros, say) takes a path that reads its rows again for every bit of the order.
  *
  * Errors, before any device work: HG_ERR_ARG, HG_ERR_ROWS (items above max_items),
  * HG_ERR_CUDA.
@@ -787,7 +791,8 @@ typedef struct hg_beam_state {
  *   parents   items * beams signed integers of id_bytes (4 or 8) bytes: parents[item *
  *             beams + j] is a beam of the same item. One outside [0, beams)
  *             leaves its row as it is
- *   states    n_states records; the rows of a state and the states do not overlap
+ *   states    n_states records; the rows of a state and the states do not overlap (a state
+ *             listed twice is refused)
  *
  * All rows of an item take their parents' contents as they were before the call. Only
  * rows that change are written. Errors, before any device work: HG_ERR_ARG (also:

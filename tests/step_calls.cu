@@ -79,7 +79,7 @@ int main() {
                     size_t stride, const uint8_t* finished, int end, int items, void* tokens,
                     int id_bytes) {
     show(what, hg_beam_select(h, logits, ld, lse, stride, f, finished, end, items, tokens, d,
-                              id_bytes, f, nullptr, nullptr));
+                              id_bytes, f + 16, nullptr, nullptr));
   };
   auto reorder = [&](const char* what, hg_beam_state s) {
     show(what, hg_beam_reorder(h, d, 8, 2, &s, 1, nullptr));
@@ -103,6 +103,15 @@ int main() {
   select("no tokens", a, 50, nullptr, 0, nullptr, -1, 2, nullptr, 8);
   select("ids of 2 bytes", a, 50, nullptr, 0, nullptr, -1, 2, c, 2);
   select("ids not aligned", a, 50, nullptr, 0, nullptr, -1, 2, c + 4, 8);
+  auto overlap = [&](const char* what, void* tokens, void* parents, float* picked, uint8_t* done) {
+    show(what, hg_beam_select(h, a, 50, nullptr, 0, f, b + 40, 3, 2, tokens, parents, 8, picked,
+                              done, nullptr));
+  };
+  overlap("totals over scores", c, d, f, nullptr);
+  overlap("totals over the last score", c, d, f + 5, nullptr);
+  overlap("flags over flags", c, d, f + 24, b + 45);
+  overlap("tokens over parents", c + 8, c, f + 12, nullptr);
+  overlap("parents over totals", c, d, reinterpret_cast<float*>(d + 60), nullptr);
   reorder("no data", {nullptr, 1, 0, 8, 1, 0, 8});
   reorder("rows overlap", {a, 1, 0, 7, 1, 0, 8});
   reorder("pieces overlap", {a, 1, 0, 64, 4, 4, 8});
@@ -110,6 +119,8 @@ int main() {
   reorder("outer over rows", {a, 2, 47, 8, 1, 0, 8});
   reorder("bytes beyond 64 bits", {a, 1, 0, (size_t)1 << 61, 1, 0, (size_t)1 << 61});
   reorder("steps beyond 64 bits", {a, (size_t)1 << 40, (size_t)1 << 40, 8, 1, 0, 8});
+  const hg_beam_state twice[3] = {{a, 1, 0, 8, 1, 0, 8}, {b, 1, 0, 8, 1, 0, 8}, {a, 1, 0, 8, 1, 0, 8}};
+  show("a state twice", hg_beam_reorder(h, d, 8, 2, twice, 3, nullptr));
   show("states missing", hg_beam_reorder(h, d, 8, 2, nullptr, 1, nullptr));
   show("too many states", hg_beam_reorder(h, d, 8, 2, nullptr, HG_MAX_STATES + 1, nullptr));
   show("no parents", hg_beam_reorder(h, nullptr, 8, 2, nullptr, 0, nullptr));
@@ -235,17 +246,18 @@ int main() {
   grad("over s", {.x = a});
   grad("in place, other distance", {.x = b, .ld_x = 24});
   grad("odd grad_gain", {.gain_out = d + 1});
+  grad("over the gain", {.gain_out = d});
   std::printf("too many rows\n");
   rows("rows", {.N = 3});
   grad("grad", {.N = 3});
   std::printf("served\n");
   rows("no rows", {.x = nullptr, .N = 0, .out = nullptr});
   grad("no rows", {.s = nullptr, .rstd = nullptr, .up = nullptr, .N = 0, .x = nullptr,
-                   .gain_out = d});
+                   .gain_out = d + 512});
   rows("in place", {.res = c, .ld_res = 16, .sum = c, .ld_sum = 16, .out = a});
   rows("one row, other distance", {.N = 1, .out = a, .ld_out = 24});
   rows("8 bits", {.type = HG_E4M3, .scales = f, .block = 128});
-  grad("in place", {.more = c, .ld_more = 16, .gain_out = d});
+  grad("in place", {.more = c, .ld_more = 16, .gain_out = d + 512});
   std::printf("end\n");
   fakeSetDevice(0);
   show("destroy", hg_norm_destroy(h));

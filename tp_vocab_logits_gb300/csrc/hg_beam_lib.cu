@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <functional>
 #include <new>
 
 #include "hg_beam.cuh"
@@ -47,6 +48,31 @@ bool state_ok(const hg_beam_state& s, size_t rows) {
     if (span > kMost) return false;
   }
   return true;
+}
+
+// Arrays that the kernels write, the first `outs`, overlap neither each other nor the rest.
+struct Array {
+  const void* p;
+  size_t bytes;
+};
+template <int N>
+bool apart(const Array (&a)[N], int outs) {
+  for (int i = 0; i < outs; ++i)
+    for (int j = i + 1; j < N; ++j) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(a[i].p), y = reinterpret_cast<uintptr_t>(a[j].p);
+      if (a[i].p && a[j].p && x < y + a[j].bytes && y < x + a[i].bytes) return false;
+    }
+  return true;
+}
+
+// No state is listed twice: both would be moved at once.
+bool states_differ(const hg_beam_state* states, int n) {
+  const void* data[HG_MAX_STATES];
+  int some = 0;
+  for (int i = 0; i < n; ++i)
+    if (states[i].outer && states[i].pieces && states[i].piece_bytes) data[some++] = states[i].data;
+  std::sort(data, data + some, std::less<const void*>());
+  return std::adjacent_find(data, data + some) == data + some;
 }
 
 }  // namespace
@@ -128,6 +154,10 @@ int hg_beam_select(hg_beam* h, const void* logits, size_t ld_logits, const float
         !aligned(scores, 4) || !ids_ok(tokens, id_bytes) || !ids_ok(parents, id_bytes) || !picked ||
         !aligned(picked, 4))
       return HG_ERR_ARG;
+    const size_t picks = (size_t)items * h->picks;
+    if (!apart<6>({{tokens, picks * id_bytes}, {parents, picks * id_bytes}, {picked, picks * 4},
+                {picked_finished, picks}, {scores, rows * 4}, {finished, rows}}, 4))
+      return HG_ERR_ARG;
   }
   if (items > h->max_items) return HG_ERR_ROWS;
   const int st = check_device(h);
@@ -155,9 +185,11 @@ int hg_beam_reorder(hg_beam* h, const void* parents, int id_bytes, int items,
     return HG_ERR_ARG;
   if (items > 0 && !ids_ok(parents, id_bytes)) return HG_ERR_ARG;
   if (items > h->max_items) return HG_ERR_ROWS;
-  if (items > 0)
+  if (items > 0) {
     for (int i = 0; i < n_states; ++i)
       if (!state_ok(states[i], (size_t)items * h->beams)) return HG_ERR_ARG;
+    if (!states_differ(states, n_states)) return HG_ERR_ARG;
+  }
   const int st = check_device(h);
   if (st != HG_OK || items == 0 || n_states == 0) return st;
   return as_status(hg::beam::reorder(*h, parents, id_bytes, items, states, n_states, stream));

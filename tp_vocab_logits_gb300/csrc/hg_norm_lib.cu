@@ -139,7 +139,7 @@ int hg_norm_rows_grad(hg_norm* h, const void* s, size_t ld_s, const void* gain, 
   if (!matrix_ok(h, s, ld_s, e, N) || !matrix_ok(h, grad_out, ld_grad_out, e, N) ||
       (grad_sum && !matrix_ok(h, grad_sum, ld_grad_sum, e, N)) ||
       (grad_x && !matrix_ok(h, grad_x, ld_grad_x, e, N)) || !gain || !aligned(gain, e) ||
-      (N > 0 && (!rstd || !aligned(rstd, 4))) || !aligned(grad_gain, e))
+      (N > 0 && (!rstd || !aligned(rstd, 4))) || !aligned(grad_gain, e) || grad_gain == gain)
     return HG_ERR_ARG;
   if (N > 0 && grad_x &&
       (grad_x == s || !in_place_ok(grad_x, ld_grad_x, grad_out, ld_grad_out, N) ||
