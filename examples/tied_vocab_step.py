@@ -6,8 +6,9 @@ The [V, K] matrix lies in TP shards, as hg_gather_fused takes it, and is both
 the embedding and the LM head. Between them stands one residual layer, in plain
 torch. A step runs the four vocabulary operators as a trainer would: the lookup,
 the loss (a mean over the unmasked targets), its gradient written to the
-gradient shards, and the lookup's gradient added to the same shards. Prints the
-loss of every step.
+gradient shards, and the lookup's gradient added to the same shards. With --norm
+the residual's addition is the norm's before the head, and its gradient the one of
+both of its terms. Prints the loss of every step.
 """
 
 from __future__ import annotations
@@ -33,7 +34,7 @@ def batch(vocab: int, rows: int, masked: float, gen: torch.Generator):
 
 
 def train(steps=30, vocab=8192, hidden=512, rows=2048, tp=4, masked=0.1, lr=0.03,
-          seed=0, log=print) -> list:
+          seed=0, log=print, norm=False) -> list:
     cols = -(-vocab // tp)
     gen = torch.Generator(device="cuda").manual_seed(seed)
     dtype = torch.bfloat16
@@ -44,6 +45,8 @@ def train(steps=30, vocab=8192, hidden=512, rows=2048, tp=4, masked=0.1, lr=0.03
     # fp32 masters, their bf16 copies and gradients; the shards are views.
     master = {"matrix": normal((tp * cols, hidden), 0.02),
               "layer": normal((hidden, hidden), 1.0 / math.sqrt(hidden))}
+    if norm:
+        master["gain"] = torch.ones(hidden, device="cuda")
     weight = {k: v.to(dtype) for k, v in master.items()}
     grad = {k: torch.empty_like(v) for k, v in weight.items()}
     shards, grad_shards = (list(t["matrix"].split(cols)) for t in (weight, grad))
@@ -53,6 +56,9 @@ def train(steps=30, vocab=8192, hidden=512, rows=2048, tp=4, masked=0.1, lr=0.03
     x = torch.empty((rows, hidden), device="cuda", dtype=dtype)
     y, dy, dx = (torch.empty_like(x) for _ in range(3))
     loss, lse = (torch.empty(rows, device="cuda") for _ in range(2))
+    if norm:
+        hn = hg.hg_norm_create(hidden, rows, dtype=dtype)
+        s, rstd = torch.empty_like(x), torch.empty_like(loss)
     scale = math.sqrt(hidden)
     data = [batch(vocab, rows, masked, gen) for _ in range(4)]
     losses = []
@@ -61,13 +67,18 @@ def train(steps=30, vocab=8192, hidden=512, rows=2048, tp=4, masked=0.1, lr=0.03
         # Forward: embedding, a residual layer, the loss.
         hg.hg_vocab_embed(h, tokens, shards, x, scale=scale)
         a = torch.tanh(x @ weight["layer"])
-        torch.add(x, a, out=y)
+        if norm:
+            hg.hg_norm_rows(hn, a, weight["gain"], y, residual=x, sum_out=s, rstd=rstd)
+        else:
+            torch.add(x, a, out=y)
         hg.hg_vocab_loss(h, y, shards, targets, loss, lse)
         count = (targets >= 0).sum().clamp(min=1)
         mean = loss.sum() / count
         # Backward: the head's gradient is written, the embedding's added to it.
         up = torch.where(targets >= 0, 1.0 / count, 0.0)
         hg.hg_vocab_loss_grad(h, y, shards, targets, lse, up, dy, grad_shards)
+        if norm:
+            hg.hg_norm_rows_grad(hn, s, weight["gain"], rstd, dy, dy, grad["gain"])
         da = dy * (1 - a * a)
         torch.matmul(x.t(), da, out=grad["layer"])
         torch.add(dy, da @ weight["layer"].t(), out=dx)
@@ -86,6 +97,8 @@ def train(steps=30, vocab=8192, hidden=512, rows=2048, tp=4, masked=0.1, lr=0.03
             log(f"step {step:3d}  loss {losses[-1]:.4f}")
     hg.hg_vocab_sync(h)
     h.close()
+    if norm:
+        hn.close()
     return losses
 
 
@@ -96,6 +109,7 @@ def main() -> None:
         ap.add_argument(f"--{name}", type=int, default=value)
     ap.add_argument("--masked", type=float, default=0.1)
     ap.add_argument("--lr", type=float, default=0.03)
+    ap.add_argument("--norm", action="store_true")
     train(**vars(ap.parse_args()))
 
 
