@@ -134,18 +134,26 @@ struct Access {
   static constexpr int E = 16 / sizeof(T);
   uint4 w;
 
-  // Copies elements [e0, e0 + E) of a row of `vocab` ahead, some of which may lie outside:
-  // those are -inf, and are not read.
-  static __device__ __forceinline__ void copy_edge(uint4* to, const T* row, int e0, int vocab) {
-    if (e0 >= 0 && e0 + E <= vocab) {
-      copy_ahead(to, row + e0);
-      return;
-    }
+  // Elements [e0, e0 + E) of a row of `vocab`; those that lie outside are -inf, and are not
+  // read (others are in their place, so that no load waits for a branch).
+  static __device__ __forceinline__ Access edge(const T* row, int e0, int vocab) {
     T v[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      v[e] = e0 + e >= 0 && e0 + e < vocab ? row[e0 + e] : Elem<T>::down(-INFINITY);
-    memcpy(to, v, 16);
+    for (int e = 0; e < E; ++e) v[e] = Elem<T>::down(-INFINITY);
+    if (e0 + E > 0 && e0 < vocab) {
+      T x[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = row[min(max(e0 + e, 0), vocab - 1)];
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e0 + e >= 0 && e0 + e < vocab) v[e] = x[e];
+    }
+    Access a;
+    memcpy(&a.w, v, 16);
+    return a;
+  }
+  static __device__ __forceinline__ bool inside(int e0, int vocab) {
+    return e0 >= 0 && e0 + E <= vocab;
   }
   __device__ void widen(float (&v)[E]) const {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -279,58 +287,43 @@ struct Exponentials {
 
 constexpr float kLeast = -3.402823466e38f;
 
-// A bin for every eighth of an octave of the distance from the best.
-constexpr int kBins = 240;
-__device__ __forceinline__ int bin_of(uint32_t d) {
-  if (d < 8) return (int)d;
-  const int e = 31 - __clz(d);
-  return (e - 2) * 8 + (int)((d >> (e - 3)) & 7);
-}
-__device__ __forceinline__ uint32_t bin_end(int bin) {
-  if (bin < 8) return (uint32_t)bin;
-  return ((uint32_t)(8 + bin % 8 + 1) << (bin / 8 - 1)) - 1;
-}
+constexpr int kLogGroupings = 5;  // at least 32 groups of a CTA's threads
 
 struct BoundShared {
-  int bins[kBins];
-  uint32_t top[kMostJoinWarps];
+  uint32_t word[kMostJoinWarps][33];
+  uint32_t top[2 * HG_MAX_PICKS];
+  uint32_t bound;
 };
 
 // A value that at least n of the threads' words (ordered values; 0: none) are not under, and
-// not many more: the end of the bin that the n-th largest is in. The least finite value if
-// there are not n.
+// not many more: the n-th largest of the maxima of groups of threads, twice n of them (which
+// 1.4 n words reach where they are in any order). A group takes one thread from each of some
+// warps, another lane of every one, as neighbours, and threads a part apart, have alike values.
+// The least finite value if there are not n.
 template <int WARPS>
 __device__ __forceinline__ float bound_of_best(int n, uint32_t word, BoundShared& s) {
   constexpr unsigned kAll = 0xffffffffu;
-  const int lane = threadIdx.x & 31;
-  uint32_t top = word;
-  top = __reduce_max_sync(kAll, top);
-  if (lane == 0) s.top[threadIdx.x >> 5] = top;
-  if (threadIdx.x < kBins) s.bins[threadIdx.x] = 0;
+  constexpr int kThreadsHere = WARPS * 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int log_groups = max(kLogGroupings, 32 - __clz(2 * n - 1));
+  static_assert(2 * HG_MAX_PICKS <= 256, "no more groups than threads");
+  s.word[warp][(lane + warp * 5 + warp / 8) & 31] = word;
   __syncthreads();
-  top = __reduce_max_sync(kAll, s.top[lane % WARPS]);
-  if (word) atomicAdd(&s.bins[bin_of(top - word)], 1);
+  uint32_t top = s.word[tid % WARPS][tid / WARPS];
+  const int width = kThreadsHere >> log_groups;  // threads of a group
+  for (int m = 1; m < width; m <<= 1) top = max(top, __shfl_xor_sync(kAll, top, m));
+  const int group = tid / width, turn = tid % width;
+  if (turn == 0) s.top[group] = top;
   __syncthreads();
-  // The first bin up to which there are enough; each warp for itself, eight bins a lane.
-  int upto[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    upto[i] = (lane * 8 + i < kBins ? s.bins[lane * 8 + i] : 0) + (i ? upto[i - 1] : 0);
-  int before = upto[7];
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const int other = __shfl_up_sync(kAll, before, m);
-    if (lane >= m) before += other;
+  int rank = 0;
+  for (int i = turn; i < 1 << log_groups; i += width) {
+    const uint32_t other = s.top[i];
+    rank += other > top || (other == top && i < group);
   }
-  const unsigned reach = __ballot_sync(kAll, before >= n);
-  before -= upto[7];
-  int bin = lane * 8;
-#pragma unroll
-  for (int i = 0; i < 7; ++i) bin += before + upto[i] < n;
-  if (!reach) return kLeast;
-  const uint32_t far = bin_end(__shfl_sync(kAll, bin, __ffs(reach) - 1));
-  const uint32_t w = far < top ? top - far : 0;
-  return w < ordered(kLeast) ? kLeast : unordered(w);
+  for (int m = 1; m < width; m <<= 1) rank += __shfl_xor_sync(kAll, rank, m);
+  if (turn == 0 && rank == n - 1) s.bound = top;
+  __syncthreads();
+  return s.bound < ordered(kLeast) ? kLeast : unordered(s.bound);
 }
 
 // ---- one CTA's part of a row -------------------------------------------------------
@@ -349,29 +342,25 @@ struct Part {
   __device__ __forceinline__ int element(int thread, int i, int k) const {
     return (((first + i) * R + k) * kThreads + thread) * E - shift();
   }
-  // Calls f(logit, token) for the elements of a thread from `least` on, in chunk i.
+  // Calls f(logit, token) for the elements of a thread from `least` (above -inf) on, in chunk i.
   template <typename F>
   __device__ __forceinline__ void each(int thread, int i, float least, F f) const {
     uint32_t mask = 0;
-    const int e0 = element(0, i, 0);
-    if (e0 >= 0 && e0 + kThreads * R * E <= vocab) {
-      Access<T> x[R];  // all loads before the first use
+    Access<T> x[R];  // all loads before the first use
 #pragma unroll
-      for (int k = 0; k < R; ++k)
-        x[k].w = *reinterpret_cast<const uint4*>(row + element(thread, i, k));
+    for (int k = 0; k < R; ++k) {
+      const int e0 = element(thread, i, k);
+      if (Access<T>::inside(e0, vocab))
+        x[k].w = *reinterpret_cast<const uint4*>(row + e0);
+      else
+        x[k] = Access<T>::edge(row, e0, vocab);
+    }
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        float v[E];
-        x[k].widen(v);
+    for (int k = 0; k < R; ++k) {
+      float v[E];
+      x[k].widen(v);
 #pragma unroll
-        for (int e = 0; e < E; ++e) mask |= v[e] >= least ? 1u << (k * E + e) : 0u;
-      }
-    } else {
-#pragma unroll 4
-      for (int m = 0; m < R * E; ++m) {
-        const int at = element(thread, i, m / E) + m % E;
-        if (at >= 0 && at < vocab && Elem<T>::up(row[at]) >= least) mask |= 1u << m;
-      }
+      for (int e = 0; e < E; ++e) mask |= v[e] >= least ? 1u << (k * E + e) : 0u;
     }
     for (; mask; mask &= mask - 1) {
       const int m = __ffs(mask) - 1, at = element(thread, i, m / E) + m % E;
@@ -396,7 +385,7 @@ struct JoinShared {
   float score[HG_MAX_BEAMS];
   float near[HG_MAX_BEAMS];  // score - logsumexp in fp32
   bool done[HG_MAX_BEAMS];   // finished, and still a candidate
-  float largest[2];          // magnitude of near, below kHuge, of 32 beams each
+  uint32_t largest[2];       // magnitude of near, below kHuge, as bits
   bool reaches[HG_MAX_BEAMS];  // the bound, by a logit
   int warp_count[2][kMostJoinWarps];
   double top_total[kMostJoinWarps];
@@ -418,7 +407,7 @@ struct JoinShared {
   __device__ __noinline__ float exactly(int b, float x) const { return (float)sum(b, x); }
   // Three roundings of at most half a unit in the last place of the two terms and of the sum.
   __device__ __forceinline__ float off(float t) const {
-    const float most = fmaxf(largest[0], largest[1]);
+    const float most = __uint_as_float(max(largest[0], largest[1]));
     return fabsf(t) < INFINITY ? 3.f * 5.9604645e-8f * (most + fabsf(t)) : 0.f;
   }
   // Lists a candidate that fp32 can tell from -inf.
@@ -452,8 +441,8 @@ __device__ __forceinline__ void put_id(void* p, int bytes, size_t i, int v) {
     static_cast<int*>(p)[i] = v;
 }
 
-__device__ __forceinline__ void put_pick(const SelectArgs& a, int item, int rank, bool there,
-                                         double total, int beam, u64 key) {
+__device__ __forceinline__ void put_pick(const SelectArgs& a, const JoinShared& s, int item,
+                                         int rank, bool there, double total, int beam, u64 key) {
   const SelectCall& c = a.c;
   const size_t at = (size_t)item * a.picks + rank;
   const int token = there ? (int)~(uint32_t)key : -1;
@@ -462,34 +451,60 @@ __device__ __forceinline__ void put_pick(const SelectArgs& a, int item, int rank
   c.picked[at] = there ? (float)total : -INFINITY;
   if (c.picked_finished)
     c.picked_finished[at] =
-        there && (token == c.end || (c.finished && c.finished[(size_t)item * a.beams + beam]));
+        there && (token == c.end || s.done[beam]);
 }
 
-// Logsumexp of a row from what its parts' warps have, by one warp. The logarithm of the
-// sum's exponent is exact to 64 bits, that of its mantissa, below 0.35, to 32.
-__device__ __forceinline__ double row_lse(const SelectArgs& a, int part0, int parts) {
-  const int lane = threadIdx.x & 31;
-  Exponentials t;
-  for (int i = lane; i < parts * kWarps; i += 32) {
-    const float2 s = __ldcg(a.stats + (size_t)part0 * kWarps + i);
-    t.join(s.x, s.y);
+// What parts' warps have of a row's exponentials, by one warp.
+struct RowStats {
+  static constexpr int kOfLane = 4;
+  int first, all;  // the row's, of all that there are
+  float2 v[kOfLane];
+
+  __device__ __forceinline__ void enter(const SelectArgs& a, int row) {
+    const int part0 = a.part_of(a.cta_of(row * a.chunks), row);
+    first = part0 * kWarps;
+    all = (a.part_of(a.cta_of((row + 1) * a.chunks - 1), row) - part0 + 1) * kWarps;
   }
+  __device__ __forceinline__ void load(const SelectArgs& a, int from) {
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1)
-    t.join(__shfl_xor_sync(0xffffffffu, t.most, m), __shfl_xor_sync(0xffffffffu, t.sum, m));
-  if (!(t.sum < INFINITY)) return t.sum;  // NaN
-  if (!Exponentials::plain(t.most)) return t.most;
-  int e = 0;
-  float f = frexpf(t.sum, &e);  // in [0.5, 1)
-  if (f < 0.70710678f) {
-    f *= 2.f;
-    --e;
+    for (int k = 0; k < kOfLane; ++k) {
+      const int i = from + k * 32 + (threadIdx.x & 31);
+      v[k] = i < all ? __ldcg(a.stats + first + i) : make_float2(-INFINITY, 0.f);
+    }
   }
-  // kLog2e is 1 - kLog2eOff times log2(e): its share of the logits, nearly the largest one's.
-  return t.sum > 0.f ? ((double)Exponentials::shift(t.most) + e) * kLn2 + (double)logf(f) +
-                           (double)t.most * kLog2eOff
+  // The row's logsumexp; the first values are loaded. The logarithm of the sum's exponent is
+  // exact to 64 bits, that of its mantissa, below 0.35, to 32.
+  __device__ __forceinline__ double lse(const SelectArgs& a) {
+    float most = -INFINITY, sum = 0.f;
+    for (int from = 0;;) {
+      float top = most;
+#pragma unroll
+      for (int k = 0; k < kOfLane; ++k) top = fmaxf(top, v[k].x);
+      top = unordered(__reduce_max_sync(0xffffffffu, ordered(top)));
+      sum *= Exponentials::weight(most, top);
+#pragma unroll
+      for (int k = 0; k < kOfLane; ++k) sum += v[k].y * Exponentials::weight(v[k].x, top);
+      most = top;
+      from += kOfLane * 32;
+      if (from >= all) break;
+      load(a, from);
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (!(sum < INFINITY)) return sum;  // NaN
+    if (!Exponentials::plain(most)) return most;
+    int e = 0;
+    float f = frexpf(sum, &e);  // in [0.5, 1)
+    if (f < 0.70710678f) {
+      f *= 2.f;
+      --e;
+    }
+    // kLog2e is 1 - kLog2eOff times log2(e): its share of the logits, nearly the largest one's.
+    return sum > 0.f ? ((double)Exponentials::shift(most) + e) * kLn2 + (double)logf(f) +
+                           (double)most * kLog2eOff
                      : -INFINITY;
-}
+  }
+};
 
 template <int WARPS>
 __device__ __forceinline__ int count_all(int c, int turn, JoinShared& s) {
@@ -582,7 +597,7 @@ __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinSha
       if (o.before(top)) top = o;
     }
     under = top;  // once none, nothing comes after it
-    if (threadIdx.x == 0) put_pick(a, item, i, top.beam >= 0, top.total, top.beam, top.key);
+    if (threadIdx.x == 0) put_pick(a, s, item, i, top.beam >= 0, top.total, top.beam, top.key);
   }
 }
 
@@ -597,6 +612,9 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
   // The groups' maxima; the last value of a thread is a finished beam's score.
   const int listed = parts << a.log_groups;
   const float* maxima = a.maxima + ((size_t)part0 << a.log_groups);
+  RowStats stats;
+  const bool sums = !c.lse && warp < a.beams;
+  if (sums) stats.enter(a, row0 + warp);
   wait_for_predecessor();
   let_successor_start();
   float value[kValues];
@@ -607,46 +625,50 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
     value[k] = __ldcg(maxima + i);
     beam[k] = __ldcg(a.beam_of + part0 + (i >> a.log_groups));
   }
-  float near = 0.f;
+  if (sums) stats.load(a, 0);
+  // How large the terms of a total are at most, for its rounding.
+  auto magnitude = [](float near) { return fabsf(near) < kHuge ? __float_as_uint(fabsf(near)) : 0u; };
+  uint32_t most = 0;
   value[kValues - 1] = -INFINITY;
   if ((int)threadIdx.x < a.beams) {
     const int b = threadIdx.x, row = row0 + b;
     const float score = c.scores[row];
     const bool done = c.finished && c.finished[row] && score > -INFINITY;
     const double lse = c.lse ? (double)c.lse[row * c.lse_stride] : 0.0;
-    near = (float)((double)score - lse);
+    const float near = (float)((double)score - lse);
     s.score[b] = score;
     s.done[b] = done;
     s.lse[b] = lse;
     s.near[b] = near;
     s.reaches[b] = false;
     if (done) value[kValues - 1] = score;
+    most = magnitude(near);
   }
   if (threadIdx.x == 0) s.hits = s.count = 0;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0 && warp < 2) s.largest[warp] = most;
+  static_assert(HG_MAX_BEAMS <= 64, "two warps have the beams");
+  __syncthreads();
   if (!c.lse) {
-    __syncthreads();
-    for (int b = warp; b < a.beams; b += (THREADS / 32)) {
-      const int row = row0 + b, first = a.part_of(a.cta_of(row * a.chunks), row);
-      if (!searched(c, row)) continue;
-      const double lse =
-          row_lse(a, first, a.part_of(a.cta_of((row + 1) * a.chunks - 1), row) - first + 1);
+    for (int b = warp; b < a.beams; b += THREADS / 32) {
+      if (!(s.score[b] > -INFINITY) || s.done[b]) continue;
+      if (b != warp) {
+        stats.enter(a, row0 + b);
+        stats.load(a, 0);
+      }
+      const double lse = stats.lse(a);
       if (lane == 0) {
+        const float near = (float)((double)s.score[b] - lse);
         s.lse[b] = lse;
-        s.near[b] = (float)((double)s.score[b] - lse);
+        s.near[b] = near;
+        atomicMax(&s.largest[0], magnitude(near));
       }
     }
     __syncthreads();
-    if ((int)threadIdx.x < a.beams) near = s.near[threadIdx.x];
   }
-  // How large the terms of a total are at most, for its rounding.
-  near = fabsf(near) < kHuge ? fabsf(near) : 0.f;
-  const uint32_t largest = __reduce_max_sync(0xffffffffu, __float_as_uint(near));
-  if (lane == 0 && warp < 2) s.largest[warp] = __uint_as_float(largest);
-  static_assert(HG_MAX_BEAMS <= 64, "two warps have the beams");
-  __syncthreads();
 
-  // The groups' best totals, nearly, and their words from below.
-  uint32_t word = 0;
+  // The groups' best totals, nearly, and the word of the best of them from below.
+  float best = -INFINITY;
 #pragma unroll
   for (int k = 0; k < kValues; ++k) {
     float t = value[k];
@@ -655,11 +677,13 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
       t = there && t > -INFINITY ? s.nearly(beam[k], t) : -INFINITY;
     }
     value[k] = t;
-    if (t > -INFINITY) word = max(word, ordered(t - s.off(t)));
+    best = fmaxf(best, t);
   }
+  const uint32_t word = best > -INFINITY ? ordered(best - s.off(best)) : 0;
   const float from = bound_of_best<THREADS / 32>(a.picks, word, s.bound);
 #pragma unroll
   for (int k = 0; k < kValues; ++k) {
+    if (!(best + s.off(best) >= from)) break;
     if (!(value[k] + s.off(value[k]) >= from)) continue;
     if (k == kValues - 1) {
       s.add(value[k], threadIdx.x, (uint32_t)~c.end);
@@ -727,11 +751,11 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
     if (there && eighth == 0 && rank < a.picks) {
       const double d =
           __longlong_as_double((long long)(total >> 63 ? total & ~(1ull << 63) : ~total));
-      put_pick(a, item, rank, true, d, b, key);
+      put_pick(a, s, item, rank, true, d, b, key);
     }
   }
   for (int i = found + threadIdx.x; i < a.picks; i += THREADS)
-    put_pick(a, item, i, false, 0.0, -1, 0);
+    put_pick(a, s, item, i, false, 0.0, -1, 0);
 }
 
 template <typename T, int R>
@@ -764,9 +788,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           for (int k = 0; k < R; ++k) copy_ahead(to + k * kThreads, from + k * kThreads);
         } else {
 #pragma unroll 1
-          for (int k = 0; k < R; ++k)
-            Access<T>::copy_edge(to + k * kThreads, ahead_at,
-                                 e0 + (k * kThreads + (int)threadIdx.x) * E, a.vocab);
+          for (int k = 0; k < R; ++k) {
+            const int e = e0 + (k * kThreads + (int)threadIdx.x) * E;
+            if (Access<T>::inside(e, a.vocab))
+              copy_ahead(to + k * kThreads, ahead_at + e);
+            else
+              to[k * kThreads] = Access<T>::edge(ahead_at, e, a.vocab).w;
+          }
         }
       }
       ++ahead;
