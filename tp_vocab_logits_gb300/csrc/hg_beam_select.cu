@@ -76,9 +76,16 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 __device__ __forceinline__ float unordered(uint32_t u) {
   return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
 }
+// (64-bit arithmetic is slow: the bits are looked at.)
 __device__ __forceinline__ u64 ordered(double v) {
-  const u64 u = (u64)__double_as_longlong(v + 0.0);
-  return u >> 63 ? ~u : u | 1ull << 63;
+  const u64 u = (u64)__double_as_longlong(v);
+  return u >> 63 && u << 1 ? ~u : u | 1ull << 63;
+}
+// Whether it is a number that is not -inf in fp32, to which half a unit beyond the largest
+// number rounds.
+__device__ __forceinline__ bool counts(double v) {
+  const u64 u = (u64)__double_as_longlong(v), size = u & ~(1ull << 63);
+  return size <= 0x7ff0000000000000ull && !(u >> 63 && size >= 0x47effffff0000000ull);
 }
 
 // Larger keys are better candidates of a row; 0 is none.
@@ -311,7 +318,8 @@ __device__ __forceinline__ float bound_of_best(int n, uint32_t word, BoundShared
   __syncthreads();
   uint32_t top = s.word[tid % WARPS][tid / WARPS];
   const int width = kThreadsHere >> log_groups;  // threads of a group
-  for (int m = 1; m < width; m <<= 1) top = max(top, __shfl_xor_sync(kAll, top, m));
+  if (width == 32) top = __reduce_max_sync(kAll, top);
+  else for (int m = 1; m < width; m <<= 1) top = max(top, __shfl_xor_sync(kAll, top, m));
   const int group = tid / width, turn = tid % width;
   if (turn == 0) s.top[group] = top;
   __syncthreads();
@@ -320,27 +328,28 @@ __device__ __forceinline__ float bound_of_best(int n, uint32_t word, BoundShared
     const uint32_t other = s.top[i];
     rank += other > top || (other == top && i < group);
   }
-  for (int m = 1; m < width; m <<= 1) rank += __shfl_xor_sync(kAll, rank, m);
+  if (width == 32) rank = __reduce_add_sync(kAll, rank);
+  else for (int m = 1; m < width; m <<= 1) rank += __shfl_xor_sync(kAll, rank, m);
   if (turn == 0 && rank == n - 1) s.bound = top;
   __syncthreads();
   return s.bound < ordered(kLeast) ? kLeast : unordered(s.bound);
 }
 
-// ---- one CTA's part of a row -------------------------------------------------------
+// ---- a row -------------------------------------------------------------------------
 
-// Chunks [first, first + chunks) of a row, as the threads of a CTA have them.
+// A row, as the threads of a CTA have it.
 template <typename T, int R>
-struct Part {
+struct Row {
   static constexpr int E = Access<T>::E;
-  const T* row;  // null: its logits do not count
-  int first, chunks, vocab;
+  const T* row;
+  int vocab;
 
   __device__ __forceinline__ int shift() const {
     return (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
   }
   // The first element of a thread's access k of chunk i.
   __device__ __forceinline__ int element(int thread, int i, int k) const {
-    return (((first + i) * R + k) * kThreads + thread) * E - shift();
+    return ((i * R + k) * kThreads + thread) * E - shift();
   }
   // Calls f(logit, token) for the elements of a thread from `least` (above -inf) on, in chunk i.
   template <typename F>
@@ -371,17 +380,12 @@ struct Part {
 
 // ---- joining an item's parts -------------------------------------------------------
 
-// A group of threads whose largest logit reaches the bound: what it has of a row.
-struct Hit {
-  int row, first, chunks, thread;
-};
-
 struct JoinShared {
   u64 total[kList], key[kList];
   unsigned char beam[kList];
-  Hit hit[kHits];
+  int hit[kHits];  // groups of threads whose largest logit reaches the bound, and their beams
   BoundShared bound;
-  double lse[HG_MAX_BEAMS];
+  double lse[HG_MAX_BEAMS], score_64[HG_MAX_BEAMS];
   float score[HG_MAX_BEAMS];
   float near[HG_MAX_BEAMS];  // score - logsumexp in fp32
   bool done[HG_MAX_BEAMS];   // finished, and still a candidate
@@ -395,7 +399,7 @@ struct JoinShared {
 
   // The total of a beam's logit, as it is compared.
   __device__ __forceinline__ double sum(int b, float x) const {
-    return (double)score[b] + ((double)x - lse[b]);
+    return score_64[b] + ((double)x - lse[b]);
   }
   // The same to within `off` of it in fp32 (64-bit additions are slow, and few candidates
   // come near the best).
@@ -412,7 +416,7 @@ struct JoinShared {
   }
   // Lists a candidate that fp32 can tell from -inf.
   __device__ __noinline__ void add(double t, int b, u64 k) {
-    if (!((float)t > -INFINITY)) return;
+    if (!counts(t)) return;
     const int at = atomicAdd(&count, 1);
     if (at >= kList) return;
     total[at] = ordered(t);
@@ -454,6 +458,12 @@ __device__ __forceinline__ void put_pick(const SelectArgs& a, const JoinShared& 
         there && (token == c.end || s.done[beam]);
 }
 
+// a + b, and what the rounding left out.
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
+}
+
 // What parts' warps have of a row's exponentials, by one warp.
 struct RowStats {
   static constexpr int kOfLane = 4;
@@ -472,9 +482,8 @@ struct RowStats {
       v[k] = i < all ? __ldcg(a.stats + first + i) : make_float2(-INFINITY, 0.f);
     }
   }
-  // The row's logsumexp; the first values are loaded. The logarithm of the sum's exponent is
-  // exact to 64 bits, that of its mantissa, below 0.35, to 32.
-  __device__ __forceinline__ double lse(const SelectArgs& a) {
+  // The row's logsumexp, as hi + lo; the first values are loaded.
+  __device__ __forceinline__ float2 lse(const SelectArgs& a) {
     float most = -INFINITY, sum = 0.f;
     for (int from = 0;;) {
       float top = most;
@@ -491,18 +500,25 @@ struct RowStats {
     }
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    if (!(sum < INFINITY)) return sum;  // NaN
-    if (!Exponentials::plain(most)) return most;
-    int e = 0;
-    float f = frexpf(sum, &e);  // in [0.5, 1)
+    if (!(sum < INFINITY)) return make_float2(sum, 0.f);  // NaN
+    if (!Exponentials::plain(most)) return make_float2(most, 0.f);
+    if (!(sum > 0.f)) return make_float2(-INFINITY, 0.f);
+    int exponent = 0;
+    float f = frexpf(sum, &exponent);  // in [0.5, 1)
     if (f < 0.70710678f) {
       f *= 2.f;
-      --e;
+      --exponent;
     }
-    // kLog2e is 1 - kLog2eOff times log2(e): its share of the logits, nearly the largest one's.
-    return sum > 0.f ? ((double)Exponentials::shift(most) + e) * kLn2 + (double)logf(f) +
-                           (double)most * kLog2eOff
-                     : -INFINITY;
+    // The logarithm of the powers of two is a sum of two numbers, that of the mantissa, below
+    // 0.35, one. kLog2e is 1 - kLog2eOff times log2(e): its share of the logits, nearly the
+    // largest one's.
+    constexpr float kHi = (float)kLn2, kLo = (float)(kLn2 - (double)kHi);
+    const float n = Exponentials::shift(most), e = (float)exponent;
+    const float p = __fmul_rn(n, kHi), q = __fmul_rn(e, kHi);
+    const float2 first = two_sum(p, q), second = two_sum(first.x, logf(f));
+    const float lo = fmaf(n, kHi, -p) + fmaf(e, kHi, -q) + first.y + second.y + (n + e) * kLo +
+                     most * (float)kLog2eOff;
+    return two_sum(second.x, lo);
   }
 };
 
@@ -527,8 +543,8 @@ __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinSha
     u64* list = a.list + (size_t)(row0 + b) * n;
     for (int i = threadIdx.x; i < n; i += THREADS) list[i] = 0;
     if (!s.reaches[b]) continue;
-    const Part<T, R> part = {static_cast<const T*>(a.c.logits) + (size_t)(row0 + b) * a.c.ld, 0,
-                             a.chunks, a.vocab};
+    const Row<T, R> one = {static_cast<const T*>(a.c.logits) + (size_t)(row0 + b) * a.c.ld,
+                             a.vocab};
     // All tokens' complements have the bits above the vocabulary's.
     const int low = 32 - __clz(a.vocab);
     u64 bound = 0;
@@ -539,8 +555,8 @@ __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinSha
       }
       const u64 next = bound | 1ull << bit;
       int c = 0;
-      for (int i = first; i < part.chunks; i += kStep)
-        part.each(thread, i, kLeast, [&](float x, int token) { c += key_of(x, token) >= next; });
+      for (int i = first; i < a.chunks; i += kStep)
+        one.each(thread, i, kLeast, [&](float x, int token) { c += key_of(x, token) >= next; });
       c = count_all<THREADS / 32>(c, bit & 1, s);
       if (c >= n) bound = next;
       if (c == n) break;
@@ -548,8 +564,8 @@ __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinSha
     __syncthreads();
     if (threadIdx.x == 0) s.count = 0;
     __syncthreads();
-    for (int i = first; i < part.chunks; i += kStep)
-      part.each(thread, i, kLeast, [&](float x, int token) {
+    for (int i = first; i < a.chunks; i += kStep)
+      one.each(thread, i, kLeast, [&](float x, int token) {
         if (key_of(x, token) < bound) return;
         const int at = atomicAdd(&s.count, 1);
         if (at < n) list[at] = key_of(x, token);
@@ -574,7 +590,7 @@ __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinSha
         if (!s.done[t.beam]) continue;
         t.total = s.score[t.beam];
       }
-      if (!((float)t.total > -INFINITY)) continue;
+      if (!counts(t.total)) continue;
       if ((i == 0 || under.before(t)) && t.before(top)) top = t;
     }
 #pragma unroll
@@ -634,11 +650,12 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
     const int b = threadIdx.x, row = row0 + b;
     const float score = c.scores[row];
     const bool done = c.finished && c.finished[row] && score > -INFINITY;
-    const double lse = c.lse ? (double)c.lse[row * c.lse_stride] : 0.0;
-    const float near = (float)((double)score - lse);
+    const float lse = c.lse ? c.lse[row * c.lse_stride] : 0.f;
+    const float near = score - lse;
     s.score[b] = score;
+    s.score_64[b] = (double)score;
     s.done[b] = done;
-    s.lse[b] = lse;
+    s.lse[b] = (double)lse;
     s.near[b] = near;
     s.reaches[b] = false;
     if (done) value[kValues - 1] = score;
@@ -648,6 +665,7 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
   most = __reduce_max_sync(0xffffffffu, most);
   if (lane == 0 && warp < 2) s.largest[warp] = most;
   static_assert(HG_MAX_BEAMS <= 64, "two warps have the beams");
+  static_assert(kMostValues <= 1 << 16, "a hit's place and beam are a word");
   __syncthreads();
   if (!c.lse) {
     for (int b = warp; b < a.beams; b += THREADS / 32) {
@@ -656,10 +674,11 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
         stats.enter(a, row0 + b);
         stats.load(a, 0);
       }
-      const double lse = stats.lse(a);
+      const float2 lse = stats.lse(a);
       if (lane == 0) {
-        const float near = (float)((double)s.score[b] - lse);
-        s.lse[b] = lse;
+        const float2 d = two_sum(s.score[b], -lse.x);
+        const float near = fabsf(d.x) < kHuge ? d.x + (d.y - lse.y) : d.x;
+        s.lse[b] = (double)lse.x + (double)lse.y;
         s.near[b] = near;
         atomicMax(&s.largest[0], magnitude(near));
       }
@@ -692,15 +711,7 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
     s.reaches[beam[k]] = true;
     const int at = atomicAdd(&s.hits, 1);
     if (at >= kHits) continue;
-    const int i = threadIdx.x + k * THREADS;
-    const int part = i >> a.log_groups, group = i - (part << a.log_groups);
-    const int row = row0 + beam[k], begin = row * a.chunks, end = begin + a.chunks;
-    int first = begin, last = end;
-    if (!a.whole_rows) {
-      first = max(begin, a.first_chunk(part0 + part - row));
-      last = min(end, a.first_chunk(part0 + part - row + 1));
-    }
-    s.hit[at] = {row, first - begin, last - first, group << (kLogThreads - a.log_groups)};
+    s.hit[at] = beam[k] << 16 | ((int)threadIdx.x + k * THREADS);
   }
   __syncthreads();
   const int hits = s.hits;
@@ -710,20 +721,27 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
     const int units = (hits * a.longest) << log_width;
     for (int u = threadIdx.x; u < units; u += THREADS) {
       const int pair = u >> log_width, h = a.by_longest.divide(pair);
-      const Hit hit = s.hit[h];
-      const int chunk = pair - h * a.longest, b = hit.row - row0;
-      if (chunk >= hit.chunks) continue;
-      const Part<T, R> part = {static_cast<const T*>(c.logits) + (size_t)hit.row * c.ld, hit.first,
-                               hit.chunks, a.vocab};
+      const int hit = s.hit[h], b = hit >> 16, in = hit & 0xffff;
+      const int part = in >> a.log_groups, group = in - (part << a.log_groups);
+      // What the group has of the row.
+      const int row = row0 + b, begin = row * a.chunks;
+      int first = begin, last = begin + a.chunks;
+      if (!a.whole_rows) {
+        first = max(first, a.first_chunk(part0 + part - row));
+        last = min(last, a.first_chunk(part0 + part - row + 1));
+      }
+      const int chunk = first + pair - h * a.longest;
+      if (chunk >= last) continue;
+      const Row<T, R> whole = {static_cast<const T*>(c.logits) + (size_t)row * c.ld, a.vocab};
       // From which logit on a total may reach the bound: well below it.
       const float least = from - s.near[b];
       const bool plain = fabsf(s.near[b]) < kHuge && fabsf(least) < kHuge;
-      part.each(hit.thread + (u & ((1 << log_width) - 1)), chunk,
-                plain ? least - 4.f * s.off(fabsf(from) + fabsf(least)) : kLeast,
-                [&](float x, int token) {
-                  const float t = s.nearly(b, x);
-                  if (t + s.off(t) >= from) s.add(s.sum(b, x), b, key_of(x, token));
-                });
+      whole.each((group << log_width) + (u & ((1 << log_width) - 1)), chunk - begin,
+               plain ? least - 4.f * s.off(fabsf(from) + fabsf(least)) : kLeast,
+               [&](float x, int token) {
+                 const float t = s.nearly(b, x);
+                 if (t + s.off(t) >= from) s.add(s.sum(b, x), b, key_of(x, token));
+               });
     }
   }
   __syncthreads();
@@ -734,8 +752,8 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
   }
   // Each candidate's rank; eight lanes count what comes before it.
   const int eighth = threadIdx.x % 8;
-  for (int i0 = 0; i0 < found; i0 += THREADS / 8) {
-    const int i = i0 + threadIdx.x / 8;
+  for (int i0 = warp * 4; i0 < found; i0 += THREADS / 8) {
+    const int i = i0 + lane / 8;
     const bool there = i < found;
     const u64 total = there ? s.total[i] : ~0ull, key = there ? s.key[i] : ~0ull;
     const int b = there ? s.beam[i] : 0;
