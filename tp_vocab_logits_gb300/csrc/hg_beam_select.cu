@@ -286,10 +286,6 @@ struct Exponentials {
     const u64 both = add2(sums[0], sums[1]);
     sum = low(both) + high(both);
   }
-  __device__ __forceinline__ void join(float other_most, float other_sum) {
-    raise(other_most);
-    sum += other_sum * weight(other_most, most);
-  }
 };
 
 constexpr float kLeast = -3.402823466e38f;
@@ -851,12 +847,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (threadIdx.x == 0) a.beam_of[part] = on ? row - a.by_beams.divide(row) * a.beams : kNone;
     if (on) {
       if (!a.c.lse) {
-        sums.raise(best);
+        const float top = unordered(__reduce_max_sync(0xffffffffu, ordered(best)));
+        float sum = sums.sum * Exponentials::weight(sums.most, top);
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1)
-          sums.join(__shfl_xor_sync(0xffffffffu, sums.most, m),
-                    __shfl_xor_sync(0xffffffffu, sums.sum, m));
-        if (lane == 0) a.stats[(size_t)part * kWarps + warp] = make_float2(sums.most, sums.sum);
+        for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        if (lane == 0) a.stats[(size_t)part * kWarps + warp] = make_float2(top, sum);
       }
       const int log_width = kLogThreads - a.log_groups;
       for (int m = 1; m < 1 << log_width; m <<= 1)
