@@ -33,10 +33,15 @@ static_assert(1 << kLogThreads == kThreads, "groups of threads are counted in po
 constexpr int kStages = 2;       // chunks in the ring
 constexpr int kMostJoinWarps = 32;
 constexpr int kList = 1024;      // candidates of an item that are ranked at once
+constexpr int kRanked = 128;     // that are ranked as they are: ranking takes their square
 constexpr int kHits = 512;       // groups of threads whose elements are read again
 constexpr int kCtasPerSm = 4;
-constexpr int kValues = 5;  // of a thread in join_kernel: groups, and a finished beam's
-constexpr int kMostValues = 1024 * (kValues - 1);  // maxima that are joined of an item
+// Maxima that a thread of join_kernel takes. Many picks have many elements read again, of
+// groups that are finer where there are more of them (163840 logits, an item of 64 beams with 128
+// picks: 48 and 35 us; 8 items of 8 with 16: 11.9 and 14.0). Many parts need the room, or rows
+// stay whole (an item of 32 beams with 32 picks: 21 and 17).
+constexpr int kFewValues = 4, kManyValues = 16;
+constexpr int kFewPicks = 32;
 constexpr int kLeastGroups = 8;    // of a part's threads, at least, that have a maximum: warps
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr double kLn2 = 0.693147180559945309417;
@@ -298,13 +303,12 @@ struct BoundShared {
   uint32_t bound;
 };
 
-// A value that at least n of the threads' words (ordered values; 0: none) are not under, and
-// not many more: the n-th largest of the maxima of groups of threads, twice n of them (which
+// A word that at least n of the threads' words (0: none) are not under, and not many more: the n-th largest of the maxima of groups of threads, twice n of them (which
 // 1.4 n words reach where they are in any order). A group takes one thread from each of some
-// warps, another lane of every one, as neighbours, and threads a part apart, have alike values.
-// The least finite value if there are not n.
+// warps, another lane of every one: warps apart and other lanes, as neighbours are of one beam.
+// 0 if there are not n.
 template <int WARPS>
-__device__ __forceinline__ float bound_of_best(int n, uint32_t word, BoundShared& s) {
+__device__ __forceinline__ uint32_t bound_of_best(int n, uint32_t word, BoundShared& s) {
   constexpr unsigned kAll = 0xffffffffu;
   constexpr int kThreadsHere = WARPS * 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -312,8 +316,9 @@ __device__ __forceinline__ float bound_of_best(int n, uint32_t word, BoundShared
   static_assert(2 * HG_MAX_PICKS <= 256, "no more groups than threads");
   s.word[warp][(lane + warp * 5 + warp / 8) & 31] = word;
   __syncthreads();
-  uint32_t top = s.word[tid % WARPS][tid / WARPS];
   const int width = kThreadsHere >> log_groups;  // threads of a group
+  // Warps as far apart as they can be.
+  uint32_t top = s.word[tid % width * (WARPS / width) + tid % WARPS / width][tid / WARPS];
   if (width == 32) top = __reduce_max_sync(kAll, top);
   else for (int m = 1; m < width; m <<= 1) top = max(top, __shfl_xor_sync(kAll, top, m));
   const int group = tid / width, turn = tid % width;
@@ -328,7 +333,7 @@ __device__ __forceinline__ float bound_of_best(int n, uint32_t word, BoundShared
   else for (int m = 1; m < width; m <<= 1) rank += __shfl_xor_sync(kAll, rank, m);
   if (turn == 0 && rank == n - 1) s.bound = top;
   __syncthreads();
-  return s.bound < ordered(kLeast) ? kLeast : unordered(s.bound);
+  return s.bound;
 }
 
 // ---- a row -------------------------------------------------------------------------
@@ -613,7 +618,7 @@ __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinSha
   }
 }
 
-template <typename T, int R, int THREADS>
+template <typename T, int R, int THREADS, int VALUES>
 __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant__ SelectArgs a) {
   __shared__ JoinShared s;
   const SelectCall& c = a.c;
@@ -621,7 +626,6 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
   const int item = blockIdx.x, row0 = item * a.beams, row_last = row0 + a.beams - 1;
   const int part0 = a.part_of(a.cta_of(row0 * a.chunks), row0);
   const int parts = a.part_of(a.cta_of((row_last + 1) * a.chunks - 1), row_last) - part0 + 1;
-  // The groups' maxima; the last value of a thread is a finished beam's score.
   const int listed = parts << a.log_groups;
   const float* maxima = a.maxima + ((size_t)part0 << a.log_groups);
   RowStats stats;
@@ -629,6 +633,7 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
   if (sums) stats.enter(a, row0 + warp);
   wait_for_predecessor();
   let_successor_start();
+  constexpr int kValues = VALUES + 1;  // the last is a finished beam's score
   float value[kValues];
   int beam[kValues];
 #pragma unroll
@@ -661,7 +666,7 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
   most = __reduce_max_sync(0xffffffffu, most);
   if (lane == 0 && warp < 2) s.largest[warp] = most;
   static_assert(HG_MAX_BEAMS <= 64, "two warps have the beams");
-  static_assert(kMostValues <= 1 << 16, "a hit's place and beam are a word");
+  static_assert(THREADS * VALUES <= 1 << 16, "a hit's place and beam are a word");
   __syncthreads();
   if (!c.lse) {
     for (int b = warp; b < a.beams; b += THREADS / 32) {
@@ -695,7 +700,8 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
     best = fmaxf(best, t);
   }
   const uint32_t word = best > -INFINITY ? ordered(best - s.off(best)) : 0;
-  const float from = bound_of_best<THREADS / 32>(a.picks, word, s.bound);
+  const uint32_t bound = bound_of_best<THREADS / 32>(a.picks, word, s.bound);
+  const float from = bound < ordered(kLeast) ? kLeast : unordered(bound);
 #pragma unroll
   for (int k = 0; k < kValues; ++k) {
     if (!(best + s.off(best) >= from)) break;
@@ -741,10 +747,38 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
     }
   }
   __syncthreads();
-  const int found = s.count;
+  int found = s.count;
   if (hits > kHits || found > kList) {
     pick_exactly<T, R, THREADS>(a, item, s);
     return;
+  }
+  if (found > kRanked && found > 2 * a.picks) {
+    // Of too many those whose totals' upper words reach the n-th best one's.
+    constexpr int kOwn = kList / THREADS;
+    u64 total[kOwn], key[kOwn];
+    int of[kOwn];
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      const int i = threadIdx.x + k * THREADS;
+      total[k] = i < found ? s.total[i] : 0;
+      key[k] = s.key[i];
+      of[k] = s.beam[i];
+      top = max(top, (uint32_t)(total[k] >> 32));
+    }
+    const uint32_t least = bound_of_best<THREADS / 32>(a.picks, top, s.bound);
+    if (threadIdx.x == 0) s.count = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      if (total[k] == 0 || (uint32_t)(total[k] >> 32) < least) continue;
+      const int at = atomicAdd(&s.count, 1);
+      s.total[at] = total[k];
+      s.key[at] = key[k];
+      s.beam[at] = (unsigned char)of[k];
+    }
+    __syncthreads();
+    found = s.count;
   }
   // Each candidate's rank; eight lanes count what comes before it.
   const int eighth = threadIdx.x % 8;
@@ -880,7 +914,9 @@ cudaError_t select_as(const hg_beam& h, SelectArgs& a, cudaStream_t stream) {
   a.more = (int)(all % ctas);
   // An item's parts at most: a CTA's share may end in its rows, and begin, anywhere.
   long long parts = div_up((long long)h.beams * a.chunks, a.each) + 1 + h.beams;
-  a.whole_rows = parts > kMostValues / kLeastGroups;
+  const int values =
+      h.picks > kFewPicks || parts * kLeastGroups > 1024 * kFewValues ? kManyValues : kFewValues;
+  a.whole_rows = parts > 1024 * values / kLeastGroups;
   if (a.whole_rows) {
     a.each = (int)div_up(rows, full) * a.chunks;
     a.more = 0;
@@ -888,10 +924,10 @@ cudaError_t select_as(const hg_beam& h, SelectArgs& a, cudaStream_t stream) {
     parts = h.beams;
   }
   // As many groups of threads as there is room for values of their maxima; less where that
-  // lets small CTAs join, which more items than SMs need (256 items: 29 and 23 us).
-  const int joiners = a.c.items > h.sms && parts * kLeastGroups <= 256 * (kValues - 1) ? 256 : 1024;
+  // lets small CTAs join, which more items than SMs need (256 items: 28 and 24 us).
+  const bool small = values == kFewValues && a.c.items > h.sms && parts * kLeastGroups <= 256 * values;
   a.log_groups = kLogThreads;
-  while (parts << a.log_groups > joiners * (kValues - 1)) --a.log_groups;
+  while (parts << a.log_groups > (small ? 256 : 1024) * values) --a.log_groups;
   a.longest = a.each + (a.more > 0) < a.chunks ? a.each + (a.more > 0) : a.chunks;
   a.by_chunks = Divisor(a.chunks);
   a.by_each = Divisor(a.each);
@@ -902,10 +938,14 @@ cudaError_t select_as(const hg_beam& h, SelectArgs& a, cudaStream_t stream) {
       launch_dependent(select_kernel<T, R>, a, (unsigned)ctas, kThreads,
                        (size_t)kStages * R * kThreads * 16, 1, stream);
   if (e != cudaSuccess) return e;
-  return parts << a.log_groups <= 256 * (kValues - 1)
-             ? launch_dependent(join_kernel<T, R, 256>, a, (unsigned)a.c.items, 256, 0, 1, stream)
-             : launch_dependent(join_kernel<T, R, 1024>, a, (unsigned)a.c.items, 1024, 0, 1,
-                                stream);
+  if (values == kManyValues)
+    return launch_dependent(join_kernel<T, R, 1024, kManyValues>, a, (unsigned)a.c.items, 1024, 0,
+                            1, stream);
+  return parts << a.log_groups <= 256 * values
+             ? launch_dependent(join_kernel<T, R, 256, kFewValues>, a, (unsigned)a.c.items, 256, 0,
+                                1, stream)
+             : launch_dependent(join_kernel<T, R, 1024, kFewValues>, a, (unsigned)a.c.items, 1024,
+                                0, 1, stream);
 }
 
 // Chunks of 16 KB, or smaller ones where there would be few.
