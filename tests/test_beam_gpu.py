@@ -223,6 +223,34 @@ def test_select_ties(V, picks, dtype):
     h.close()
 
 
+@pytest.mark.parametrize("items,beams,V,picks", [
+    (2, 1, 1000, 128), (1, 64, 20000, 128), (3, 5, 700, 40), (1, 33, 40000, 33), (2, 16, 9000, 16),
+    (200, 2, 5000, 8), (160, 1, 3000, 128)])
+@pytest.mark.parametrize("order", ["sorted", "by lane", "one beam", "far apart"])
+def test_select_uneven_logits(items, beams, V, picks, order):
+    """Where the best are not spread over rows and beams: in the order of the tokens, or of
+    their place among a warp's lanes; all of one beam; beams a few units apart."""
+    g = gen_of(V + picks)
+    rows = items * beams
+    noise = torch.rand((rows, V), generator=g, device="cuda")
+    token = torch.arange(V, device="cuda").float()
+    scores = torch.rand((items, beams), generator=g, device="cuda") * 0.01
+    if order == "sorted":
+        z = -2.0 * torch.log(token + 3) + noise * 0.01
+    elif order == "by lane":
+        z = -(token // 8 % 32) + noise
+    else:
+        z = noise * 6 - 3
+        step = 30.0 if order == "one beam" else 1.5
+        scores = scores - step * torch.arange(beams, device="cuda").flip(0)
+    for dtype in (bf16, fp32):
+        logits = z.to(dtype)
+        h = hg.hg_beam_create(items, beams, V, picks, dtype=dtype)
+        lse = exact_lse(logits).float()
+        check_select(Call(h, logits, scores, lse=lse), True)
+        h.close()
+
+
 def test_select_special_logits():
     """NaN is no candidate where the logsumexp is given, and takes its row out where it
     is not; +inf likewise, but a candidate before all others in the first case."""

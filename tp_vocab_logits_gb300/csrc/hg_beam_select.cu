@@ -5,11 +5,13 @@
 // CTA has of a row) keeps the largest logit and, where the logsumexp is wanted, the running
 // maximum and sum of its exponentials: nothing that a chunk costs depends on the number of
 // picks, and no warp waits for another. A second kernel, a CTA per item, joins the parts:
-// with the rows' scores and logsumexps, the n-th largest of the threads' best totals bounds
-// the item's n-th best from below, so only the threads that reach it, little more than n,
-// have their elements read again (from L2) for the candidates. (Lists of the best that were
-// kept up to date chunk by chunk, by CTA or by warp, took two to four times as long; joined by
-// the last CTA of the first kernel, an item takes 12 to 20 us of dependent steps for 256 threads.)
+// with the rows' scores and logsumexps, the threads' best totals bound the item's n-th best
+// from below, so only the threads that reach it, little more than n, have their elements read
+// again (from L2) for the candidates. 32 items of 8 beams, 163840 logits, 16 picks: 22.3 us,
+// 3.8 TB/s, of which the join's chain of dependent steps (sums, bound, elements, ranks) is 5 us;
+// 20.2 us where the logsumexps are given. (Lists of the best that were kept up to date
+// chunk by chunk, by CTA or by warp, took two to four times as long; joined by the last CTA of
+// the first kernel, an item takes 12 to 20 us for 256 threads.)
 
 #include <cmath>
 #include <cstring>
@@ -35,6 +37,7 @@ constexpr int kMostJoinWarps = 32;
 constexpr int kList = 1024;      // candidates of an item that are ranked at once
 constexpr int kRanked = 128;     // that are ranked as they are: ranking takes their square
 constexpr int kHits = 512;       // groups of threads whose elements are read again
+constexpr int kRounds = 4;       // of closer bounds, where there are more of either
 constexpr int kCtasPerSm = 4;
 // Maxima that a thread of join_kernel takes. Many picks have many elements read again, of
 // groups that are finer where there are more of them (163840 logits, an item of 64 beams with 128
@@ -85,6 +88,9 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 __device__ __forceinline__ u64 ordered(double v) {
   const u64 u = (u64)__double_as_longlong(v);
   return u >> 63 && u << 1 ? ~u : u | 1ull << 63;
+}
+__device__ __forceinline__ double unordered(u64 u) {
+  return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
 }
 // Whether it is a number that is not -inf in fp32, to which half a unit beyond the largest
 // number rounds.
@@ -415,6 +421,12 @@ struct JoinShared {
     const float most = __uint_as_float(max(largest[0], largest[1]));
     return fabsf(t) < INFINITY ? 3.f * 5.9604645e-8f * (most + fabsf(t)) : 0.f;
   }
+  // Lists a group of threads, the `place`-th that an item has.
+  __device__ __forceinline__ void note(int b, int place) {
+    reaches[b] = true;
+    const int at = atomicAdd(&hits, 1);
+    if (at < kHits) hit[at] = b << 16 | place;
+  }
   // Lists a candidate that fp32 can tell from -inf.
   __device__ __noinline__ void add(double t, int b, u64 k) {
     if (!counts(t)) return;
@@ -618,6 +630,74 @@ __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinSha
   }
 }
 
+// Lists the elements of the listed groups whose totals may reach the bound, a thread's of a
+// chunk each.
+template <typename T, int R, int THREADS>
+__device__ __forceinline__ void collect(const SelectArgs& a, int row0, int part0, float from,
+                                        JoinShared& s) {
+  const int log_width = kLogThreads - a.log_groups;
+  const unsigned units = (unsigned)(min(s.hits, kHits) * a.longest) << log_width;
+  for (unsigned u = threadIdx.x; u < units; u += THREADS) {
+    const int pair = (int)(u >> log_width), h = a.by_longest.divide(pair);
+    const int hit = s.hit[h], b = hit >> 16, in = hit & 0xffff;
+    const int part = in >> a.log_groups, group = in - (part << a.log_groups);
+    // What the group has of the row.
+    const int row = row0 + b, begin = row * a.chunks;
+    int first = begin, last = begin + a.chunks;
+    if (!a.whole_rows) {
+      first = max(first, a.first_chunk(part0 + part - row));
+      last = min(last, a.first_chunk(part0 + part - row + 1));
+    }
+    const int chunk = first + pair - h * a.longest;
+    if (chunk >= last) continue;
+    const Row<T, R> whole = {static_cast<const T*>(a.c.logits) + (size_t)row * a.c.ld, a.vocab};
+    // From which logit on a total may reach the bound: well below it.
+    const float least = from - s.near[b];
+    const bool plain = fabsf(s.near[b]) < kHuge && fabsf(least) < kHuge;
+    whole.each((group << log_width) + (int)(u & ((1 << log_width) - 1)), chunk - begin,
+               plain ? least - 4.f * s.off(fabsf(from) + fabsf(least)) : kLeast,
+               [&](float x, int token) {
+                 const float t = s.nearly(b, x);
+                 if (t + s.off(t) >= from) s.add(s.sum(b, x), b, key_of(x, token));
+               });
+  }
+}
+
+// Where there are too many, as where the best are neighbours: of those that are listed the n-th
+// best is a closer bound, if they are not alike. Returns whether all fit then. (Logits that fall
+// with the token, an item of 32 beams with 32 picks: 14.6 ms by pick_exactly, 38 us so.)
+template <typename T, int R, int THREADS>
+__device__ __noinline__ bool narrow(const SelectArgs& a, int row0, int part0, int listed,
+                                    float from, JoinShared& s) {
+  const float* maxima = a.maxima + ((size_t)part0 << a.log_groups);
+  for (int round = 0; round < kRounds; ++round) {
+    uint32_t top = 0;
+    for (int i = threadIdx.x; i < min(s.count, kList); i += THREADS)
+      top = max(top, (uint32_t)(s.total[i] >> 32));
+    const uint32_t bound = bound_of_best<THREADS / 32>(a.picks, top, s.bound);
+    float next = bound ? (float)unordered((u64)bound << 32) : kLeast;
+    next -= s.off(next);
+    if (!(next > from)) return false;
+    from = next;
+    if (threadIdx.x == 0) s.hits = s.count = 0;
+    __syncthreads();
+    if ((int)threadIdx.x < a.beams && s.done[threadIdx.x] && s.score[threadIdx.x] >= from)
+      s.add(s.score[threadIdx.x], threadIdx.x, (uint32_t)~a.c.end);
+    for (int i = threadIdx.x; i < listed; i += THREADS) {
+      const float value = __ldcg(maxima + i);
+      const int b = __ldcg(a.beam_of + part0 + (i >> a.log_groups));
+      if (b == kNone || !(value > -INFINITY)) continue;
+      const float t = s.nearly(b, value);
+      if (t + s.off(t) >= from) s.note(b, i);
+    }
+    __syncthreads();
+    collect<T, R, THREADS>(a, row0, part0, from, s);
+    __syncthreads();
+    if (s.hits <= kHits && s.count <= kList) return true;
+  }
+  return false;
+}
+
 template <typename T, int R, int THREADS, int VALUES>
 __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant__ SelectArgs a) {
   __shared__ JoinShared s;
@@ -706,52 +786,20 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
   for (int k = 0; k < kValues; ++k) {
     if (!(best + s.off(best) >= from)) break;
     if (!(value[k] + s.off(value[k]) >= from)) continue;
-    if (k == kValues - 1) {
+    if (k == kValues - 1)
       s.add(value[k], threadIdx.x, (uint32_t)~c.end);
-      continue;
-    }
-    s.reaches[beam[k]] = true;
-    const int at = atomicAdd(&s.hits, 1);
-    if (at >= kHits) continue;
-    s.hit[at] = beam[k] << 16 | ((int)threadIdx.x + k * THREADS);
+    else
+      s.note(beam[k], threadIdx.x + k * THREADS);
   }
   __syncthreads();
-  const int hits = s.hits;
-  if (hits <= kHits) {
-    // The groups' elements, a thread's of a chunk each.
-    const int log_width = kLogThreads - a.log_groups;
-    const int units = (hits * a.longest) << log_width;
-    for (int u = threadIdx.x; u < units; u += THREADS) {
-      const int pair = u >> log_width, h = a.by_longest.divide(pair);
-      const int hit = s.hit[h], b = hit >> 16, in = hit & 0xffff;
-      const int part = in >> a.log_groups, group = in - (part << a.log_groups);
-      // What the group has of the row.
-      const int row = row0 + b, begin = row * a.chunks;
-      int first = begin, last = begin + a.chunks;
-      if (!a.whole_rows) {
-        first = max(first, a.first_chunk(part0 + part - row));
-        last = min(last, a.first_chunk(part0 + part - row + 1));
-      }
-      const int chunk = first + pair - h * a.longest;
-      if (chunk >= last) continue;
-      const Row<T, R> whole = {static_cast<const T*>(c.logits) + (size_t)row * c.ld, a.vocab};
-      // From which logit on a total may reach the bound: well below it.
-      const float least = from - s.near[b];
-      const bool plain = fabsf(s.near[b]) < kHuge && fabsf(least) < kHuge;
-      whole.each((group << log_width) + (u & ((1 << log_width) - 1)), chunk - begin,
-               plain ? least - 4.f * s.off(fabsf(from) + fabsf(least)) : kLeast,
-               [&](float x, int token) {
-                 const float t = s.nearly(b, x);
-                 if (t + s.off(t) >= from) s.add(s.sum(b, x), b, key_of(x, token));
-               });
-    }
-  }
+  collect<T, R, THREADS>(a, row0, part0, from, s);
   __syncthreads();
-  int found = s.count;
-  if (hits > kHits || found > kList) {
+  if ((s.hits > kHits || s.count > kList) &&
+      !narrow<T, R, THREADS>(a, row0, part0, listed, from, s)) {
     pick_exactly<T, R, THREADS>(a, item, s);
     return;
   }
+  int found = s.count;
   if (found > kRanked && found > 2 * a.picks) {
     // Of too many those whose totals' upper words reach the n-th best one's.
     constexpr int kOwn = kList / THREADS;
@@ -797,9 +845,7 @@ __global__ void __launch_bounds__(THREADS, 1) join_kernel(const __grid_constant_
 #pragma unroll
     for (int m = 4; m > 0; m >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, m);
     if (there && eighth == 0 && rank < a.picks) {
-      const double d =
-          __longlong_as_double((long long)(total >> 63 ? total & ~(1ull << 63) : ~total));
-      put_pick(a, s, item, rank, true, d, b, key);
+      put_pick(a, s, item, rank, true, unordered(total), b, key);
     }
   }
   for (int i = found + threadIdx.x; i < a.picks; i += THREADS)
