@@ -37,6 +37,18 @@ __device__ __forceinline__ float combine(float a, float b) {
   return MAX ? fmaxf(a, b) : a + b;
 }
 
+// Over a warp, the same value in each lane. Maxima are of magnitudes, ordered as their bits.
+template <bool MAX>
+__device__ __forceinline__ float warp_all(float v) {
+  if constexpr (MAX) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+  } else {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+  }
+}
+
 // Over the CTA's threads, the same value in each; `red` is free again afterwards.
 template <bool MAX>
 __device__ float block_all(float v, float* red) {
@@ -99,14 +111,55 @@ __device__ __forceinline__ Pack<T, E> narrow(const float (&v)[E]) {
   return p;
 }
 
+// Two fp32 operations in one instruction, and the elements of an access two at a time (the
+// 8-bit output and the gradient issue in three of four cycles: 4096 rows of 7168, 8 bits, a scale
+// a row 36.5 -> 33.2 us, the gradient 43.9 -> 43.0).
+typedef unsigned long long u64;
+__device__ __forceinline__ u64 pair(float lo, float hi) {
+  return (u64)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ float low(u64 p) { return __uint_as_float((uint32_t)p); }
+__device__ __forceinline__ float high(u64 p) { return __uint_as_float((uint32_t)(p >> 32)); }
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+template <typename T, int E>
+__device__ __forceinline__ void widen_pairs(const Pack<T, E>& p, u64 (&v)[E / 2]) {
+  float f[E];
+  widen(p, f);
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) v[i] = pair(f[2 * i], f[2 * i + 1]);
+}
+
 // x + residual, rounded.
 template <typename T, int E>
 __device__ __forceinline__ Pack<T, E> added(const Pack<T, E>& x, const Pack<T, E>& residual) {
   float a[E], b[E];
   widen(x, a);
   widen(residual, b);
+  if constexpr (E % 2 == 0) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) a[e] += b[e];
+    for (int e = 0; e < E; e += 2) {
+      const u64 sum = add2(pair(a[e], a[e + 1]), pair(b[e], b[e + 1]));
+      a[e] = low(sum);
+      a[e + 1] = high(sum);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] += b[e];
+  }
   return narrow<T, E>(a);
 }
 
@@ -131,17 +184,13 @@ struct Place {
 // is free again after the group's next barrier.
 template <bool MAX>
 __device__ __forceinline__ float group_all(float v, float* red, const Place& at) {
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) v = combine<MAX>(v, __shfl_xor_sync(0xffffffffu, v, m));
+  v = warp_all<MAX>(v);
   if (at.step == 32) return v;
   const int lane = threadIdx.x & 31, warps = at.step / 32;
   float* mine = red + at.sub * warps;
   if (lane == 0) mine[at.first >> 5] = v;
   at.sync();
-  v = lane < warps ? mine[lane] : 0.f;
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) v = combine<MAX>(v, __shfl_xor_sync(0xffffffffu, v, m));
-  return v;
+  return warp_all<MAX>(lane < warps ? mine[lane] : 0.f);
 }
 
 template <typename T, int E, int A>
@@ -263,42 +312,67 @@ __device__ __forceinline__ void store_e4m3(const RowsArgs& a, size_t n, bool the
     if constexpr (E == 1) {
       q.v[0] = to_e4m3(y[j][0] * inverse);
     } else {
+      uint16_t w[E / 2];
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
-        const uint16_t w = to_e4m3x2(y[j][e] * inverse, y[j][e + 1] * inverse);
-        q.v[e] = (uint8_t)w;
-        q.v[e + 1] = (uint8_t)(w >> 8);
+        const u64 x = mul2(pair(y[j][e], y[j][e + 1]), pair(inverse, inverse));
+        w[e / 2] = to_e4m3x2(low(x), high(x));
       }
+      memcpy(&q, w, E);
     }
     const int i = at.first + j * at.step;
     if (i < accesses) reinterpret_cast<Pack<uint8_t, E>*>(out)[i] = q;
   }
 }
 
-// From the squares of a row's sum to its outputs. `red`: two arrays for group_all.
-template <typename T, int E, int A, bool QUANT>
+// From the squares of a row's sum to its outputs (SUM: it is one of them). `red`: two arrays
+// for group_all.
+template <typename T, int E, int A, bool QUANT, bool SUM>
 __device__ __forceinline__ void finish_row(const RowsArgs& a, Pack<T, E> (&s)[A],
                                            const Pack<T, E> (&gain)[A], size_t n, bool there,
                                            const Place& at, float (&red)[2][32]) {
   const NormCall& c = a.c;
   float squares = 0.f;
+  if constexpr (E % 2 == 0) {
+    u64 sums = 0;
 #pragma unroll
-  for (int j = 0; j < A; ++j) {
-    float v[E];
-    widen(s[j], v);
+    for (int j = 0; j < A; ++j) {
+      u64 v[E / 2];
+      widen_pairs(s[j], v);
 #pragma unroll
-    for (int e = 0; e < E; ++e) squares += v[e] * v[e];
+      for (int i = 0; i < E / 2; ++i) sums = fma2(v[i], v[i], sums);
+    }
+    squares = low(sums) + high(sums);
+  } else {
+#pragma unroll
+    for (int j = 0; j < A; ++j) {
+      float v[E];
+      widen(s[j], v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) squares += v[e] * v[e];
+    }
   }
   const float rstd = rsqrtf(group_all<false>(squares, red[0], at) / (float)a.K + c.eps);
   if (there && c.rstd && at.first == 0) c.rstd[n] = rstd;
+  if (SUM && c.sum.p) store_row(s, c.sum, n, at, a.K / E);
   float y[A][E];
 #pragma unroll
   for (int j = 0; j < A; ++j) {
     float g[E];
     widen(s[j], y[j]);
     widen(gain[j], g);
+    if constexpr (E % 2 == 0) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[j][e] = y[j][e] * rstd * g[e];
+      for (int e = 0; e < E; e += 2) {
+        const u64 x = mul2(mul2(pair(y[j][e], y[j][e + 1]), pair(rstd, rstd)),
+                           pair(g[e], g[e + 1]));
+        y[j][e] = low(x);
+        y[j][e + 1] = high(x);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[j][e] = y[j][e] * rstd * g[e];
+    }
   }
   if constexpr (QUANT) {
     store_e4m3<E, A>(a, n, there, at, red[1], y);
@@ -333,7 +407,7 @@ __global__ void __launch_bounds__(kMostThreads) rows_kernel(const __grid_constan
     load_row(g, Rows{c.gain, 0}, 0, at, accesses);
     if (c.sum.p) store_row(s, c.sum, n, at, accesses);
   }
-  finish_row<T, E, A, QUANT>(a, s, g, n, there, at, red);
+  finish_row<T, E, A, QUANT, false>(a, s, g, n, there, at, red);
 }
 
 // Every stride-th row per group, S rows of each thread (this one's among them) in the ring.
@@ -381,8 +455,11 @@ __global__ void __launch_bounds__(kMostThreads)
         memset(&s[j], 0, 16);
       }
     }
-    if (c.sum.p) store_row(s, c.sum, n, at, accesses);
-    finish_row<T, E, A, QUANT>(a, s, g, n, true, at, red[turn]);
+    // The sum is stored just before the output: both streams of stores are where few loads are
+    // (8192 rows of 7168: 74 us stored here, 70 us there; in 8 bits, where the output comes late,
+    // it is the other way about, 18.5 and 19.0 us for 2048 rows).
+    if (QUANT && c.sum.p) store_row(s, c.sum, n, at, accesses);
+    finish_row<T, E, A, QUANT, !QUANT>(a, s, g, n, true, at, red[turn]);
     turn ^= 1;
     if (++stage == S) stage = 0;
   }
@@ -463,17 +540,35 @@ struct GradArgs {
 template <typename T, int E, bool GAIN>
 __device__ __forceinline__ float add_products(const Pack<T, E>& s, const Pack<T, E>& up,
                                               const Pack<T, E>& gain, float rstd, float (&acc)[E]) {
-  float v[E], u[E], g[E], inner = 0.f;
-  widen(s, v);
-  widen(up, u);
-  widen(gain, g);
+  if constexpr (E % 2 == 0) {
+    u64 v[E / 2], u[E / 2], g[E / 2], inner = 0;
+    widen_pairs(s, v);
+    widen_pairs(up, u);
+    widen_pairs(gain, g);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float t = u[e] * v[e];
-    inner += t * g[e];
-    if (GAIN) acc[e] += t * rstd;
+    for (int i = 0; i < E / 2; ++i) {
+      const u64 t = mul2(u[i], v[i]);
+      inner = fma2(t, g[i], inner);
+      if (GAIN) {
+        const u64 sum = fma2(t, pair(rstd, rstd), pair(acc[2 * i], acc[2 * i + 1]));
+        acc[2 * i] = low(sum);
+        acc[2 * i + 1] = high(sum);
+      }
+    }
+    return low(inner) + high(inner);
+  } else {
+    float v[E], u[E], g[E], inner = 0.f;
+    widen(s, v);
+    widen(up, u);
+    widen(gain, g);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float t = u[e] * v[e];
+      inner += t * g[e];
+      if (GAIN) acc[e] += t * rstd;
+    }
+    return inner;
   }
-  return inner;
 }
 
 // grad_x of an access; inner: the row's mean of d * s, times rstd^3.
@@ -486,8 +581,19 @@ __device__ __forceinline__ Pack<T, E> grad_of_access(const Pack<T, E>& s, const 
   widen(up, u);
   widen(more, m);
   widen(gain, g);
+  if constexpr (E % 2 == 0) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = rstd * (u[e] * g[e]) - v[e] * inner + m[e];
+    for (int e = 0; e < E; e += 2) {
+      const u64 rest = fma2(pair(v[e], v[e + 1]), pair(-inner, -inner), pair(m[e], m[e + 1]));
+      const u64 d = mul2(pair(u[e], u[e + 1]), pair(g[e], g[e + 1]));
+      const u64 x = fma2(d, pair(rstd, rstd), rest);
+      v[e] = low(x);
+      v[e + 1] = high(x);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = rstd * (u[e] * g[e]) - v[e] * inner + m[e];
+  }
   return narrow<T, E>(v);
 }
 
