@@ -1252,21 +1252,25 @@ def run_fused_only(args):
     return 0
 
 
-def run_vocab_only(args):
-    """The vocabulary operators on the cases of perf/operators.py, one JSON line
-    per case: us per call of a loop over three sets of inputs, and the share of
-    the measured HBM and bf16 rates in the case's own bytes and operations."""
+def run_operators_only(args):
+    """The vocabulary operators on the cases of perf/operators.py (--norm-beam: the norm's
+    and the beam search's, of perf/more_operators.py), one JSON line per case: us per call of a
+    loop over three sets of inputs, and the share of the measured HBM and bf16 rates in the
+    case's own bytes and operations."""
+    import importlib
+
     import torch
 
-    from perf import operators
     from tp_vocab_logits_gb300 import _build
+    operators = importlib.import_module("perf.operators" if args.vocab else "perf.more_operators")
+    kind = "vocab" if args.vocab else "norm_beam"
     _build.build()
     torch.cuda.set_device(0)
     stream = torch.cuda.current_stream()
     pk = peaks()
     operators.own = True
     for case in operators.listed():
-        if not case["op"].startswith(args.vocab_op):
+        if args.vocab and not case["op"].startswith(args.vocab_op):
             continue
         states = [operators.prepare(case, SEED + k) for k in range(3)]
         fns = [lambda s=s: operators.run(s) for s in states]
@@ -1274,7 +1278,7 @@ def run_vocab_only(args):
         calls = int(min(args.calls, max(3, 1e13 / max(work["flops"], 50 * work["bytes"]))))
         t = time_calls(torch, fns, calls, 3, stream, "timed_vocab") * 1e-3 / calls
         gbs, tf = work["bytes"] / t / 1e9, work["flops"] / t / 1e12
-        print(json.dumps({"vocab": case["name"], "calls": calls, "us_per_call": round(t * 1e6, 2),
+        print(json.dumps({kind: case["name"], "calls": calls, "us_per_call": round(t * 1e6, 2),
                           "gbs": round(gbs, 1), "tflops": round(tf, 1),
                           "hbm_frac": round(gbs / pk["hbm_gbs"], 3),
                           "bf16_frac": round(tf / pk["bf16_tflops"], 3)}), flush=True)
@@ -1302,6 +1306,8 @@ def main(argv=None):
     ap.add_argument("--vocab", action="store_true",
                     help="embedding, loss and their gradients only, one line per case")
     ap.add_argument("--vocab-op", default="", help="--vocab: operators whose name starts so")
+    ap.add_argument("--norm-beam", action="store_true",
+                    help="norm and beam search operators only, one line per case")
     ap.add_argument("--timeline", action="store_true",
                     help="launch timeline of graph-replayed gathers (TP8, V=163840), one line "
                          "per M")
@@ -1338,8 +1344,8 @@ def main(argv=None):
         return run_fused_only(args)
     if args.stats:
         return run_stats_only(args)
-    if args.vocab:
-        return run_vocab_only(args)
+    if args.vocab or args.norm_beam:
+        return run_operators_only(args)
     if args.timeline:
         return run_timeline(args)
     if args.fused_timeline:
