@@ -247,6 +247,50 @@ def test_other_streams():
     other.close()
 
 
+def test_calls_of_one_handle_that_overlap():
+    """Those that need no workspace, on two streams at once."""
+    g = gen_of(6)
+    h, hb = hg.hg_norm_create(1024, 4000), hg.hg_beam_create(4, 8, 100, 8)
+    x, gain = normal(g, (2, 4000, 1024)), normal(g, (1024,))
+    out, want = torch.empty_like(x), torch.empty_like(x)
+    state = normal(g, (2, 32, 5000))
+    parents = torch.randint(0, 8, (2, 4, 8), generator=g, device="cuda")
+    moved = [want_states([(state[k], 0)], parents[k])[0] for k in range(2)]
+    for k in range(2):
+        hg.hg_norm_rows(h, x[k], gain, want[k])
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        for k in range(2):
+            hg.hg_norm_rows(h, x[k], gain, out[k], stream=streams[k])
+    for k in range(2):
+        hg.hg_beam_reorder(hb, parents[k], [state[k]], stream=streams[k])
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and all(torch.equal(state[k], moved[k]) for k in range(2))
+    h.close()
+    hb.close()
+
+
+@pytest.mark.parametrize("states", [1, 33, 256])
+def test_many_states_in_a_captured_call(states):
+    """More states than a launch takes, of many layouts, captured and replayed."""
+    g = gen_of(states)
+    hb = hg.hg_beam_create(2, 3, 100, 3)
+    parents = torch.tensor([[2, 0, 0], [1, 1, 7]], device="cuda")
+    kept = [(normal(g, (6, 3 + k % 5, 16)), 0) if k % 2 else (normal(g, (2, 6, 40))[:, :, :31], 1)
+            for k in range(states)]
+    first = [t.clone() for t, _ in kept]
+    want = want_states(kept, parents)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hg.hg_beam_reorder(hb, parents, kept)
+    assert same([t for t, _ in kept], first)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert same([t for t, _ in kept], want)
+    hb.close()
+
+
 # ---- training ----------------------------------------------------------------------
 
 
