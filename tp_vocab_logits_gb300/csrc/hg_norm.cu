@@ -910,7 +910,7 @@ cudaError_t rows_as(const hg_norm& h, RowsArgs& a, cudaStream_t stream) {
 }
 
 // Rows in the ring and threads of an SM. Plain rows run at the copy rate with one group of
-// 448 threads (8192 rows of 7168 bf16: 70-74 us, 79 with two groups); the 8-bit output's
+// 448 threads (8192 rows of 7168 bf16: 70 us, 79 with two groups); the 8-bit output's
 // second round of maxima wants two (2048 rows: 25 and 19 us), and so does the gradient
 // (4096 rows: 62 and 44 us).
 constexpr int kStages = 3, kStagesQuant = 2;
