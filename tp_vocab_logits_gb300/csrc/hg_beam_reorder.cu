@@ -28,6 +28,7 @@ typedef unsigned long long u64;
 constexpr int kMoveThreads = 128;
 constexpr int kColumns = 2;      // of a thread at a time
 constexpr int kStates = 32;     // states of one launch
+constexpr size_t kNarrowMost = 1 << 20;  // bytes of rows in short accesses beside 16-byte ones
 constexpr size_t kMoveMost = 136 * 1024;  // shared memory of a CTA's columns
 static_assert((size_t)2 * HG_MAX_BEAMS * kColumns * 32 * 16 <= kMoveMost, "at least a warp");
 constexpr size_t kSharedOfSm = 228 * 1024;
@@ -152,36 +153,52 @@ struct Cursor {
 };
 
 template <int BYTES>
-__device__ __forceinline__ void copy_ahead(uint4* to, const void* from) {
+__device__ __forceinline__ void copy_ahead(void* to, const void* from) {
   const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
   if constexpr (BYTES == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
-  else if constexpr (BYTES == 4)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(from) : "memory");
-  else if constexpr (BYTES == 2)  // too short to be copied ahead
-    *reinterpret_cast<uint16_t*>(to) = *static_cast<const uint16_t*>(from);
   else
-    *reinterpret_cast<unsigned char*>(to) = *static_cast<const unsigned char*>(from);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(from) : "memory");
 }
 
-template <int BYTES>
-__device__ __forceinline__ void read_as(const Columns& c, const Moves& m, uint4* held) {
+// W: an access. SLOT: a column's place in shared memory. Those too short to be copied ahead are loaded for a few rows at a time.
+template <typename W, typename SLOT>
+__device__ __forceinline__ void read_as(const Columns& c, const Moves& m, SLOT* held) {
   const int n = m.reads;
-  for (int r = 0; r < n; ++r) {
-    const u64 from = m.from[r];
+  if constexpr (sizeof(W) >= 4) {
+    for (int r = 0; r < n; ++r) {
+      const u64 from = m.from[r];
 #pragma unroll
-    for (int k = 0; k < kColumns; ++k)
-      if (c.at[k]) copy_ahead<BYTES>(held + (r * kColumns + k) * blockDim.x, c.at[k] + from);
+      for (int k = 0; k < kColumns; ++k)
+        if (c.at[k])
+          copy_ahead<sizeof(W)>(held + (r * kColumns + k) * blockDim.x, c.at[k] + from);
+    }
+  } else {
+    constexpr int kRows = 8;
+    for (int r0 = 0; r0 < n; r0 += kRows) {
+      W v[kRows][kColumns];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int k = 0; k < kColumns; ++k)
+          if (r0 + r < n && c.at[k]) v[r][k] = *reinterpret_cast<const W*>(c.at[k] + m.from[r0 + r]);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int k = 0; k < kColumns; ++k)
+          if (r0 + r < n && c.at[k])
+            *reinterpret_cast<W*>(held + ((r0 + r) * kColumns + k) * blockDim.x) = v[r][k];
+    }
   }
 }
 
-template <typename W>
-__device__ __forceinline__ void write_as(const Columns& c, const Moves& m, const uint4* held) {
+template <typename W, typename SLOT>
+__device__ __forceinline__ void write_as(const Columns& c, const Moves& m, const SLOT* held) {
   const int n = m.writes;
 #pragma unroll 2
   for (int w = 0; w < n; ++w) {
     const u64 to = m.to[w];
-    const uint4* from = held + m.place[w] * kColumns * blockDim.x;
+    const SLOT* from = held + m.place[w] * kColumns * blockDim.x;
     W v[kColumns];
 #pragma unroll
     for (int k = 0; k < kColumns; ++k) v[k] = *reinterpret_cast<const W*>(from + k * blockDim.x);
@@ -191,21 +208,22 @@ __device__ __forceinline__ void write_as(const Columns& c, const Moves& m, const
   }
 }
 
-__device__ __forceinline__ void read(const Columns& c, const Moves& m, uint4* held) {
-  if (c.bytes == 16)
-    read_as<16>(c, m, held);
-  else if (c.bytes == 4)
-    read_as<4>(c, m, held);
+template <typename SLOT>
+__device__ __forceinline__ void read(const Columns& c, const Moves& m, SLOT* held) {
+  if constexpr (sizeof(SLOT) == 16)
+    if (c.bytes == 16) return read_as<uint4>(c, m, held);
+  if (c.bytes == 4)
+    read_as<uint32_t>(c, m, held);
   else if (c.bytes == 2)
-    read_as<2>(c, m, held);
+    read_as<uint16_t>(c, m, held);
   else
-    read_as<1>(c, m, held);
+    read_as<unsigned char>(c, m, held);
 }
-
-__device__ __forceinline__ void write(const Columns& c, const Moves& m, const uint4* held) {
-  if (c.bytes == 16)
-    write_as<uint4>(c, m, held);
-  else if (c.bytes == 4)
+template <typename SLOT>
+__device__ __forceinline__ void write(const Columns& c, const Moves& m, const SLOT* held) {
+  if constexpr (sizeof(SLOT) == 16)
+    if (c.bytes == 16) return write_as<uint4>(c, m, held);
+  if (c.bytes == 4)
     write_as<uint32_t>(c, m, held);
   else if (c.bytes == 2)
     write_as<uint16_t>(c, m, held);
@@ -213,15 +231,18 @@ __device__ __forceinline__ void write(const Columns& c, const Moves& m, const ui
     write_as<unsigned char>(c, m, held);
 }
 
+// SLOT of 32 bits: of accesses of 4 bytes and less, which leave most of 16 bytes unused and with
+// them the room for threads (9 items of 28 beams, 85 MB in 2-byte accesses: 669 and 50 us).
+template <typename SLOT>
 __global__ void __launch_bounds__(kMoveThreads)
     reorder_kernel(const __grid_constant__ ReorderArgs a) {
-  extern __shared__ uint4 smem[];  // [2][beams][kColumns][threads]
+  extern __shared__ uint4 smem[];  // [2][beams][kColumns][threads] of SLOT
   __shared__ Moves lists[kMoveThreads / 32][2];  // of this unit and of the next
   wait_for_predecessor();
   let_successor_start();
   Moves* const moves = lists[threadIdx.x >> 5];
-  uint4* const held[2] = {smem + threadIdx.x,
-                          smem + threadIdx.x + a.beams * kColumns * blockDim.x};
+  SLOT* const slots = reinterpret_cast<SLOT*>(smem) + threadIdx.x;
+  SLOT* const held[2] = {slots, slots + a.beams * kColumns * blockDim.x};
   const u64 cta = blockIdx.x;
   u64 unit = cta * a.each + min(cta, a.more);
   const u64 last = unit + a.each + (cta < a.more ? 1 : 0) - 1;
@@ -234,8 +255,11 @@ __global__ void __launch_bounds__(kMoveThreads)
     Columns next = columns;
     if (unit < last) {
       cursor.step(a, unit + 1, moves);
-      next = cursor.columns(a);
-      read(next, moves[next.moves], held[side ^ 1]);
+      next.moves = cursor.list;
+      if (moves[cursor.list].writes > 0) {
+        next = cursor.columns(a);
+        read(next, moves[next.moves], held[side ^ 1]);
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -247,29 +271,41 @@ __global__ void __launch_bounds__(kMoveThreads)
 
 }  // namespace
 
-cudaError_t reorder(const hg_beam& h, const void* parents, int id_bytes, int items,
-                    const hg_beam_state* states, int n_states, cudaStream_t stream) {
+namespace {
+
+// Bytes of a state's accesses; 0: there is nothing in it.
+int access_of(const hg_beam_state& s) {
+  if (s.outer == 0 || s.pieces == 0 || s.piece_bytes == 0) return 0;
+  size_t bits = reinterpret_cast<uintptr_t>(s.data) | s.piece_bytes | s.row_stride;
+  if (s.outer > 1) bits |= s.outer_stride;
+  if (s.pieces > 1) bits |= s.piece_stride;
+  return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+}
+
+// The states whose accesses are of `least` to `widest` bytes, 32 a launch.
+template <typename SLOT>
+cudaError_t reorder_as(int least, int widest, const hg_beam& h, const void* parents, int id_bytes, int items,
+                       const hg_beam_state* states, int n_states, cudaStream_t stream) {
   // As many threads as the shared memory of their columns allows, and CTAs to fill an SM.
   int threads = kMoveThreads;
-  while ((size_t)2 * h.beams * kColumns * threads * 16 > kMoveMost) threads /= 2;
-  const size_t smem = (size_t)2 * h.beams * kColumns * threads * 16;
-  const u64 per_sm = kSharedOfSm / (smem + sizeof(Moves) * 2 * kMoveThreads / 32 + 1024);
+  while ((size_t)2 * h.beams * kColumns * threads * sizeof(SLOT) > kMoveMost) threads /= 2;
+  const size_t smem = (size_t)2 * h.beams * kColumns * threads * sizeof(SLOT);
+  const u64 room = kSharedOfSm / (smem + sizeof(Moves) * 2 * kMoveThreads / 32 + 1024);
+  const u64 per_sm = room < (u64)(2048 / threads) ? room : (u64)(2048 / threads);
   for (int next = 0; next < n_states;) {
     ReorderArgs a = {};
     a.parents = Ids{parents, id_bytes};
     a.beams = h.beams;
     for (; next < n_states && a.n_states < kStates; ++next) {
       const hg_beam_state& in = states[next];
-      if (in.outer == 0 || in.pieces == 0 || in.piece_bytes == 0) continue;
+      const int bytes = access_of(in);
+      if (bytes < least || bytes > widest) continue;
       State& s = a.state[a.n_states];
       s.data = static_cast<unsigned char*>(in.data);
       s.outer_stride = in.outer_stride;
       s.row_stride = in.row_stride;
       s.piece_stride = in.piece_stride;
-      size_t bits = reinterpret_cast<uintptr_t>(in.data) | in.piece_bytes | in.row_stride;
-      if (in.outer > 1) bits |= in.outer_stride;
-      if (in.pieces > 1) bits |= in.piece_stride;
-      s.bytes = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+      s.bytes = bytes;
       s.pieces = in.pieces;
       s.accesses = in.piece_bytes / s.bytes;
       s.columns = in.outer * in.pieces * s.accesses;
@@ -288,15 +324,42 @@ cudaError_t reorder(const hg_beam& h, const void* parents, int id_bytes, int ite
     a.each = a.units / grid;
     a.more = a.units % grid;
     const cudaError_t e =
-        launch_dependent(reorder_kernel, a, grid, (unsigned)threads, smem, 1, stream);
+        launch_dependent(reorder_kernel<SLOT>, a, grid, (unsigned)threads, smem, 1, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
+}  // namespace
+
+cudaError_t reorder(const hg_beam& h, const void* parents, int id_bytes, int items,
+                    const hg_beam_state* states, int n_states, cudaStream_t stream) {
+  if (h.beams == 1) return cudaSuccess;  // no row has another to take
+  // Short accesses have a launch of their own where they are many, or alone: it takes 1.5 us.
+  size_t narrow = 0;
+  bool wide = false;
+  for (int i = 0; i < n_states; ++i) {
+    const hg_beam_state& s = states[i];
+    const int bytes = access_of(s);
+    if (bytes == 16) wide = true;
+    if (bytes > 0 && bytes < 16) narrow += s.outer * s.pieces * s.piece_bytes * items * h.beams;
+  }
+  const int least = !wide || narrow > kNarrowMost ? 16 : 1;
+  const cudaError_t e =
+      wide ? reorder_as<uint4>(least, 16, h, parents, id_bytes, items, states, n_states, stream)
+           : cudaSuccess;
+  return e == cudaSuccess && least == 16 && narrow > 0
+             ? reorder_as<uint32_t>(1, 4, h, parents, id_bytes, items, states, n_states, stream)
+             : e;
+}
+
 cudaError_t reorder_prepare() {
-  return cudaFuncSetAttribute(reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)kMoveMost);
+  const cudaError_t e = cudaFuncSetAttribute(
+      reorder_kernel<uint4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMoveMost);
+  return e == cudaSuccess ? cudaFuncSetAttribute(reorder_kernel<uint32_t>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)kMoveMost)
+                          : e;
 }
 
 }  // namespace beam
