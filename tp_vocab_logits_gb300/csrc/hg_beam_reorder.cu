@@ -7,7 +7,7 @@
 // places in shared memory, are under way while it writes these, and a CTA goes through
 // neighbouring columns. Memory bounds it, once the instructions do not: a warp lists an
 // item's rows when it comes to it, and a thread moves two columns by that list (32 items
-// of 8 beams, 1.49 GB read and written: 246 us, 6.1 TB/s; 284 us with the rows looked up for
+// of 8 beams, 1.49 GB read and written: 243 us, 6.1 TB/s; 284 us with the rows looked up for
 // each column, 289 us with four columns a thread, which leaves too few warps).
 
 #include "hg_beam.cuh"
