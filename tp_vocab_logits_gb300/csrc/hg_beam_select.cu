@@ -535,12 +535,16 @@ struct RowStats {
   }
 };
 
+// Over the CTA's threads, the same value in each. One barrier orders a call's writes before its
+// reads; the next call writes while others may still read this one's, so `turn`, which has to
+// be another than the call before had, says which of two places is used.
 template <int WARPS>
 __device__ __forceinline__ int count_all(int c, int turn, JoinShared& s) {
   c = __reduce_add_sync(0xffffffffu, c);
   if ((threadIdx.x & 31) == 0) s.warp_count[turn][threadIdx.x >> 5] = c;
   __syncthreads();
-  return __reduce_add_sync(0xffffffffu, (threadIdx.x & 31) < WARPS ? s.warp_count[turn][threadIdx.x & 31] : 0);
+  const int lane = threadIdx.x & 31;
+  return __reduce_add_sync(0xffffffffu, lane < WARPS ? s.warp_count[turn][lane] : 0);
 }
 
 // Where too many candidates are alike for the list: the best of each row that has some,
@@ -552,6 +556,7 @@ __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinSha
   const int thread = threadIdx.x % kThreads, first = threadIdx.x / kThreads;
   constexpr int kStep = THREADS / kThreads;
   const int row0 = item * a.beams, n = a.picks;
+  int turn = 0;
   for (int b = 0; b < a.beams; ++b) {
     u64* list = a.list + (size_t)(row0 + b) * n;
     for (int i = threadIdx.x; i < n; i += THREADS) list[i] = 0;
@@ -570,7 +575,7 @@ __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinSha
       int c = 0;
       for (int i = first; i < a.chunks; i += kStep)
         one.each(thread, i, kLeast, [&](float x, int token) { c += key_of(x, token) >= next; });
-      c = count_all<THREADS / 32>(c, bit & 1, s);
+      c = count_all<THREADS / 32>(c, turn ^= 1, s);  // not the bit's parity: bits are skipped
       if (c >= n) bound = next;
       if (c == n) break;
     }
