@@ -684,10 +684,10 @@ __global__ void __launch_bounds__(kMostThreads) grad_kernel(const __grid_constan
   if (GAIN) store_partial<E, A>(a, acc, at);
 }
 
-constexpr int kFewColumns = 64;  // of a CTA, four groups of threads taking every fourth row
+constexpr int kFewColumns = 64;  // of a CTA, 4 to 16 groups of threads taking every so many'th row
 
-// Few rows in one launch: the first N CTAs make grad_x, a row each; the others grad_gain,
-// which needs no sum over a row, from the rows as they lie (so grad_x is not grad_out).
+// Few rows in one launch: the first N CTAs make grad_x, if it is wanted, a row each; the others
+// grad_gain, which needs no sum over a row, from the rows as they lie (so grad_x is not grad_out).
 template <typename T, int E>
 __global__ void __launch_bounds__(kMostThreads) few_kernel(const __grid_constant__ GradArgs a) {
   __shared__ float red[32];
@@ -695,7 +695,8 @@ __global__ void __launch_bounds__(kMostThreads) few_kernel(const __grid_constant
   wait_for_predecessor();
   let_successor_start();
   const GradCall& c = a.c;
-  if ((int)blockIdx.x < c.N) {
+  const int of_x = c.grad_x.p ? c.N : 0;
+  if ((int)blockIdx.x < of_x) {
     const Place at(a.shape);
     if ((int)threadIdx.x >= at.step) return;
     Pack<T, E> g[1];
@@ -706,7 +707,7 @@ __global__ void __launch_bounds__(kMostThreads) few_kernel(const __grid_constant
     return;
   }
   const int column = threadIdx.x % kFewColumns, sub = threadIdx.x / kFewColumns;
-  const int subs = blockDim.x / kFewColumns, k = (blockIdx.x - c.N) * kFewColumns + column;
+  const int subs = blockDim.x / kFewColumns, k = (blockIdx.x - of_x) * kFewColumns + column;
   float v = 0.f;
   if (k < a.K && sub < subs)
 #pragma unroll 4
@@ -1003,17 +1004,24 @@ cudaError_t grad_stream(const hg_norm& h, GradArgs& a, cudaStream_t stream) {
 constexpr int kFewRows = 64;
 
 // Few rows take one launch, or few accesses a thread, as their latency counts; many rows
-// in 16-byte accesses are streamed; others take A or twice as many accesses a thread.
+// in 16-byte accesses are streamed; others take A or twice as many accesses a thread. Whether
+// grad_x is wanted, and over grad_out, changes nothing in the order of grad_gain's sum: of few
+// rows grad_x is then made by a launch behind it.
 template <typename T, int E, int A>
 cudaError_t grad_by(const hg_norm& h, GradArgs& a, cudaStream_t stream) {
   const GradCall& c = a.c;
   const int accesses = a.K / E;
-  if (c.N > 0 && c.N <= kFewRows && accesses <= kMostThreads && c.grad_gain && c.grad_x.p &&
-      c.grad_x.p != c.grad_out.p) {
-    a.shape = {(int)round_up(accesses, 32), 1};
-    const unsigned block = a.shape.threads < 256 ? 256u : (unsigned)round_up(a.shape.threads, 64);
-    return launch_dependent(few_kernel<T, E>, a, (unsigned)(c.N + div_up(a.K, kFewColumns)), block,
-                            0, 1, stream);
+  if (c.N > 0 && c.N <= kFewRows && accesses <= kMostThreads && c.grad_gain) {
+    const bool in_place = c.grad_x.p && c.grad_x.p == c.grad_out.p;
+    GradArgs few = a;
+    if (in_place) few.c.grad_x = {};
+    few.shape = {(int)round_up(accesses, 32), 1};
+    const unsigned block =
+        few.shape.threads < 256 ? 256u : (unsigned)round_up(few.shape.threads, 64);
+    const unsigned grid = (unsigned)((few.c.grad_x.p ? c.N : 0) + div_up(a.K, kFewColumns));
+    const cudaError_t e = launch_dependent(few_kernel<T, E>, few, grid, block, 0, 1, stream);
+    if (e != cudaSuccess || !in_place) return e;
+    a.c.grad_gain = nullptr;
   }
   if (c.N <= h.sms && accesses <= kMostThreads) return grad_as<T, E, 1>(h, a, stream);
   if constexpr (E * sizeof(T) == 16) {
