@@ -624,7 +624,8 @@ int hg_vocab_loss_grad(hg_vocab *h, const void *hidden, size_t ld_hidden,
  * of that device, the same inputs give the same bits). The gradients of one handle share
  * its workspace: they, and graphs that hold them, run one after another. Calls of hg_norm_rows
  * need none and may overlap. No output overlaps an input or another output, but where that
- * is allowed below. Where all pointers and row distances are 16-byte (or 4-byte) aligned,
+ * is allowed below: other overlaps are refused (HG_ERR_ARG), but for scales over the gain, which
+ * is not looked for. Columns of one wider matrix do not overlap. Where all pointers and row distances are 16-byte (or 4-byte) aligned,
  * rows move in such words.
  */
 typedef struct hg_norm hg_norm;
@@ -763,7 +764,7 @@ size_t hg_beam_workspace_bytes(const hg_beam *h);
  * scores, finished and reordering (tokens, hg_vocab_embed's input); with picks = 2 * beams
  * there are beams of them that do not end. Where fewer candidates are left, the last
  * picks have token and parent -1, total -inf and are not finished. No output overlaps an
- * input or another output. An item with more than 1000 equal candidates at the last pick
+ * input or another output: refused, but for outputs over lse, which are not looked for. An item with more than 1000 equal candidates at the last pick
  * (a row of zeros, say) takes a path that reads its rows again for every bit of the order.
  *
  * Errors, before any device work: HG_ERR_ARG, HG_ERR_ROWS (items above max_items),
@@ -790,9 +791,10 @@ typedef struct hg_beam_state {
  *
  *   parents   items * beams signed integers of id_bytes (4 or 8) bytes: parents[item *
  *             beams + j] is a beam of the same item. One outside [0, beams)
- *             leaves its row as it is
+ *             leaves its row as it is. They lie outside the states (else refused)
  *   states    n_states records; the rows of a state and the states do not overlap (a state
- *             listed twice is refused)
+ *             listed twice is refused; states that share a part of their runs are not
+ *             looked for)
  *
  * All rows of an item take their parents' contents as they were before the call. Only
  * rows that change are written. Errors, before any device work: HG_ERR_ARG (also:

@@ -7,6 +7,7 @@
 #include <new>
 
 #include "hg_beam.cuh"
+#include "hg_overlap.cuh"
 
 namespace {
 
@@ -50,19 +51,42 @@ bool state_ok(const hg_beam_state& s, size_t rows) {
   return true;
 }
 
-// Arrays that the kernels write, the first `outs`, overlap neither each other nor the rest.
-struct Array {
-  const void* p;
-  size_t bytes;
-};
-template <int N>
-bool apart(const Array (&a)[N], int outs) {
-  for (int i = 0; i < outs; ++i)
-    for (int j = i + 1; j < N; ++j) {
-      const uintptr_t x = reinterpret_cast<uintptr_t>(a[i].p), y = reinterpret_cast<uintptr_t>(a[j].p);
-      if (a[i].p && a[j].p && x < y + a[j].bytes && y < x + a[i].bytes) return false;
+// Whether [from, to), as a distance in bytes from the state's data, holds a part of its runs. A
+// dimension of a larger stride steps over all that those of smaller ones span.
+bool state_holds(const hg_beam_state& s, size_t rows, long long from, long long to) {
+  struct Dim {
+    long long count, stride;
+  } dim[3] = {{(long long)s.outer, (long long)s.outer_stride},
+              {(long long)rows, (long long)s.row_stride},
+              {(long long)s.pieces, (long long)s.piece_stride}};
+  long long span[4] = {(long long)s.piece_bytes};
+  for (Dim& d : dim)
+    if (d.count == 1) d.stride = 0;
+  std::sort(dim, dim + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  for (int k = 0; k < 3; ++k) span[k + 1] = span[k] + dim[k].stride * (dim[k].count - 1);
+  // What `level` dimensions span, from `at` on. A part that lies inside whole holds a run; at most
+  // two of a dimension's parts lie inside in part.
+  auto inside = [&](auto& self, int level, long long at) -> bool {
+    if (at >= to || at + span[level] <= from) return false;
+    if (level == 0 || (from <= at && at + span[level] <= to)) return true;
+    const Dim& d = dim[level - 1];
+    if (d.stride == 0) return self(self, level - 1, at);
+    const long long before = from - at - span[level - 1];  // a part that begins here ends before
+    for (long long i = before < 0 ? 0 : before / d.stride + 1; i < d.count; ++i) {
+      if (at + i * d.stride >= to) return false;
+      if (self(self, level - 1, at + i * d.stride)) return true;
     }
-  return true;
+    return false;
+  };
+  return inside(inside, 3, 0);
+}
+
+// The parents lie outside the states, whose rows move while others read them.
+bool parents_ok(const void* parents, size_t bytes, const hg_beam_state& s, size_t rows) {
+  if (s.outer == 0 || s.pieces == 0 || s.piece_bytes == 0) return true;
+  const long long from =
+      (long long)(reinterpret_cast<uintptr_t>(parents) - reinterpret_cast<uintptr_t>(s.data));
+  return !state_holds(s, rows, from, from + (long long)bytes);
 }
 
 // No state is listed twice: both would be moved at once.
@@ -155,8 +179,9 @@ int hg_beam_select(hg_beam* h, const void* logits, size_t ld_logits, const float
         !aligned(picked, 4))
       return HG_ERR_ARG;
     const size_t picks = (size_t)items * h->picks;
-    if (!apart<6>({{tokens, picks * id_bytes}, {parents, picks * id_bytes}, {picked, picks * 4},
-                {picked_finished, picks}, {scores, rows * 4}, {finished, rows}}, 4))
+    if (!hg::apart<7>({{tokens, picks * id_bytes}, {parents, picks * id_bytes}, {picked, picks * 4},
+                       {picked_finished, picks}, {scores, rows * 4}, {finished, rows},
+                       {logits, rows, ld_logits * e, h->vocab * e}}, 4))
       return HG_ERR_ARG;
   }
   if (items > h->max_items) return HG_ERR_ROWS;
@@ -186,8 +211,10 @@ int hg_beam_reorder(hg_beam* h, const void* parents, int id_bytes, int items,
   if (items > 0 && !ids_ok(parents, id_bytes)) return HG_ERR_ARG;
   if (items > h->max_items) return HG_ERR_ROWS;
   if (items > 0) {
+    const size_t rows = (size_t)items * h->beams;
     for (int i = 0; i < n_states; ++i)
-      if (!state_ok(states[i], (size_t)items * h->beams)) return HG_ERR_ARG;
+      if (!state_ok(states[i], rows) || !parents_ok(parents, rows * id_bytes, states[i], rows))
+        return HG_ERR_ARG;
     if (!states_differ(states, n_states)) return HG_ERR_ARG;
   }
   const int st = check_device(h);

@@ -6,10 +6,11 @@
 #include <new>
 
 #include "hg_norm.cuh"
+#include "hg_overlap.cuh"
 
 namespace {
 
-using hg::norm::Rows;
+using hg::Block;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -19,9 +20,13 @@ bool matrix_ok(const hg_norm* h, const void* p, size_t ld, size_t elem, int N) {
                     ld <= (size_t)LLONG_MAX / 8 / (size_t)(N + 1));
 }
 
-// Where an output is an input's own rows, it is so row by row.
-bool in_place_ok(const void* out, size_t ld_out, const void* in, size_t ld_in, int N) {
-  return !out || out != in || ld_out == ld_in || N <= 1;
+Block rows_block(const hg_norm* h, const void* p, size_t ld, size_t elem, int N) {
+  return Block(p, (size_t)N, ld * elem, (size_t)h->K * elem);
+}
+
+// An output that may be an input's own rows, row by row, and overlaps them in no other way.
+bool in_place_ok(const Block& out, const Block& in) {
+  return (out.p == in.p && (out.distance == in.distance || out.rows <= 1)) || !hg::overlap(out, in);
 }
 
 int as_status(cudaError_t e) { return e == cudaSuccess ? HG_OK : HG_ERR_CUDA; }
@@ -106,13 +111,18 @@ int hg_norm_rows(hg_norm* h, const void* x, size_t ld_x, const void* residual,
   if (e4m3 ? (N > 0 && !scales) || !aligned(scales, 4) || (scale_block != 0 && scale_block != 128)
            : scales || scale_block != 0)
     return HG_ERR_ARG;
-  if (N > 0 && ((out == sum) || (e4m3 && (out == x || out == residual)) ||
-                !in_place_ok(sum, ld_sum, x, ld_x, N) ||
-                !in_place_ok(sum, ld_sum, residual, ld_residual, N) ||
-                !in_place_ok(out, ld_out, x, ld_x, N) ||
-                !in_place_ok(out, ld_out, residual, ld_residual, N)))
-    return HG_ERR_ARG;
   if (N > h->max_rows) return HG_ERR_ROWS;
+  const size_t n = N, blocks = scale_block ? (h->K + 127) / 128 : 1;
+  const Block of_x = rows_block(h, x, ld_x, e, N), of_res = rows_block(h, residual, ld_residual, e, N);
+  const Block of_sum = rows_block(h, sum, ld_sum, e, N);
+  const Block of_out = rows_block(h, out, ld_out, e4m3 ? 1 : e, N), of_rstd(rstd, n * 4);
+  const Block of_scales(scales, n * blocks * 4), of_gain(gain, h->K * e);
+  if (hg::overlap(of_sum, of_out) || !in_place_ok(of_sum, of_x) || !in_place_ok(of_sum, of_res) ||
+      (e4m3 ? hg::overlap(of_out, of_x) || hg::overlap(of_out, of_res)
+            : !in_place_ok(of_out, of_x) || !in_place_ok(of_out, of_res)) ||
+      !hg::apart<6>({of_rstd, of_scales, of_x, of_res, of_sum, of_out}, 2) ||
+      !hg::apart<4>({of_sum, of_out, of_rstd, of_gain}, 3))
+    return HG_ERR_ARG;
   const int st = check_device(h);
   if (st != HG_OK || N == 0) return st;
   hg::norm::NormCall c;
@@ -141,11 +151,15 @@ int hg_norm_rows_grad(hg_norm* h, const void* s, size_t ld_s, const void* gain, 
       (grad_x && !matrix_ok(h, grad_x, ld_grad_x, e, N)) || !gain || !aligned(gain, e) ||
       (N > 0 && (!rstd || !aligned(rstd, 4))) || !aligned(grad_gain, e) || grad_gain == gain)
     return HG_ERR_ARG;
-  if (N > 0 && grad_x &&
-      (grad_x == s || !in_place_ok(grad_x, ld_grad_x, grad_out, ld_grad_out, N) ||
-       !in_place_ok(grad_x, ld_grad_x, grad_sum, ld_grad_sum, N)))
-    return HG_ERR_ARG;
   if (N > h->max_rows) return HG_ERR_ROWS;
+  const Block of_s = rows_block(h, s, ld_s, e, N), of_x = rows_block(h, grad_x, ld_grad_x, e, N);
+  const Block of_up = rows_block(h, grad_out, ld_grad_out, e, N);
+  const Block of_more = rows_block(h, grad_sum, ld_grad_sum, e, N);
+  const Block of_rstd(rstd, (size_t)N * 4), of_gain(gain, h->K * e), of_sums(grad_gain, h->K * e);
+  if (!in_place_ok(of_x, of_up) || !in_place_ok(of_x, of_more) ||
+      !hg::apart<5>({of_x, of_sums, of_s, of_rstd, of_gain}, 2) ||
+      !hg::apart<3>({of_sums, of_up, of_more}, 1))
+    return HG_ERR_ARG;
   const int st = check_device(h);
   if (st != HG_OK || (N == 0 && (!grad_gain || accumulate))) return st;
   hg::norm::GradCall c;
