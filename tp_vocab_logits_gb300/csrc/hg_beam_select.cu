@@ -41,8 +41,8 @@ constexpr int kRounds = 4;       // of closer bounds, where there are more of ei
 constexpr int kCtasPerSm = 4;
 // Maxima that a thread of join_kernel takes. Many picks have many elements read again, of
 // groups that are finer where there are more of them (163840 logits, an item of 64 beams with 128
-// picks: 48 and 35 us; 8 items of 8 with 16: 11.9 and 14.0). Many parts need the room, or rows
-// stay whole (an item of 32 beams with 32 picks: 21 and 17).
+// picks: 48 and 35 us; 8 items of 8 with 16: 11.9 and 14.0). Many parts need the room, or a part's
+// threads share few maxima (an item of 32 beams with 32 picks: 21 and 17).
 constexpr int kFewValues = 4, kManyValues = 16;
 constexpr int kFewPicks = 32;
 constexpr int kLeastGroups = 8;    // of a part's threads, at least, that have a maximum: warps
@@ -59,7 +59,6 @@ struct SelectArgs {
   int each, more;      // chunks of a CTA; the first `more` CTAs have one more
   Divisor by_chunks, by_each, by_each_and_one, by_beams, by_longest;
   int all;             // chunks of the call
-  int whole_rows;      // CTAs have whole rows
   int longest;         // chunks of a part, at most
   int log_groups;      // groups of a CTA's threads that have a maximum each
   float* maxima;       // [part][groups]
@@ -73,7 +72,7 @@ struct SelectArgs {
   }
   // The number of what a CTA has of a row: going through the chunks, each new part raises the
   // CTA, the row, or both.
-  __device__ int part_of(int cta, int row) const { return whole_rows ? row : cta + row; }
+  __device__ int part_of(int cta, int row) const { return cta + row; }
 };
 
 // Bits of a value that is no NaN, in an order of unsigned integers; both zeros alike.
@@ -201,17 +200,6 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, __half) {
 }
 
 // The largest element that is not NaN (-inf or NaN if there is none).
-template <typename T>
-__device__ __forceinline__ float largest_of(const Access<T>& x) {
-  if constexpr (sizeof(T) == 2) {
-    const float2 f = Elem<T>::unpack2(
-        max2(max2(x.w.x, x.w.y, T{}), max2(x.w.z, x.w.w, T{}), T{}));
-    return fmaxf(f.x, f.y);
-  } else {
-    return fmaxf(fmaxf(__uint_as_float(x.w.x), __uint_as_float(x.w.y)),
-                 fmaxf(__uint_as_float(x.w.z), __uint_as_float(x.w.w)));
-  }
-}
 template <typename T, int R>
 __device__ __forceinline__ float largest(const Access<T> (&x)[R]) {
   if constexpr (sizeof(T) == 2) {
@@ -648,11 +636,8 @@ __device__ __forceinline__ void collect(const SelectArgs& a, int row0, int part0
     const int part = in >> a.log_groups, group = in - (part << a.log_groups);
     // What the group has of the row.
     const int row = row0 + b, begin = row * a.chunks;
-    int first = begin, last = begin + a.chunks;
-    if (!a.whole_rows) {
-      first = max(first, a.first_chunk(part0 + part - row));
-      last = min(last, a.first_chunk(part0 + part - row + 1));
-    }
+    const int first = max(begin, a.first_chunk(part0 + part - row));
+    const int last = min(begin + a.chunks, a.first_chunk(part0 + part - row + 1));
     const int chunk = first + pair - h * a.longest;
     if (chunk >= last) continue;
     const Row<T, R> whole = {static_cast<const T*>(a.c.logits) + (size_t)row * a.c.ld, a.vocab};
@@ -908,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   for (int i = 0; i < kStages - 1; ++i) copy(i);
   int row = a.by_chunks.divide(g0), chunk = g0 - row * a.chunks, stage = 0;
   // A part's number that the last CTA's end and this one's beginning leave out.
-  if (chunk == 0 && blockIdx.x > 0 && !a.whole_rows && threadIdx.x == 0)
+  if (chunk == 0 && blockIdx.x > 0 && threadIdx.x == 0)
     a.beam_of[a.part_of(blockIdx.x, row) - 1] = kNone;
   Exponentials sums;
   float best = -INFINITY;
@@ -959,21 +944,16 @@ cudaError_t select_as(const hg_beam& h, SelectArgs& a, cudaStream_t stream) {
   const long long all = rows * a.chunks;
   if (all > 0x3fffffffLL) return cudaErrorInvalidValue;  // more logits than any device holds
   const long long full = (long long)kCtasPerSm * h.sms;
-  long long ctas = full < all ? full : all;
+  const long long ctas = full < all ? full : all;
   a.all = (int)all;
   a.each = (int)(all / ctas);
   a.more = (int)(all % ctas);
-  // An item's parts at most: a CTA's share may end in its rows, and begin, anywhere.
-  long long parts = div_up((long long)h.beams * a.chunks, a.each) + 1 + h.beams;
+  // An item's parts at most: a CTA's share may end in its rows, and begin, anywhere. A share is
+  // more than half of all / full chunks, so that 152 SMs make at most 1281 parts of an item.
+  const long long parts = div_up((long long)h.beams * a.chunks, a.each) + 1 + h.beams;
+  if (parts > 1024 * kManyValues / kLeastGroups) return cudaErrorInvalidValue;
   const int values =
       h.picks > kFewPicks || parts * kLeastGroups > 1024 * kFewValues ? kManyValues : kFewValues;
-  a.whole_rows = parts > 1024 * values / kLeastGroups;
-  if (a.whole_rows) {
-    a.each = (int)div_up(rows, full) * a.chunks;
-    a.more = 0;
-    ctas = div_up(all, a.each);
-    parts = h.beams;
-  }
   // As many groups of threads as there is room for values of their maxima; less where that
   // lets small CTAs join, which more items than SMs need (256 items: 28 and 24 us).
   const bool small = values == kFewValues && a.c.items > h.sms && parts * kLeastGroups <= 256 * values;
