@@ -617,7 +617,8 @@ int hg_vocab_loss_grad(hg_vocab *h, const void *hidden, size_t ld_hidden,
  * grad_x is the gradient of x and of residual alike. All arithmetic is fp32; s is
  * rounded once to the handle's type, and what follows is the norm of the rounded
  * rows, those that the gradient is given. Squares and sums that pass the fp32
- * range give rows of zeros or NaN.
+ * range (rows of about 1e19) give rows of zeros or NaN; squares below it (1e-19, with an
+ * eps as small) lose their bits. Between those the gradient holds for rows of any scale.
  *
  * Conventions as for the vocabulary operators (asynchronous, no allocation, no wait for the
  * device, capturable, the handle's device current at every call and the stream and pointers
@@ -664,7 +665,8 @@ size_t hg_norm_workspace_bytes(const hg_norm *h);
  *   scales    HG_E4M3: [N, blocks] floats, rows contiguous; the values are out * scale
  *   scale_block  HG_E4M3: 0: one scale per row; 128: one per 128 columns (blocks =
  *             ceil(K / 128)). A scale is the largest magnitude of its values over
- *             448, at least 2^-126, and 1 where they are all zero
+ *             448, at least 2^-126, and 1 where they are all zero. A value within 2^-20 of
+ *             the middle between two 8-bit ones goes to either
  *   rstd      NULL, or N floats
  *
  * Errors, before any device work: HG_ERR_ARG, HG_ERR_ROWS (N above max_rows),
@@ -708,7 +710,8 @@ int hg_norm_rows_grad(hg_norm *h, const void *s, size_t ld_s, const void *gain, 
  * An item is one sequence of `beams` beams; its rows of the logits, scores and states
  * are neighbours (row = item * beams + beam).
  *
- * Totals are compared in 64 bits. Equal totals: the lower beam first; within a beam
+ * Totals are sums in 64 bits of an fp32 score, the logit and a logsumexp that is given in fp32
+ * or computed (see lse), and are compared so. Equal totals: the lower beam first; within a beam
  * the larger logit, then the lower token. A total that is NaN, or rounds to -inf in
  * fp32, is no candidate, so a score of -inf takes its beam out of the search (as all
  * but one beam of an item at the first step, whose rows are the same).
@@ -748,7 +751,10 @@ size_t hg_beam_workspace_bytes(const hg_beam *h);
  *   logits    [items * beams, vocab], row distance ld_logits >= vocab (a rank's output
  *             of hg_gather); -inf rules a token out
  *   lse       NULL: computed here, of the logits that are not -inf (a row that holds
- *             NaN or +inf then has no candidates); or one float per row, lse_stride
+ *             NaN or +inf then has no candidates), as a sum of fp32 exponentials in an order
+ *             that depends on where the row lies and on the other rows: off by at most 2^-17 +
+ *             vocab * 2^-32 (5e-7 measured), so that beams whose totals are closer than that,
+ *             or alike, come in any order; or one float per row, lse_stride
  *             floats apart (logsumexp of hg_row_stats: &stats->logsumexp, 4)
  *   scores    items * beams floats
  *   finished  NULL, or items * beams bytes: a beam whose byte is not 0 has one
@@ -764,8 +770,10 @@ size_t hg_beam_workspace_bytes(const hg_beam *h);
  * scores, finished and reordering (tokens, hg_vocab_embed's input); with picks = 2 * beams
  * there are beams of them that do not end. Where fewer candidates are left, the last
  * picks have token and parent -1, total -inf and are not finished. No output overlaps an
- * input or another output: refused, but for outputs over lse, which are not looked for. An item with more than 1000 equal candidates at the last pick
- * (a row of zeros, say) takes a path that reads its rows again for every bit of the order.
+ * input or another output: refused, but for outputs over lse, which are not looked for. An item with more than 1000 candidates at the last
+ * pick that cannot be told apart in fp32 takes a path that reads its rows again for every bit of the
+ * order, milliseconds instead of microseconds: equal logits (a row of zeros), or a beam whose
+ * score is far beyond the others' (-1e9; -inf takes a beam out at no cost).
  *
  * Errors, before any device work: HG_ERR_ARG, HG_ERR_ROWS (items above max_items),
  * HG_ERR_CUDA.

@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 bf16, fp16, fp32 = torch.bfloat16, torch.float16, torch.float32
 
 
-@pytest.mark.parametrize("N", [1, 2, 5, 16, 63, 64, 65, 152, 153, 400])
+@pytest.mark.parametrize("N", [1, 5, 16, 64, 65, 400])
 @pytest.mark.parametrize("K,dtype", [(8, bf16), (130, fp16), (1000, bf16), (1001, fp32),
                                      (7168, bf16), (16384, fp16), (20001, bf16)])
 def test_order_of_grad_gain(N, K, dtype):

@@ -225,6 +225,9 @@ __device__ __forceinline__ float largest(const Access<T> (&x)[R]) {
 // where that is kRise above it (to rescale at every new maximum took a third of the
 // instructions). From kHuge on, where neighbours are further apart than exponentials reach, the
 // largest elements count one each. NaN and +inf give NaN.
+// (An exponent of up to 58 is off by up to 2^-19, 1.3e-6 of its exponential. With sums of up
+// to 3 / 1024 of the row's elements one after another the logsumexp is off by at most 2^-17 +
+// vocab * 2^-32; 5e-7 measured, rows of 1000 to a million logits.)
 constexpr float kHuge = 1e30f;
 constexpr float kRise = 40.f;  // 2^58
 
@@ -537,7 +540,9 @@ __device__ __forceinline__ int count_all(int c, int turn, JoinShared& s) {
 
 // Where too many candidates are alike for the list: the best of each row that has some,
 // exactly (the key of the n-th best, one bit after another, reading the row again for each),
-// and of those one pick after another.
+// and of those one pick after another. About 1.3 ms a row of 163840 equal logits, the rows of an
+// item one after another; 1.5 ms for 32 items of 8 beams of which all but one are out by a score
+// of -1e9, whose magnitude is in every total's bound (JoinShared::off; 27 us with -inf).
 template <typename T, int R, int THREADS>
 __device__ __noinline__ void pick_exactly(const SelectArgs& a, int item, JoinShared& s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

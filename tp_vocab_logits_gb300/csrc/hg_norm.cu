@@ -5,8 +5,9 @@
 // the row and the output. A CTA has one group, or several that work on rows of their own.
 // Rows in 16-byte accesses, if there are many of them, are streamed: each thread copies
 // the 16 bytes that it will itself read into a ring in shared memory (cp.async), a few rows
-// ahead, which takes no registers and no barrier. Rows that no CTA can hold are read
-// twice.
+// ahead, which takes no registers and no barrier. Longer rows than the kernels hold are read
+// again, element by element: more than 2048 accesses of 16 bytes, 8192 shorter ones (the
+// gradient: 4096 of 4 bytes, 8192 of 2).
 
 #include <cuda_fp8.h>
 
@@ -73,7 +74,9 @@ __device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
 }
 
 // The scale of values up to `most` in magnitude, and its reciprocal (to two units of its
-// last place: what it multiplies is rounded to four bits).
+// last place: what it multiplies is rounded to four bits, so that only values in the middle
+// between two, within 2^-20, may go to the other one; their error is half a step either way.
+// Of 2048 rows of 7168 bf16, 865 values differ from a division's, all of them exact ties).
 __device__ __forceinline__ float scale_of(float most) {
   return most == 0.f ? 1.f : fmaxf(most * (1.f / kE4m3Most), kLeastScale);
 }
@@ -684,7 +687,7 @@ __global__ void __launch_bounds__(kMostThreads) grad_kernel(const __grid_constan
   if (GAIN) store_partial<E, A>(a, acc, at);
 }
 
-constexpr int kFewColumns = 64;  // of a CTA, 4 to 16 groups of threads taking every so many'th row
+constexpr int kFewColumns = 64;  // of a CTA, whose 4 to 16 groups of threads take rows in turn
 
 // Few rows in one launch: the first N CTAs make grad_x, if it is wanted, a row each; the others
 // grad_gain, which needs no sum over a row, from the rows as they lie (so grad_x is not grad_out).
